@@ -263,6 +263,78 @@ ZM_API int zm_ttt_chunked(const zm_ttt_desc* desc, int order, int64_t n_chunks,
                    float* w1, float* w2, float* w3, void* o,
                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* Layer norm of token rows, as in front of zm_ttt_layer's projections:
+ *   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps), y = (x - mu) r gamma + beta
+ * over the width of each row, in fp32 (the variance from the distances to the
+ * mean), rounded once to the io type. */
+typedef struct zm_norm_desc {
+  int32_t width;      /* a multiple of 8, at most 8192 (wider: ZM_ERR_UNSUPPORTED) */
+  int32_t io_dtype;   /* zm_dtype of x, y, dy, dx */
+  float eps;          /* > 0 */
+  int32_t reserved;   /* must be 0 */
+} zm_norm_desc;
+
+/* x, y: [n][width] rows of strides ld_x, ld_y (>= width, multiples of 8), bases
+ * 16-byte aligned.  gamma, beta: fp32 [width], either may be NULL (1, 0).
+ * stats: NULL, or fp32 [2][n] that receives mu, then r, for the backward.  y
+ * may be x (same stride); otherwise they must not overlap.  n = 0 is valid. */
+ZM_API int zm_layer_norm(const zm_norm_desc* desc, int64_t n, const void* x, int64_t ld_x,
+                  const float* gamma, const float* beta, void* y, int64_t ld_y, float* stats,
+                  void* stream);
+
+/* Bytes of workspace of zm_layer_norm_backward (never less for more rows). */
+ZM_API int zm_layer_norm_backward_workspace_size(const zm_norm_desc* desc, int64_t n, size_t* bytes);
+
+/* The gradient: with xh = (x - mu) r from stats and a = dy gamma,
+ *   dx = r (a - mean(a) - xh mean(a xh)), dgamma = sum_rows dy xh, dbeta = sum_rows dy.
+ * dgamma, dbeta: fp32 [width], overwritten (n = 0: zeros); either may be NULL.
+ * dx may be dy or x (same stride).  Sums in fixed order: bitwise reproducible.
+ * The workspace is 256-byte aligned; with both dgamma and dbeta NULL it is not
+ * read and may be NULL. */
+ZM_API int zm_layer_norm_backward(const zm_norm_desc* desc, int64_t n, const void* dy, int64_t ld_dy,
+                  const void* x, int64_t ld_x, const float* gamma, const float* stats,
+                  void* dx, int64_t ld_dx, float* dgamma, float* dbeta,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rotary positions with up to four axes (time, height, width) on the q and k of
+ * [n, heads, d_head] tokens.  Pair p < P = sum of sections belongs to the axis
+ * whose section holds it (axis 0's pairs first) and turns by the angle
+ * pos[t][axis] freqs[p]:  (x, y) -> (x cos - y sin, x sin + y cos).
+ * The two dims of pair p:
+ *   ZM_ROTARY_HALVES       p and p + P
+ *   ZM_ROTARY_PAIRS        2 p and 2 p + 1
+ *   ZM_ROTARY_AXIS_HALVES  the halves of the axis's own block: with f the pairs
+ *                          of earlier axes and s its own, p + f and p + f + s
+ * Dims from 2 P on pass unrotated.  The angle is formed in 64 bits and reduced
+ * before it is rounded, so far positions lose no precision; position 0 (as of
+ * a frame's special tokens) leaves finite values unchanged.  A position that is
+ * infinite or NaN gives NaN in the pairs of its axis. */
+typedef enum zm_rotary_layout {
+  ZM_ROTARY_HALVES = 0,
+  ZM_ROTARY_PAIRS = 1,
+  ZM_ROTARY_AXIS_HALVES = 2
+} zm_rotary_layout;
+
+typedef struct zm_rotary_desc {
+  int32_t heads_q;      /* 1..64 */
+  int32_t heads_k;      /* 0..64; 0: no k, its pointers are not read */
+  int32_t d_head;       /* a multiple of 8, at most 256 (wider: ZM_ERR_UNSUPPORTED) */
+  int32_t io_dtype;     /* zm_dtype of q, k */
+  int32_t layout;       /* zm_rotary_layout */
+  int32_t inverse;      /* 0, or 1: by minus the angle (the rotation's gradient) */
+  int32_t pos_f32;      /* positions: 0 int32, 1 fp32 */
+  int32_t axes;         /* 1..4 */
+  int32_t sections[4];  /* pairs of each axis, >= 0; 1 <= P <= d_head / 2; unused axes 0 */
+  int64_t ld_q, ld_k, ld_q_out, ld_k_out;  /* token strides, multiples of 8, >= heads * d_head */
+} zm_rotary_desc;
+
+/* pos: [n][axes] contiguous; freqs: fp32 [P] (radians per unit of position).
+ * q_out may be q and k_out may be k (same stride: in place, what is unrotated
+ * is then not touched); otherwise no two of the arrays may overlap.  q and k
+ * may be slices of one projection's rows.  n = 0 is valid. */
+ZM_API int zm_rotary(const zm_rotary_desc* desc, int64_t n, const void* pos, const float* freqs,
+              const void* q, const void* k, void* q_out, void* k_out, void* stream);
+
 /* Static description of a status code. */
 ZM_API const char* zm_status_string(int status);
 

@@ -21,12 +21,15 @@ APPLY_THEN_UPDATE, UPDATE_THEN_APPLY = 0, 1
 STREAM_EMIT_BF16, STREAM_REUSE_BF16 = 0x100, 0x200
 SCRATCH_BYTES = 64 << 20  # ZM_TTT_SCRATCH_BYTES
 STEP_GRADIENT, STEP_NEWTON_SCHULZ = 0, 1
+ROTARY_HALVES, ROTARY_PAIRS, ROTARY_AXIS_HALVES = 0, 1, 2
 
 EXPORTED = (
     "zm_ttt_workspace_size", "zm_ttt_update", "zm_ttt_update_loss", "zm_ttt_apply",
     "zm_ttt_update_apply", "zm_ttt_update_apply_scratch",
     "zm_ttt_stream_step", "zm_ttt_chunked", "zm_ttt_layer_workspace_size", "zm_ttt_layer",
     "zm_status_string", "zm_ttt_last_error", "zm_ttt_version", "zm_ttt_set_profile_events",
+    "zm_layer_norm", "zm_layer_norm_backward_workspace_size", "zm_layer_norm_backward",
+    "zm_rotary",
 )
 
 
@@ -57,6 +60,33 @@ class LayerWeights(ctypes.Structure):
         ("eta_scale", ctypes.c_float),
         ("rms_eps", ctypes.c_float),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("width", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [
+        ("heads_q", ctypes.c_int32),
+        ("heads_k", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("inverse", ctypes.c_int32),
+        ("pos_f32", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * 4),
+        ("ld_q", ctypes.c_int64),
+        ("ld_k", ctypes.c_int64),
+        ("ld_q_out", ctypes.c_int64),
+        ("ld_k_out", ctypes.c_int64),
     ]
 
 
@@ -100,6 +130,15 @@ def load_library(path: str | None = None):
     lib.zm_ttt_last_error.restype = ctypes.c_char_p
     lib.zm_ttt_version.argtypes = []
     lib.zm_ttt_set_profile_events.argtypes = [ctypes.POINTER(_P), ctypes.c_int]
+    _ND, _RD = ctypes.POINTER(NormDesc), ctypes.POINTER(RotaryDesc)
+    lib.zm_layer_norm.argtypes = [_ND, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P]
+    lib.zm_layer_norm_backward_workspace_size.argtypes = [_ND, _I64, ctypes.POINTER(_SZ)]
+    lib.zm_layer_norm_backward.argtypes = [_ND, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P,
+                                           _P, _SZ, _P]
+    lib.zm_rotary.argtypes = [_RD, _I64, _P, _P, _P, _P, _P, _P, _P]
+    for name in ("zm_layer_norm", "zm_layer_norm_backward_workspace_size",
+                 "zm_layer_norm_backward", "zm_rotary"):
+        getattr(lib, name).restype = ctypes.c_int
     for name in ("zm_ttt_workspace_size", "zm_ttt_update", "zm_ttt_update_loss", "zm_ttt_apply",
                  "zm_ttt_update_apply", "zm_ttt_update_apply_scratch",
                  "zm_ttt_stream_step", "zm_ttt_chunked", "zm_ttt_layer_workspace_size",
@@ -471,6 +510,177 @@ def layer(x, w_in, w_gate, gamma, w1, w2, w3, eta_scale=0.01, rms_eps=1e-6, reno
         _stream(x.device))
     _check(st, "zm_ttt_layer")
     return outs, o
+
+
+# ---------------------------------------------------------------------------
+# operators around a token sequence
+# ---------------------------------------------------------------------------
+def _same_gpu(first, *others):
+    """All on one GPU: checked after shapes and types, as for the other calls."""
+    if not first.is_cuda:
+        raise ZmError("tensors must be on the GPU")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ZmError(f"tensors must all be on {first.device}, got one on {t.device}")
+
+
+class _on_device:
+    """Makes a tensor's device the current one for a call, if it is not."""
+
+    def __init__(self, device):
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(
+            device)
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard:
+            self.guard.__exit__(*exc)
+
+
+def _row_stride(x, width):
+    """Stride of a 2-D tensor's rows (any for one row or none)."""
+    if x.shape[0] > 0 and x.stride(1) != 1:
+        raise ZmError("rows need unit column stride")
+    return x.stride(0) if x.shape[0] > 1 else width
+
+
+def _vector(t, width, name):
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (width,)
+                          or not t.is_contiguous()):
+        raise ZmError(f"{name} must be a contiguous fp32 tensor of {width} elements")
+
+
+def _norm_rows(name, t, like=None):
+    if t.dtype not in _IO or t.dim() != 2:
+        raise ZmError(f"{name} must be a 2-D bf16 or fp32 tensor")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+        raise ZmError(f"{name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} "
+                      f"{tuple(t.shape)}")
+
+
+def _norm_stats(stats, n):
+    if stats.dtype != torch.float32 or tuple(stats.shape) != (2, n) or not stats.is_contiguous():
+        raise ZmError(f"stats must be contiguous fp32 [2, {n}]")
+
+
+def layer_norm(x, gamma=None, beta=None, eps=1e-6, out=None, stats=None):
+    """y = (x - mean) / sqrt(var + eps) * gamma + beta over the rows of x
+    [n, width] (bf16 or fp32); gamma, beta fp32 [width] or None.  stats: an fp32
+    [2, n] tensor to receive each row's mean and 1 / sqrt(var + eps), for
+    layer_norm_backward.  out=x normalises in place."""
+    _norm_rows("x", x)
+    n, width = x.shape
+    y = torch.empty((n, width), dtype=x.dtype, device=x.device) if out is None else out
+    if out is not None:
+        _norm_rows("out", out, x)
+    _vector(gamma, width, "gamma")
+    _vector(beta, width, "beta")
+    if stats is not None:
+        _norm_stats(stats, n)
+    ld_x, ld_y = _row_stride(x, width), _row_stride(y, width)
+    _same_gpu(x, gamma, beta, y, stats)
+    with _on_device(x.device):
+        st = load_library().zm_layer_norm(
+            ctypes.byref(NormDesc(width, _IO[x.dtype], float(eps), 0)), n, _ptr(x), ld_x,
+            _ptr(gamma), _ptr(beta), _ptr(y), ld_y, _ptr(stats), _stream(x.device))
+    _check(st, "zm_layer_norm")
+    return y
+
+
+def layer_norm_backward_workspace_size(n: int, width: int, dtype=torch.bfloat16) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().zm_layer_norm_backward_workspace_size(
+        ctypes.byref(NormDesc(int(width), _IO[dtype], 1e-6, 0)), int(n), ctypes.byref(out)),
+        "zm_layer_norm_backward_workspace_size")
+    return int(out.value)
+
+
+def layer_norm_backward(dy, x, stats, gamma=None, out=None, dgamma=None, dbeta=None,
+                        workspace=None):
+    """(dx, dgamma, dbeta) of layer_norm from its x, the stats it wrote, and dy.
+    out=dy or out=x writes dx in place; dgamma, dbeta: fp32 [width] to write to."""
+    _norm_rows("x", x)
+    _norm_rows("dy", dy, x)
+    n, width = x.shape
+    dx = torch.empty((n, width), dtype=x.dtype, device=x.device) if out is None else out
+    if out is not None:
+        _norm_rows("out", out, x)
+    _vector(gamma, width, "gamma")
+    _norm_stats(stats, n)
+    both = torch.empty((2, width), dtype=torch.float32, device=x.device)
+    dgamma = both[0] if dgamma is None else dgamma
+    dbeta = both[1] if dbeta is None else dbeta
+    _vector(dgamma, width, "dgamma")
+    _vector(dbeta, width, "dbeta")
+    lds = [_row_stride(t, width) for t in (dy, x, dx)]
+    _same_gpu(x, dy, stats, gamma, dx, dgamma, dbeta, workspace)
+    need = layer_norm_backward_workspace_size(n, width, x.dtype)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device) if workspace is None \
+        else workspace
+    with _on_device(x.device):
+        st = load_library().zm_layer_norm_backward(
+            ctypes.byref(NormDesc(width, _IO[x.dtype], 1e-6, 0)), n, _ptr(dy), lds[0], _ptr(x),
+            lds[1], _ptr(gamma), _ptr(stats), _ptr(dx), lds[2], _ptr(dgamma), _ptr(dbeta),
+            _ptr(ws), _ws_bytes(ws), _stream(x.device))
+    _check(st, "zm_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def _heads_rows(name, t, n, heads, d, dtype):
+    """Checks a [n, heads, d] token tensor and returns its token stride."""
+    if t.dtype != dtype or dtype not in _IO:
+        raise ZmError(f"{name}: dtype {t.dtype}, the call needs bf16 or fp32 throughout")
+    if tuple(t.shape) != (n, heads, d):
+        raise ZmError(f"{name}: shape {tuple(t.shape)} != [{n}, {heads}, {d}]")
+    if n > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ZmError(f"{name}: token tensors need unit stride on d and d on heads")
+    return t.stride(0) if n > 1 else heads * d
+
+
+def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_out=None,
+           k_out=None):
+    """Rotates q [n, Hq, d] and k [n, Hk, d] (or None) by their positions: pos
+    [n, axes] int32 or fp32, freqs fp32 [P], sections the pairs of each axis
+    (sum P <= d / 2; dims from 2 P on pass unrotated), layout how the dims pair
+    (ROTARY_HALVES, ROTARY_PAIRS, ROTARY_AXIS_HALVES).  inverse=True turns
+    back, which is the gradient.  q_out=q, k_out=k rotate in place.  Returns
+    (q_out, k_out)."""
+    if q.dim() != 3:
+        raise ZmError("q must be [n, heads, d]")
+    n, hq, d = q.shape
+    hk = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ZmError("k must be [n, heads, d]")
+        hk = k.shape[1]
+    sec = [int(c) for c in sections]
+    if not 1 <= len(sec) <= 4:
+        raise ZmError("sections: one to four axes")
+    if pos.dtype not in (torch.int32, torch.float32) or tuple(pos.shape) != (n, len(sec)) \
+            or not pos.is_contiguous():
+        raise ZmError(f"pos must be contiguous int32 or fp32 [{n}, {len(sec)}]")
+    _vector(freqs, sum(sec), "freqs")
+    qo = torch.empty((n, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    ko = k_out
+    if k is not None and ko is None:
+        ko = torch.empty((n, hk, d), dtype=k.dtype, device=k.device)
+    ldq, ldqo = _heads_rows("q", q, n, hq, d, q.dtype), _heads_rows("q_out", qo, n, hq, d, q.dtype)
+    ldk = ldko = 0
+    if k is not None:
+        ldk = _heads_rows("k", k, n, hk, d, q.dtype)
+        ldko = _heads_rows("k_out", ko, n, hk, d, q.dtype)
+    _same_gpu(q, k, pos, freqs, qo, ko)
+    desc = RotaryDesc(hq, hk, d, _IO[q.dtype], int(layout), 1 if inverse else 0,
+                      1 if pos.dtype == torch.float32 else 0, len(sec),
+                      (ctypes.c_int32 * 4)(*sec), ldq, ldk, ldqo, ldko)
+    with _on_device(q.device):
+        st = load_library().zm_rotary(ctypes.byref(desc), n, _ptr(pos), _ptr(freqs), _ptr(q),
+                                      _ptr(k), _ptr(qo), _ptr(ko), _stream(q.device))
+    _check(st, "zm_rotary")
+    return qo, ko
 
 
 def set_profile_events(events):

@@ -12,6 +12,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "api_util.h"
 #include "gemm_lt.h"
 #include "layer_kernels.h"
 #include "wide_path.h"
@@ -65,10 +66,6 @@ struct Scoped {
   Scoped(int s, hipStream_t stream) : stage(s), st(stream) { prof_mark(2 * s, st); }
   ~Scoped() { prof_mark(2 * stage + 1, st); }
 };
-
-inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int check_desc(const zm_ttt_desc* d) {
   if (!d) return ZM_ERR_INVALID_ARG;
@@ -195,21 +192,6 @@ int check_ws(const zm_ttt_desc* d, int64_t n_kv, int64_t n_q, void* ws, size_t w
   if (ws_bytes < L.total) return ZM_ERR_WORKSPACE;
   return ZM_OK;
 }
-
-#define ZM_TRY(expr)            \
-  do {                          \
-    const int _s = (expr);      \
-    if (_s != ZM_OK) return _s; \
-  } while (0)
-
-#define ZM_HIP(expr)                                                                \
-  do {                                                                              \
-    const hipError_t _e = (expr);                                                   \
-    if (_e != hipSuccess) {                                                         \
-      zm::set_last_error("%s: %s (%d)", #expr, hipGetErrorString(_e), (int)_e);     \
-      return ZM_ERR_HIP;                                                            \
-    }                                                                               \
-  } while (0)
 
 int finish_update(const zm_ttt_desc* d, int64_t n, const float* w1, const float* w2,
                   const float* w3, float* o1, float* o2, float* o3, float* part, int splits,
