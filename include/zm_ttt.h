@@ -335,6 +335,53 @@ typedef struct zm_rotary_desc {
 ZM_API int zm_rotary(const zm_rotary_desc* desc, int64_t n, const void* pos, const float* freqs,
               const void* q, const void* k, void* q_out, void* k_out, void* stream);
 
+/* Gated delta rule: the linear fast weight f_S(x) = S x, S [d_head][d_head] fp32
+ * per value head, trained token by token on |S k - v|^2 / 2 with a decay
+ * (the notes' linear case of the fast weight, with one gradient step of rate
+ * beta_t to each token instead of one to a chunk, and a gate):
+ *   S_t = a_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,  a_t = exp(g_t),
+ *   o_t = scale S_t q_t.
+ * Tokens: q, k [n, heads_k, d_head], v, o [n, heads, d_head] (value head h reads
+ * key head h / (heads / heads_k)); g (log decay, any value; -inf resets the
+ * state) and beta fp32 [n, heads] contiguous.  Keys are used as they are: the
+ * recurrence contracts for beta |k|^2 in [0, 2].
+ * Sequences lie one after the other: sequence b has the tokens offsets[b] ..
+ * offsets[b + 1] - 1 (device int32 [n_seq + 1], nondecreasing in 0..n; values
+ * outside are clamped to that), which may be none.  offsets may be NULL for a
+ * single sequence of all n tokens.  Rows of the outputs outside every sequence
+ * are left as they were.
+ * States: fp32 [n_seq, heads, d_head (rows: v), d_head (k)], 16-byte aligned. */
+typedef struct zm_delta_desc {
+  int32_t heads;      /* value heads, 1..64, a multiple of heads_k */
+  int32_t heads_k;    /* query/key heads */
+  int32_t d_head;     /* 64 or 128 */
+  int32_t io_dtype;   /* zm_dtype of q, k, v, o and their gradients */
+  int32_t n_seq;      /* sequences, >= 0 */
+  float scale;        /* of the outputs */
+  int64_t ld_q, ld_k, ld_v, ld_o;  /* token strides: >= heads * d_head (q, k: heads_k *
+                                      d_head), multiples of 8, at most 2^24 */
+} zm_delta_desc;
+
+/* Bytes of workspace of zm_delta_rule for n tokens in desc->n_seq sequences. */
+ZM_API int zm_delta_rule_workspace_size(const zm_delta_desc* desc, int64_t n, size_t* bytes);
+
+/* The rule over whole sequences, 64 tokens at a time (fp32 states, products of
+ * 24 bits where they reach a state).  state_in: the states before the first tokens or NULL
+ * (zeros); state_out: receives the states after the last ones, or NULL; it may
+ * be state_in.  o must not overlap the inputs.  Bitwise reproducible; sequences
+ * longer than some hundred tokens are cut into segments that run side by side
+ * where few (sequence, head) pairs would leave the GPU idle, by a rule on n,
+ * n_seq and heads alone. */
+ZM_API int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* offsets,
+                  const void* q, const void* k, const void* v, const float* g, const float* beta,
+                  const float* state_in, float* state_out, void* o,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of each of n_seq sequences (row b: sequence b), states updated in
+ * place.  No workspace. */
+ZM_API int zm_delta_rule_step(const zm_delta_desc* desc, const void* q, const void* k, const void* v,
+                       const float* g, const float* beta, float* state, void* o, void* stream);
+
 /* Static description of a status code. */
 ZM_API const char* zm_status_string(int status);
 

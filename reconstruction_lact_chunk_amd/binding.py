@@ -29,7 +29,7 @@ EXPORTED = (
     "zm_ttt_stream_step", "zm_ttt_chunked", "zm_ttt_layer_workspace_size", "zm_ttt_layer",
     "zm_status_string", "zm_ttt_last_error", "zm_ttt_version", "zm_ttt_set_profile_events",
     "zm_layer_norm", "zm_layer_norm_backward_workspace_size", "zm_layer_norm_backward",
-    "zm_rotary",
+    "zm_rotary", "zm_delta_rule_workspace_size", "zm_delta_rule", "zm_delta_rule_step",
 )
 
 
@@ -90,6 +90,21 @@ class RotaryDesc(ctypes.Structure):
     ]
 
 
+class DeltaDesc(ctypes.Structure):
+    _fields_ = [
+        ("heads", ctypes.c_int32),
+        ("heads_k", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("n_seq", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("ld_q", ctypes.c_int64),
+        ("ld_k", ctypes.c_int64),
+        ("ld_v", ctypes.c_int64),
+        ("ld_o", ctypes.c_int64),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -136,8 +151,13 @@ def load_library(path: str | None = None):
     lib.zm_layer_norm_backward.argtypes = [_ND, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P,
                                            _P, _SZ, _P]
     lib.zm_rotary.argtypes = [_RD, _I64, _P, _P, _P, _P, _P, _P, _P]
+    _DD = ctypes.POINTER(DeltaDesc)
+    lib.zm_delta_rule_workspace_size.argtypes = [_DD, _I64, ctypes.POINTER(_SZ)]
+    lib.zm_delta_rule.argtypes = [_DD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+    lib.zm_delta_rule_step.argtypes = [_DD, _P, _P, _P, _P, _P, _P, _P, _P]
     for name in ("zm_layer_norm", "zm_layer_norm_backward_workspace_size",
-                 "zm_layer_norm_backward", "zm_rotary"):
+                 "zm_layer_norm_backward", "zm_rotary", "zm_delta_rule_workspace_size",
+                 "zm_delta_rule", "zm_delta_rule_step"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("zm_ttt_workspace_size", "zm_ttt_update", "zm_ttt_update_loss", "zm_ttt_apply",
                  "zm_ttt_update_apply", "zm_ttt_update_apply_scratch",
@@ -681,6 +701,100 @@ def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_ou
                                       _ptr(k), _ptr(qo), _ptr(ko), _stream(q.device))
     _check(st, "zm_rotary")
     return qo, ko
+
+
+def _delta_inputs(q, k, v, g, beta, scale):
+    """Shape and type checks of a delta-rule call; returns its descriptor (one
+    sequence, ld_o of a contiguous output) and n."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ZmError("q, k must be [n, heads_k, d] and v [n, heads, d]")
+    n, hk, d = q.shape
+    h = v.shape[1]
+    if hk < 1 or h < 1 or h % hk:
+        raise ZmError(f"{h} value heads are no multiple of {hk} key heads")
+    lds = [_heads_rows("q", q, n, hk, d, q.dtype), _heads_rows("k", k, n, hk, d, q.dtype),
+           _heads_rows("v", v, n, h, d, q.dtype)]
+    for name, t in (("g", g), ("beta", beta)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
+            raise ZmError(f"{name} must be contiguous fp32 [{n}, {h}]")
+    return DeltaDesc(h, hk, d, _IO[q.dtype], 1, float(d ** -0.5 if scale is None else scale), *lds,
+                     h * d), n
+
+
+def _delta_offsets(offsets):
+    """Number of sequences."""
+    if offsets is None:
+        return 1
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 \
+            or not offsets.is_contiguous():
+        raise ZmError("offsets must be a contiguous int32 tensor of n_seq + 1 elements")
+    return offsets.numel() - 1
+
+
+def _delta_state(name, t, desc):
+    want = (desc.n_seq, desc.heads, desc.d_head, desc.d_head)
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != want
+                          or not t.is_contiguous()):
+        raise ZmError(f"{name} must be contiguous fp32 {list(want)}")
+
+
+def delta_rule_workspace_size(desc: DeltaDesc, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().zm_delta_rule_workspace_size(ctypes.byref(desc), int(n),
+                                                       ctypes.byref(out)),
+           "zm_delta_rule_workspace_size")
+    return int(out.value)
+
+
+def delta_rule(q, k, v, g, beta, state=None, offsets=None, scale=None, out=None, state_out=None,
+               workspace=None):
+    """The gated delta rule over packed sequences: S <- exp(g) S (I - beta k k^T) +
+    beta v k^T token by token, o = scale S q.  q, k [n, Hk, d], v [n, H, d] (bf16
+    or fp32, d 64 or 128), g, beta fp32 [n, H]; offsets int32 [n_seq + 1] on the
+    GPU (None: one sequence); state fp32 [n_seq, H, d, d] or None (zeros); scale
+    None: d ** -0.5.  Returns (o, the states after the last tokens); pass
+    state_out=state to carry the state in place, as from frame to frame.  Rows of
+    o outside every sequence are not written."""
+    desc, n = _delta_inputs(q, k, v, g, beta, scale)
+    desc.n_seq = _delta_offsets(offsets)
+    _delta_state("state", state, desc)
+    _delta_state("state_out", state_out, desc)
+    shape = (desc.n_seq, desc.heads, desc.d_head, desc.d_head)
+    o = torch.empty((n, desc.heads, desc.d_head), dtype=q.dtype, device=q.device) if out is None \
+        else out
+    desc.ld_o = _heads_rows("out", o, n, desc.heads, desc.d_head, q.dtype)
+    end = torch.empty(shape, dtype=torch.float32, device=q.device) if state_out is None \
+        else state_out
+    _same_gpu(q, k, v, g, beta, state, offsets, o, end, workspace)
+    need = delta_rule_workspace_size(desc, n)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None \
+        else workspace
+    with _on_device(q.device):
+        st = load_library().zm_delta_rule(
+            ctypes.byref(desc), n, _ptr(offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+            _ptr(state), _ptr(end), _ptr(o), _ptr(ws), _ws_bytes(ws), _stream(q.device))
+    _check(st, "zm_delta_rule")
+    return o, end
+
+
+def delta_rule_step(q, k, v, g, beta, state, scale=None, out=None):
+    """One token of each of n sequences (row b: sequence b) through the gated
+    delta rule; state fp32 [n, H, d, d] is updated in place.  Returns o."""
+    desc, n = _delta_inputs(q, k, v, g, beta, scale)
+    desc.n_seq = n
+    if state is None:
+        raise ZmError("delta_rule_step needs a state")
+    _delta_state("state", state, desc)
+    o = torch.empty((n, desc.heads, desc.d_head), dtype=q.dtype, device=q.device) if out is None \
+        else out
+    desc.ld_o = _heads_rows("out", o, n, desc.heads, desc.d_head, q.dtype)
+    _same_gpu(q, k, v, g, beta, state, o)
+    with _on_device(q.device):
+        st = load_library().zm_delta_rule_step(
+            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
+            _ptr(o), _stream(q.device))
+    _check(st, "zm_delta_rule_step")
+    return o
 
 
 def set_profile_events(events):

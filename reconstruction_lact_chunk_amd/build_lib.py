@@ -22,7 +22,8 @@ ARCH = "gfx950"
 
 SOURCES = ["weights.hip", "update_bf16.hip", "apply_bf16.hip", "frame_bf16.hip", "fp32_path.hip",
            "newton_schulz.hip", "wide_kernels.hip", "wide_gemm.hip", "wide_path.cpp", "gemm_lt.cpp",
-           "layer_kernels.hip", "wide_ns.hip", "layer_norm.hip", "rotary.hip", "seq_api.cpp", "api.cpp"]
+           "layer_kernels.hip", "wide_ns.hip", "layer_norm.hip", "rotary.hip", "seq_api.cpp",
+           "delta_prep.hip", "delta_scan.hip", "delta_step.hip", "delta_api.cpp", "api.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
@@ -69,7 +70,7 @@ def build(verbose: bool = False, defines=(), out: str = LIB, host_sanitize: bool
     build_dir = BUILD if out == LIB else out + ".objs"
     os.makedirs(build_dir, exist_ok=True)
     extra = HOST_SANITIZE if host_sanitize else ()
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose, defines, build_dir, extra), SOURCES))
     tmp = out + ".tmp"
     rocm_lib = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(hipcc()))), "lib")

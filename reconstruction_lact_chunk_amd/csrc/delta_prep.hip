@@ -1,0 +1,301 @@
+// What a chunk of the gated delta rule needs besides the state, for all chunks
+// and heads at once: T = (I + A)^-1 and P as matrix-core operand tiles, and the
+// row factors gam, dec, beta (delta_rule.h).
+#include "delta_rule.h"
+
+namespace zm {
+
+namespace {
+
+constexpr int kPitch = 68;     // floats of a row of the 64 x 64 matrices in LDS
+constexpr int kBlk = 336;      // floats of a 16 x 16 diagonal block (rows of 20; blocks 16 banks apart)
+
+// ---- tables -------------------------------------------------------------------
+// One workgroup: the clamped, nondecreasing offsets, the prefix sums of chunks
+// and segments, then every chunk's and segment's entry by a search in them.
+__global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
+  __shared__ int sh[2][1024];
+  const int t = threadIdx.x, per = (s.n_seq + 1023) / 1024;
+  const int b0 = t * per, b1 = b0 + per < s.n_seq ? b0 + per : s.n_seq;
+  // running maximum of the clamped ends
+  int top = t == 0 ? clampi(s.offsets[0], 0, s.n) : 0;
+  for (int b = b0; b < b1; ++b) {
+    const int e = clampi(s.offsets[b + 1], 0, s.n);
+    if (e > top) top = e;
+  }
+  int cur = 0;
+  sh[0][t] = top;
+  __syncthreads();
+  for (int w = 1; w < 1024; w *= 2, cur ^= 1) {
+    int v = sh[cur][t];
+    if (t >= w && sh[cur][t - w] > v) v = sh[cur][t - w];
+    sh[cur ^ 1][t] = v;
+    __syncthreads();
+  }
+  int run = t == 0 ? clampi(s.offsets[0], 0, s.n) : sh[cur][t - 1];
+  __syncthreads();
+  const int run0 = run;
+  int nc = 0, ns = 0;
+  for (int b = b0; b < b1; ++b) {
+    int e = clampi(s.offsets[b + 1], 0, s.n);
+    if (e < run) e = run;
+    const int c = (int)(((int64_t)(e - run) + kChunk - 1) / kChunk);
+    nc += c;
+    ns += c > 0 ? (c + s.seg_chunks - 1) / s.seg_chunks : 1;
+    run = e;
+  }
+  int2 sum{nc, ns};
+  for (int which = 0; which < 2; ++which) {
+    cur = 0;
+    sh[0][t] = which ? ns : nc;
+    __syncthreads();
+    for (int w = 1; w < 1024; w *= 2, cur ^= 1) {
+      sh[cur ^ 1][t] = sh[cur][t] + (t >= w ? sh[cur][t - w] : 0);
+      __syncthreads();
+    }
+    if (which) sum.y = sh[cur][t] - ns; else sum.x = sh[cur][t] - nc;
+    __syncthreads();
+  }
+  // sequence by sequence: its first chunk, its begin and its segments
+  run = run0;
+  int c0 = sum.x, s0 = sum.y;
+  for (int b = b0; b < b1; ++b) {
+    int e = clampi(s.offsets[b + 1], 0, s.n);
+    if (e < run) e = run;
+    const int c = (int)(((int64_t)(e - run) + kChunk - 1) / kChunk);
+    s.first_chunk[b] = c0;
+    s.begin[b] = run;
+    const int k = c > 0 ? (c + s.seg_chunks - 1) / s.seg_chunks : 1;
+    for (int i = 0; i < k; ++i) {
+      const int f = i * s.seg_chunks;
+      s.segs[s0 + i] = int4{c0 + f, c - f < s.seg_chunks ? c - f : s.seg_chunks, b,
+                            (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0)};
+    }
+    c0 += c;
+    s0 += k;
+    run = e;
+    if (b == s.n_seq - 1) {
+      s.first_chunk[s.n_seq] = c0;
+      s.begin[s.n_seq] = e;
+      sh[0][0] = s0;
+    }
+  }
+  __syncthreads();
+  __threadfence_block();
+  const int all = s.first_chunk[s.n_seq], segs = sh[0][0];
+  for (int i = segs + t; i < s.n_segs; i += 1024) s.segs[i] = int4{0, -1, 0, 0};
+  for (int ci = t; ci < s.n_chunks; ci += 1024) {
+    if (ci >= all) {
+      s.chunks[ci] = int4{0, 0, 0, 0};
+      continue;
+    }
+    int lo = 0, hi = s.n_seq;  // the last sequence whose first chunk is at most ci
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.first_chunk[mid] <= ci) lo = mid; else hi = mid;
+    }
+    const int at = s.begin[lo] + kChunk * (ci - s.first_chunk[lo]);
+    const int left = s.begin[lo + 1] - at;
+    s.chunks[ci] = int4{at, left < kChunk ? left : kChunk, lo, 0};
+  }
+}
+
+// ---- T and P --------------------------------------------------------------------
+// Parts of tile `tile`'s row (lane c) at dims 32 s + 8 g; rows past the chunk's
+// tokens are zero.
+template <bool F32>
+__device__ __forceinline__ Parts<Tok<F32>::NT> row_parts(const typename Tok<F32>::T* base, int64_t ld,
+                                                         int tok, int count, int col) {
+  if (tok < count) return load8(base + (int64_t)tok * ld + col);
+  return zero_parts<Tok<F32>::NT>();
+}
+
+// Operand tiles of a 64 x 64 matrix in LDS: item i of 6 x 64 is tile i / 64, lane
+// i % 64.  TR: of the transpose.
+template <int NP, bool TR>
+__device__ __forceinline__ void write_frags(const float* m, uint16_t* out) {
+  for (int i = threadIdx.x; i < kTriFrags * 64; i += 256) {
+    const int f = i >> 6, lane = i & 63, g = lane >> 4, c = lane & 15;
+    int it, ts;
+    if (!TR) {
+      it = f < 2 ? f : 2 + (f - 2) / 2;
+      ts = f < 2 ? 0 : (f - 2) & 1;
+    } else {
+      it = f < 4 ? f / 2 : f - 2;
+      ts = f < 4 ? f & 1 : 1;
+    }
+    const int row = token_row(it, c);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = 32 * ts + dtau(g, e);
+      x[e] = TR ? m[col * kPitch + row] : m[row * kPitch + col];
+    }
+    const Parts<NP> p = split8<NP>(x);
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+      *(bf16x8*)(out + (int64_t)(k * kTriFrags + f) * kFragElems + lane * 8) = p.p[k];
+  }
+}
+
+// One workgroup per (chunk, head), wave w its 16-row block w of the products
+// K K^T and Q K^T.  T by blocks of 16: the diagonal blocks' inverses by forward
+// substitution (a column a lane; unlike a product of powers of A it stays exact
+// where keys repeat), then block column w in wave w by
+//   T_iw = -D_i sum_{w <= j < i} A_ij T_jw,
+// on fp32 matrix instructions whose results are the next right operands.
+template <int D, bool F32, bool BWD>
+__global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
+  using T = typename Tok<F32>::T;
+  constexpr int NT = Tok<F32>::NT, KS = D / 32, LIM = NT == 1 ? 0 : 2;
+  __shared__ float ma[kChunk * kPitch], mp[kChunk * kPitch];
+  __shared__ float diag[4 * kBlk];
+  __shared__ double cs[kChunk];
+  __shared__ float be[kChunk];
+  const int h = blockIdx.x % a.heads, ci = blockIdx.x / a.heads;
+  const int4 ch = delta_chunk(a.sq, ci);
+  const int count = ch.y;
+  if (count == 0) return;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int hk = h / (a.heads / a.heads_k);
+  const T* const kp = (const T*)a.k.p + (int64_t)ch.x * a.k.ld + hk * D;
+  const T* const qp = (const T*)a.q.p + (int64_t)ch.x * a.q.ld + hk * D;
+  const int64_t slot = (int64_t)ci * a.heads + h;
+
+  if (w == 0) {
+    float gl = 0.f, b = 0.f;
+    if (lane < count) {
+      gl = a.g[((int64_t)ch.x + lane) * a.heads + h];
+      b = a.beta[((int64_t)ch.x + lane) * a.heads + h];
+      if (gl < kMinLogDecay) gl = kMinLogDecay;
+    }
+    // sums in 64 bits: a strong decay among weak ones must not blur their differences
+    double s = gl;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+      const double o = __shfl_up(s, m, 64);
+      if (lane >= m) s += o;
+    }
+    cs[lane] = s;
+    be[lane] = b;
+    const double last = __shfl(s, 63, 64);
+    float* const r = a.rows + slot * 3 * kChunk;
+    r[lane] = expf((float)s);
+    r[kChunk + lane] = expf((float)(last - s));
+    r[2 * kChunk + lane] = b;
+  }
+  f32x4 kk[4], qk[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int col = 32 * s + 8 * g;
+    const auto ka = row_parts<F32>(kp, a.k.ld, 16 * w + c, count, col);
+    const auto qa = row_parts<F32>(qp, a.q.ld, 16 * w + c, count, col);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > w) continue;
+      const auto kb = row_parts<F32>(kp, a.k.ld, 16 * j + c, count, col);
+      mma<LIM>(kk[j], ka, kb);
+      mma<LIM>(qk[j], qa, kb);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int col = 16 * j + c;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * g + r;
+      const float gd = row >= col ? expf((float)(cs[row] - cs[col])) : 0.f;
+      const float av = row > col ? be[row] * gd * kk[j][r] : 0.f;
+      ma[row * kPitch + col] = av;
+      mp[row * kPitch + col] = row >= col ? a.scale * gd * qk[j][r] : 0.f;
+      if (j == w) diag[w * kBlk + (4 * g + r) * 20 + c] = av;
+    }
+  }
+  __syncthreads();
+  if (w == 0) {
+    // column c of diagonal block g's inverse
+    float x[16];
+    const float* const blk = diag + g * kBlk;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == c ? 1.f : 0.f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) s = fmaf(-blk[i * 20 + j], x[j], s);
+      x[i] = s;
+    }
+    // every lane has read the block: its 16 lanes run as one
+#pragma unroll
+    for (int i = 0; i < 16; ++i) diag[g * kBlk + i * 20 + c] = x[i];
+  }
+  if constexpr (BWD)
+    write_frags<3, true>(mp, a.pt_frags + slot * 3 * kTriFrags * kFragElems);
+  else
+    write_frags<NT == 1 ? 2 : 3, false>(
+        mp, a.p_frags + slot * (NT == 1 ? 2 : 3) * kTriFrags * kFragElems);
+  __syncthreads();
+  f32x4 tc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    tc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (i == w)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) tc[i][r] = diag[i * kBlk + (4 * g + r) * 20 + c];
+  }
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    if (i <= w) continue;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < i; ++j) {
+      if (j < w) continue;
+      const f32x4 av = *(const f32x4*)(ma + (16 * i + c) * kPitch + 16 * j + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        y = __builtin_amdgcn_mfma_f32_16x16x4f32(av[r], tc[j][r], y, 0, 0, 0);
+    }
+    const f32x4 dv = *(const f32x4*)(diag + i * kBlk + c * 20 + 4 * g);
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      t = __builtin_amdgcn_mfma_f32_16x16x4f32(-dv[r], y[r], t, 0, 0, 0);
+    tc[i] = t;
+  }
+  // P's tiles are out: its place takes T
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) mp[(16 * i + 4 * g + r) * kPitch + 16 * w + c] = tc[i][r];
+  __syncthreads();
+  write_frags<3, false>(mp, a.t_frags + slot * 3 * kTriFrags * kFragElems);
+  if constexpr (BWD) write_frags<3, true>(mp, a.tt_frags + slot * 3 * kTriFrags * kFragElems);
+}
+
+template <bool BWD>
+hipError_t prep_any(const DeltaArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.sq.n_chunks * a.heads)), blk(256);
+  if (a.d == 128) {
+    if (a.f32) hipLaunchKernelGGL((k_delta_prep<128, true, BWD>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((k_delta_prep<128, false, BWD>), grid, blk, 0, st, a);
+  } else {
+    if (a.f32) hipLaunchKernelGGL((k_delta_prep<64, true, BWD>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((k_delta_prep<64, false, BWD>), grid, blk, 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_table(const DeltaSeqs& s, hipStream_t st) {
+  hipLaunchKernelGGL(k_delta_table, dim3(1), dim3(1024), 0, st, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t st) {
+  if (a.sq.n_chunks == 0) return hipSuccess;
+  return backward ? prep_any<true>(a, st) : prep_any<false>(a, st);
+}
+
+}  // namespace zm

@@ -1,0 +1,233 @@
+// Gated delta rule: shared device code, argument blocks and launchers.
+//
+// Per sequence and value head, S in R^{d x d} (fp32), a_t = exp(g_t):
+//   S_t = a_t S_{t-1} (I - b_t k_t k_t^T) + b_t v_t k_t^T,  o_t = scale S_t q_t.
+// Tokens are taken kChunk at a time.  With c_i the sum of g over the chunk's
+// tokens up to i, gam_i = exp(c_i), dec_i = exp(c_C - c_i), G_ij = exp(c_i - c_j)
+// and M = S^T at the chunk's start:
+//   A = strictly_lower(b_i G_ij k_i.k_j),  T = (I + A)^-1,  P = scale lower(G_ij q_i.k_j)
+//   R = V - gam o (K M),  U = T (b o R),  O = scale gam o (Q M) + P U,
+//   M' = gam_C M + K^T (dec o U).
+// T and P do not depend on M: delta_prep.hip forms them for all chunks at once,
+// delta_scan.hip goes through the chunks of a sequence in order.
+//
+// Matrix products run on v_mfma_f32_16x16x32_bf16.  An operand held in fp32
+// (M, U, T, P, fp32 tokens) enters as a sum of bf16 parts: three parts carry 24
+// bits, and of the products of parts those below 2^-24 are left out, so the
+// state is as exact as fp32 products would leave it at 3 (bf16 tokens) or 6
+// matrix instructions instead of the 16 that fp32 ones cost.  What is rounded to
+// bf16 in the end (O with bf16 io) takes two parts, 2^-17 each.
+//
+// The matrix cores return rows 4 g + r (r < 4) of column c in lane 16 g + c, and
+// take rows in slots 8 g + e (e < 8) of a 32-row step in the same lane.  With
+// rows mapped to slots by tau (tokens) or 8 g + e (head dims) a product's result
+// is the next product's right operand without leaving its registers.
+#pragma once
+
+#include "zm_internal.h"
+
+namespace zm {
+
+constexpr int kChunk = 64;             // tokens of a chunk
+constexpr int kTriFrags = 6;           // 16 x 32 operand tiles of a 64 x 64 triangle
+constexpr int kFragElems = 64 * 8;     // bf16 elements of one such tile
+constexpr float kMinLogDecay = -128.f; // exp of less is 0 in fp32
+
+// Where the sequences lie.  Without a table (one sequence) a chunk follows from
+// its index; offsets are clamped to 0 <= ... <= n and made nondecreasing, so that
+// no content of them reaches outside the tokens.
+struct DeltaSeqs {
+  const int* offsets;    // [n_seq + 1] or null: one sequence of all n tokens
+  int4* chunks;          // {first token, tokens, sequence, 0}, null without a table
+  int4* segs;            // {first chunk, chunks (-1: unused), sequence, 1 first | 2 last}
+  int* first_chunk;      // [n_seq + 1] scratch of the table's kernel
+  int* begin;            // [n_seq + 1] scratch: clamped offsets
+  int n, n_seq;
+  int n_chunks, n_segs;  // upper bounds over every content of offsets
+  int seg_chunks;        // chunks of a segment
+};
+
+struct DeltaTokens {
+  const void* p;
+  int64_t ld;
+};
+
+struct DeltaArgs {
+  DeltaSeqs sq;
+  DeltaTokens q, k, v;
+  const float* g;       // [n][heads]
+  const float* beta;    // [n][heads]
+  int heads, heads_k, d;
+  float scale;
+  bool f32;
+  // per (chunk, head): operand tiles and row factors
+  uint16_t* t_frags;    // [3][kTriFrags][kFragElems] parts of T
+  uint16_t* p_frags;    // parts of P (2 for bf16 io, 3 for fp32)
+  uint16_t* tt_frags;   // parts of T^T, P^T (backward)
+  uint16_t* pt_frags;
+  float* rows;          // [3][kChunk] gam, dec, beta
+};
+
+struct DeltaScanArgs {
+  const float* state_in;    // [n_seq][heads][d][d] or null (zeros)
+  float* state_out;         // the same, or null
+  const float* seg_start;   // [n_segs][heads][d][d]: states at the segments' starts, or null
+  float* trans;             // [n_segs][heads][2][d][d]: N as [d_k][d_k], B as a state (pass of transitions)
+  void* o;
+  int64_t ld_o;
+  float* m_out;             // [n_chunks][heads][d][d]: M at each chunk's start (backward), as [d_k][d_v]
+  float* u_out;             // [n][heads][d] (backward)
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+// Chunk ci: {first token, tokens (0: unused), sequence, -}.
+__device__ __forceinline__ int4 delta_chunk(const DeltaSeqs& s, int ci) {
+  if (s.chunks) return s.chunks[ci];
+  int a = 0, e = s.n;
+  if (s.offsets) {
+    a = clampi(s.offsets[0], 0, s.n);
+    e = clampi(s.offsets[1], a, s.n);
+  }
+  const int64_t st = (int64_t)a + (int64_t)kChunk * ci;
+  const int left = st < e ? (int)(e - st) : 0;
+  return int4{left > 0 ? (int)st : 0, left < kChunk ? left : kChunk, 0, 0};
+}
+
+__device__ __forceinline__ int4 delta_seg(const DeltaSeqs& s, int si) {
+  if (s.segs) return s.segs[si];
+  int a = 0, e = s.n;
+  if (s.offsets) {
+    a = clampi(s.offsets[0], 0, s.n);
+    e = clampi(s.offsets[1], a, s.n);
+  }
+  const int chunks = (int)(((int64_t)(e - a) + kChunk - 1) / kChunk);
+  const int segs = chunks > 0 ? (chunks + s.seg_chunks - 1) / s.seg_chunks : 1;
+  if (si >= segs) return int4{0, -1, 0, 0};
+  const int f = si * s.seg_chunks;
+  const int c = chunks - f < s.seg_chunks ? chunks - f : s.seg_chunks;
+  return int4{f, c, 0, (si == 0 ? 1 : 0) | (si == segs - 1 ? 2 : 0)};
+}
+
+// Token of slot e of lane group g in a 32-token step (and, for row m = 4 g' + i of
+// 16-row tile h of the step, token_row below): the order whose row and
+// transposing LDS reads the update kernel already uses.
+__device__ __forceinline__ constexpr int dtau(int g, int e) {
+  return 16 * (g >> 1) + 4 * (g & 1) + 8 * (e >> 2) + (e & 3);
+}
+// Token of row m of tile `it` (16 rows; two tiles to a step).
+__device__ __forceinline__ constexpr int token_row(int it, int m) {
+  return 32 * (it >> 1) + dtau(m >> 2, 4 * (it & 1) + (m & 3));
+}
+// Head dim of row m of state tile mt.
+__device__ __forceinline__ constexpr int dim_row(int mt, int m) {
+  return 32 * (mt >> 1) + 8 * (m >> 2) + 4 * (mt & 1) + (m & 3);
+}
+// Operand tile (it, ts) of a lower (T, P) or upper (transposed) triangle.
+__device__ __forceinline__ constexpr int low_frag(int it, int ts) { return it < 2 ? it : 2 * it - 2 + ts; }
+__device__ __forceinline__ constexpr int up_frag(int it, int ts) { return it < 2 ? 2 * it + ts : it + 2; }
+
+template <int NP>
+struct Parts {
+  bf16x8 p[NP];
+};
+
+// x as a sum of NP bf16 parts, each the rounding of what the ones before leave.
+template <int NP>
+__device__ __forceinline__ Parts<NP> split8(const float* x) {
+  Parts<NP> out;
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack_bf16x2(r[2 * i], r[2 * i + 1]);
+      if (p + 1 < NP) {
+        r[2 * i] -= bf16lo(w[i]);
+        r[2 * i + 1] -= bf16hi(w[i]);
+      }
+    }
+    out.p[p] = as_bf16x8(w);
+  }
+  return out;
+}
+template <int NP>
+__device__ __forceinline__ Parts<NP> split_tiles(const f32x4& a, const f32x4& b) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return split8<NP>(x);
+}
+
+// acc += a b over the part products of order at most LIM, the smallest first.
+template <int LIM, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& acc, const Parts<NA>& a, const Parts<NB>& b) {
+#pragma unroll
+  for (int s = LIM; s >= 0; --s)
+#pragma unroll
+    for (int p = 0; p <= s; ++p)
+      if (p < NA && s - p < NB) acc = mfma_bf16(a.p[p], b.p[s - p], acc);
+}
+
+typedef __attribute__((ext_vector_type(4))) __bf16 dbf16x4;
+typedef __attribute__((address_space(3))) dbf16x4 lds_dbf16x4;
+
+// Transposing LDS read: within 16 lanes, lane i gets element i % 4 of the 8-byte
+// words at the addresses of lanes 4 e + i / 4, e = 0..3.
+__device__ __forceinline__ dbf16x4 delta_read_tr(const uint16_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+      (lds_dbf16x4*)((__attribute__((address_space(3))) void*)(p)));
+}
+
+// Token element type and the parts it takes.
+template <bool F32>
+struct Tok {
+  using T = uint16_t;
+  static constexpr int NT = 1;
+};
+template <>
+struct Tok<true> {
+  using T = float;
+  static constexpr int NT = 3;
+};
+
+// Parts of 8 consecutive elements in memory.
+__device__ __forceinline__ Parts<1> load8(const uint16_t* p) {
+  return Parts<1>{{as_bf16x8(*(const u32x4*)p)}};
+}
+__device__ __forceinline__ Parts<3> load8(const float* p) {
+  const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+  return split_tiles<3>(a, b);
+}
+template <int NP>
+__device__ __forceinline__ Parts<NP> zero_parts() {
+  Parts<NP> z;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) z.p[p] = as_bf16x8(u32x4{0u, 0u, 0u, 0u});
+  return z;
+}
+
+// ---- launchers --------------------------------------------------------------------
+// The tables of chunks and segments (n_seq > 1).
+hipError_t launch_delta_table(const DeltaSeqs& s, hipStream_t st);
+// T and P (backward: T, T^T, P^T) and the row factors of every chunk and head.
+hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t st);
+hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st);
+// The states at the segments' starts from their transitions (s.trans).
+hipError_t launch_delta_join(const DeltaArgs& a, const DeltaScanArgs& s, float* starts,
+                             hipStream_t st);
+struct DeltaStepArgs {
+  DeltaTokens q, k, v;
+  const float* g;
+  const float* beta;
+  float* state;
+  void* o;
+  int64_t ld_o;
+  int n_seq, heads, heads_k, d;
+  float scale;
+  bool f32;
+};
+hipError_t launch_delta_step(const DeltaStepArgs& a, hipStream_t st);
+
+}  // namespace zm

@@ -1,0 +1,377 @@
+// The chunks of a segment in order: one workgroup per (segment, head), each wave
+// 32 columns of M (d_v) and all its rows (delta_rule.h).  A wave's columns need
+// nothing from the other waves but the operands they share: K and Q, read from
+// LDS in rows and, for K^T, through the transposing read; T and P, read as
+// operand tiles.  M, R and U stay in registers: each is the result of one product
+// and the right operand of the next.  Columns 2 c and 2 c + 1 of a wave belong to
+// lane c's two column tiles, so tokens go in and out as pairs.
+#include "delta_rule.h"
+
+namespace zm {
+
+namespace {
+
+template <int D, bool F32>
+struct ScanCfg {
+  static constexpr int NT = Tok<F32>::NT;
+  static constexpr int PITCH = D + 16;
+  static constexpr int TILE = kChunk * PITCH;   // one part of K or Q
+  static constexpr int WAVES = D / 32;
+  static constexpr int THREADS = 64 * WAVES;
+};
+
+// K (or Q) of the chunk into its LDS parts; rows past `count` are zero.
+template <int D, bool F32>
+__device__ __forceinline__ void stage(uint16_t* lds, const typename Tok<F32>::T* src, int64_t ld,
+                                      int count) {
+  using C = ScanCfg<D, F32>;
+  constexpr int CPR = D / 8;
+  for (int i = threadIdx.x; i < kChunk * CPR; i += C::THREADS) {
+    const int row = i / CPR, col = 8 * (i % CPR);
+    Parts<C::NT> p = zero_parts<C::NT>();
+    if (row < count) p = load8(src + (int64_t)row * ld + col);
+#pragma unroll
+    for (int k = 0; k < C::NT; ++k) *(bf16x8*)(lds + k * C::TILE + row * C::PITCH + col) = p.p[k];
+  }
+}
+
+template <int D, bool F32>
+__device__ __forceinline__ Parts<Tok<F32>::NT> lds_row(const uint16_t* lds, int row, int col) {
+  using C = ScanCfg<D, F32>;
+  Parts<C::NT> p;
+#pragma unroll
+  for (int k = 0; k < C::NT; ++k) p.p[k] = *(const bf16x8*)(lds + k * C::TILE + row * C::PITCH + col);
+  return p;
+}
+
+// Rows dim_row(mt, .) of the transpose, slots = tokens of step ts.
+template <int D, bool F32>
+__device__ __forceinline__ Parts<Tok<F32>::NT> lds_col(const uint16_t* lds, int mt, int ts, int g,
+                                                       int c) {
+  using C = ScanCfg<D, F32>;
+  Parts<C::NT> p;
+  const int row = 32 * ts + dtau(g, c >> 2), col = 32 * (mt >> 1) + 8 * (c & 3) + 4 * (mt & 1);
+#pragma unroll
+  for (int k = 0; k < C::NT; ++k) {
+    const uint16_t* at = lds + k * C::TILE + row * C::PITCH + col;
+    p.p[k] = __builtin_shufflevector(delta_read_tr(at), delta_read_tr(at + 8 * C::PITCH), 0, 1, 2, 3,
+                                     4, 5, 6, 7);
+  }
+  return p;
+}
+
+template <int NP>
+__device__ __forceinline__ Parts<NP> frag(const uint16_t* f, int i, int lane) {
+  Parts<NP> p;
+#pragma unroll
+  for (int k = 0; k < NP; ++k)
+    p.p[k] = *(const bf16x8*)(f + (k * kTriFrags + i) * kFragElems + lane * 8);
+  return p;
+}
+
+// A pair of neighbouring columns of one token.
+__device__ __forceinline__ f32x2 load_pair(const uint16_t* p) {
+  const unsigned w = *(const unsigned*)p;
+  return f32x2{bf16lo(w), bf16hi(w)};
+}
+__device__ __forceinline__ f32x2 load_pair(const float* p) { return *(const f32x2*)p; }
+__device__ __forceinline__ void store_pair(uint16_t* p, float a, float b) {
+  *(unsigned*)p = pack_bf16x2(a, b);
+}
+__device__ __forceinline__ void store_pair(float* p, float a, float b) { *(f32x2*)p = f32x2{a, b}; }
+
+// MODE 0: outputs and the last state.  MODE 1 (backward): M at every chunk's start
+// and U instead of the outputs.  MODE 2: the segment's transition: blocks of the
+// first `heads` columns run the values from a zero state, the others no values
+// from the identity, so M_end = N M_start + B.
+enum { kOutputs = 0, kKeep = 1, kTransition = 2 };
+
+template <int D, bool F32, int MODE>
+__global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanArgs sa) {
+  using C = ScanCfg<D, F32>;
+  using T = typename Tok<F32>::T;
+  constexpr int NT = C::NT, KS = D / 32, MT = D / 16, NO = NT == 1 ? 2 : 3;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[(MODE == kOutputs ? 2 : 1) * NT * C::TILE];
+  uint16_t* const kl = lds;
+  uint16_t* const ql = lds + NT * C::TILE;  // kOutputs only
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  int blk = blockIdx.x;
+  const int h = blk % a.heads;
+  blk /= a.heads;
+  const bool unit = MODE == kTransition && (blk & 1);
+  const int si = MODE == kTransition ? blk >> 1 : blk;
+  const int4 sg = delta_seg(a.sq, si);
+  if (sg.y < 0) return;
+  if (MODE == kTransition && (sg.w & 2)) return;  // nothing follows the last segment
+  const int hk = h / (a.heads / a.heads_k);
+  const int dv = 32 * (threadIdx.x >> 6) + 2 * c;  // of the lane's pair of columns
+
+  f32x4 m[MT][2];
+  const int64_t dd = (int64_t)D * D;
+  const float* init = nullptr;
+  if (MODE != kTransition) {
+    if (sa.seg_start) init = sa.seg_start + ((int64_t)si * a.heads + h) * dd;
+    else if (sa.state_in) init = sa.state_in + ((int64_t)sg.z * a.heads + h) * dd;
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+      const int dk = dim_row(mt, 4 * g);
+      if (init) {
+        m[mt][ct] = *(const f32x4*)(init + (int64_t)(dv + ct) * D + dk);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[mt][ct][r] = unit && dk + r == dv + ct ? 1.f : 0.f;
+      }
+    }
+
+  for (int j = 0; j < sg.y; ++j) {
+    const int ci = sg.x + j;
+    const int4 ch = delta_chunk(a.sq, ci);
+    const int count = ch.y;
+    const int64_t slot = (int64_t)ci * a.heads + h;
+    const uint16_t* const tf = a.t_frags + slot * 3 * kTriFrags * kFragElems;
+    const uint16_t* const pf = a.p_frags + slot * NO * kTriFrags * kFragElems;
+    const float* const rows = a.rows + slot * 3 * kChunk;
+    __syncthreads();
+    stage<D, F32>(kl, (const T*)a.k.p + (int64_t)ch.x * a.k.ld + hk * D, a.k.ld, count);
+    if (MODE == kOutputs)
+      stage<D, F32>(ql, (const T*)a.q.p + (int64_t)ch.x * a.q.ld + hk * D, a.q.ld, count);
+    __syncthreads();
+
+    if (MODE == kKeep) {
+      float* const mo = sa.m_out + slot * dd;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *(f32x2*)(mo + (int64_t)dim_row(mt, 4 * g + r) * D + dv) =
+              f32x2{m[mt][0][r], m[mt][1][r]};
+    }
+
+    // K M and Q M
+    f32x4 km[4][2], qm[4][2];
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) km[it][ct] = qm[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      Parts<3> b[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(m[2 * s][ct], m[2 * s + 1][ct]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int row = token_row(it, c), col = 32 * s + 8 * g;
+        const auto ka = lds_row<D, F32>(kl, row, col);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) mma<2>(km[it][ct], ka, b[ct]);
+        if (MODE == kOutputs) {
+          const auto qa = lds_row<D, F32>(ql, row, col);
+#pragma unroll
+          for (int ct = 0; ct < 2; ++ct) mma<NO - 1>(qm[it][ct], qa, b[ct]);
+        }
+      }
+    }
+    // X = beta o (V - gam o K M), in km
+    const T* const vp = (const T*)a.v.p + (int64_t)ch.x * a.v.ld + h * D + dv;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int t0 = token_row(it, 4 * g);
+      const f32x4 gm = *(const f32x4*)(rows + t0), be = *(const f32x4*)(rows + 2 * kChunk + t0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f32x2 v = {0.f, 0.f};
+        if (!unit && t0 + r < count) v = load_pair(vp + (int64_t)(t0 + r) * a.v.ld);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) km[it][ct][r] = be[r] * fmaf(-gm[r], km[it][ct][r], v[ct]);
+      }
+    }
+    // U = T X
+    f32x4 u[4][2];
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) u[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      Parts<3> b[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(km[2 * ts][ct], km[2 * ts + 1][ct]);
+#pragma unroll
+      for (int it = 2 * ts; it < 4; ++it) {
+        const auto ta = frag<3>(tf, low_frag(it, ts), lane);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) mma<2>(u[it][ct], ta, b[ct]);
+      }
+    }
+    if (MODE == kKeep) {
+      float* const uo = sa.u_out + ((int64_t)ch.x * a.heads + h) * D + dv;
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = token_row(it, 4 * g + r);
+          if (t < count)
+            *(f32x2*)(uo + (int64_t)t * a.heads * D) = f32x2{u[it][0][r], u[it][1][r]};
+        }
+    }
+    if (MODE == kOutputs) {
+      // O = scale gam o (Q M) + P U
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const f32x4 gm = *(const f32x4*)(rows + token_row(it, 4 * g));
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) qm[it][ct][r] *= a.scale * gm[r];
+      }
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+        Parts<NO> b[2];
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<NO>(u[2 * ts][ct], u[2 * ts + 1][ct]);
+#pragma unroll
+        for (int it = 2 * ts; it < 4; ++it) {
+          const auto pa = frag<NO>(pf, low_frag(it, ts), lane);
+#pragma unroll
+          for (int ct = 0; ct < 2; ++ct) mma<NO - 1>(qm[it][ct], pa, b[ct]);
+        }
+      }
+      T* const op = (T*)sa.o + (int64_t)ch.x * sa.ld_o + h * D + dv;
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = token_row(it, 4 * g + r);
+          if (t < count) store_pair(op + (int64_t)t * sa.ld_o, qm[it][0][r], qm[it][1][r]);
+        }
+    }
+    // M <- gam_C M + K^T (dec o U)
+    const float gl = rows[kChunk - 1];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[mt][ct][r] *= gl;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const f32x4 de = *(const f32x4*)(rows + kChunk + token_row(it, 4 * g));
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[it][ct][r] *= de[r];
+    }
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      Parts<3> b[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(u[2 * ts][ct], u[2 * ts + 1][ct]);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const auto ka = lds_col<D, F32>(kl, mt, ts, g, c);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) mma<2>(m[mt][ct], ka, b[ct]);
+      }
+    }
+  }
+
+  float* out = nullptr;
+  if (MODE == kTransition) out = sa.trans + (((int64_t)si * a.heads + h) * 2 + 1) * dd;
+  if (unit) {  // N by rows, as the join reads it
+    out -= dd;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *(f32x2*)(out + (int64_t)dim_row(mt, 4 * g + r) * D + dv) = f32x2{m[mt][0][r], m[mt][1][r]};
+    return;
+  }
+  if (MODE == kTransition) {
+  } else if ((sg.w & 2) && sa.state_out) out = sa.state_out + ((int64_t)sg.z * a.heads + h) * dd;
+  if (out) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+        *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+  }
+}
+
+// The states at the segments' starts: M <- N M + B along each sequence.  A wave has
+// 16 columns of one (sequence, head); the blocks of a sequence's first segment
+// go through all of its segments.
+template <int D>
+__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a, DeltaScanArgs sa, float* starts) {
+  constexpr int KS = D / 32, MT = D / 16, SL = D / 16;
+  const int lane = threadIdx.x, g = lane >> 4, c = lane & 15;
+  const int dv = 16 * (blockIdx.x % SL) + c;
+  const int h = (blockIdx.x / SL) % a.heads;
+  int si = blockIdx.x / SL / a.heads;
+  int4 sg = delta_seg(a.sq, si);
+  if (sg.y < 0 || !(sg.w & 1)) return;
+  const int64_t dd = (int64_t)D * D;
+  f32x4 m[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (sa.state_in)
+      m[mt] = *(const f32x4*)(sa.state_in + ((int64_t)sg.z * a.heads + h) * dd + (int64_t)dv * D +
+                              dim_row(mt, 4 * g));
+  }
+  while (true) {
+    float* const to = starts + ((int64_t)si * a.heads + h) * dd + (int64_t)dv * D;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) *(f32x4*)(to + dim_row(mt, 4 * g)) = m[mt];
+    if (sg.w & 2) return;
+    const float* const nn = sa.trans + ((int64_t)si * a.heads + h) * 2 * dd;
+    Parts<3> b[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) b[s] = split_tiles<3>(m[2 * s], m[2 * s + 1]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      m[mt] = *(const f32x4*)(nn + dd + (int64_t)dv * D + dim_row(mt, 4 * g));
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        mma<2>(m[mt], load8(nn + (int64_t)dim_row(mt, c) * D + 32 * s + 8 * g), b[s]);
+    ++si;
+    if (si >= a.sq.n_segs) return;
+    sg = delta_seg(a.sq, si);
+  }
+}
+
+template <int D, bool F32>
+hipError_t scan_any(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st) {
+  using C = ScanCfg<D, F32>;
+  const int64_t blocks = (int64_t)a.sq.n_segs * a.heads;
+  if (s.trans)
+    hipLaunchKernelGGL((k_delta_scan<D, F32, kTransition>), dim3((unsigned)(2 * blocks)),
+                       dim3(C::THREADS), 0, st, a, s);
+  else if (s.m_out)
+    hipLaunchKernelGGL((k_delta_scan<D, F32, kKeep>), dim3((unsigned)blocks), dim3(C::THREADS), 0, st, a, s);
+  else
+    hipLaunchKernelGGL((k_delta_scan<D, F32, kOutputs>), dim3((unsigned)blocks), dim3(C::THREADS),
+                       0, st, a, s);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st) {
+  if (a.d == 128) return a.f32 ? scan_any<128, true>(a, s, st) : scan_any<128, false>(a, s, st);
+  return a.f32 ? scan_any<64, true>(a, s, st) : scan_any<64, false>(a, s, st);
+}
+
+hipError_t launch_delta_join(const DeltaArgs& a, const DeltaScanArgs& s, float* starts,
+                             hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads * (a.d / 16))), blk(64);
+  if (a.d == 128) hipLaunchKernelGGL((k_delta_join<128>), grid, blk, 0, st, a, s, starts);
+  else hipLaunchKernelGGL((k_delta_join<64>), grid, blk, 0, st, a, s, starts);
+  return hipGetLastError();
+}
+
+}  // namespace zm
