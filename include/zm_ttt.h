@@ -382,6 +382,26 @@ ZM_API int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* of
 ZM_API int zm_delta_rule_step(const zm_delta_desc* desc, const void* q, const void* k, const void* v,
                        const float* g, const float* beta, float* state, void* o, void* stream);
 
+/* Bytes of workspace of zm_delta_rule_backward for n tokens in desc->n_seq sequences
+ * (about 2.5 states of a head to each 64 tokens: the states are formed again
+ * and kept chunk by chunk). */
+ZM_API int zm_delta_rule_backward_workspace_size(const zm_delta_desc* desc, int64_t n, size_t* bytes);
+
+/* The gradient of zm_delta_rule from its inputs alone: d_o [n, heads, d_head]
+ * (stride desc->ld_o) and dstate_out (gradient of the last states, NULL: zeros)
+ * give dq, dk [n, heads_k, d_head] (summed over the value heads of a key head),
+ * dv [n, heads, d_head] in the io type, dg, dbeta fp32 [n, heads] and
+ * dstate_in (NULL: not wanted).  Token strides as in the descriptor.  Rows
+ * outside every sequence are left as they were.  The outputs must not overlap the inputs
+ * (dstate_in may be dstate_out).  Where g is below -128 (a reset) its gradient is
+ * zero up to rounding.  Bitwise reproducible. */
+ZM_API int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* offsets,
+                  const void* d_o, const void* q, const void* k, const void* v, const float* g,
+                  const float* beta, const float* state_in, const float* dstate_out,
+                  void* dq, int64_t ld_dq, void* dk, int64_t ld_dk, void* dv, int64_t ld_dv,
+                  float* dg, float* dbeta, float* dstate_in,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 ZM_API const char* zm_status_string(int status);
 

@@ -30,6 +30,7 @@ EXPORTED = (
     "zm_status_string", "zm_ttt_last_error", "zm_ttt_version", "zm_ttt_set_profile_events",
     "zm_layer_norm", "zm_layer_norm_backward_workspace_size", "zm_layer_norm_backward",
     "zm_rotary", "zm_delta_rule_workspace_size", "zm_delta_rule", "zm_delta_rule_step",
+    "zm_delta_rule_backward_workspace_size", "zm_delta_rule_backward",
 )
 
 
@@ -154,10 +155,14 @@ def load_library(path: str | None = None):
     _DD = ctypes.POINTER(DeltaDesc)
     lib.zm_delta_rule_workspace_size.argtypes = [_DD, _I64, ctypes.POINTER(_SZ)]
     lib.zm_delta_rule.argtypes = [_DD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+    lib.zm_delta_rule_backward_workspace_size.argtypes = [_DD, _I64, ctypes.POINTER(_SZ)]
+    lib.zm_delta_rule_backward.argtypes = [_DD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
+                                           _P, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]
     lib.zm_delta_rule_step.argtypes = [_DD, _P, _P, _P, _P, _P, _P, _P, _P]
     for name in ("zm_layer_norm", "zm_layer_norm_backward_workspace_size",
                  "zm_layer_norm_backward", "zm_rotary", "zm_delta_rule_workspace_size",
-                 "zm_delta_rule", "zm_delta_rule_step"):
+                 "zm_delta_rule", "zm_delta_rule_step", "zm_delta_rule_backward_workspace_size",
+                 "zm_delta_rule_backward"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("zm_ttt_workspace_size", "zm_ttt_update", "zm_ttt_update_loss", "zm_ttt_apply",
                  "zm_ttt_update_apply", "zm_ttt_update_apply_scratch",
@@ -795,6 +800,54 @@ def delta_rule_step(q, k, v, g, beta, state, scale=None, out=None):
             _ptr(o), _stream(q.device))
     _check(st, "zm_delta_rule_step")
     return o
+
+
+def delta_rule_backward_workspace_size(desc: DeltaDesc, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().zm_delta_rule_backward_workspace_size(ctypes.byref(desc), int(n),
+                                                                ctypes.byref(out)),
+           "zm_delta_rule_backward_workspace_size")
+    return int(out.value)
+
+
+def delta_rule_backward(do, q, k, v, g, beta, state=None, dstate=None, offsets=None, scale=None,
+                        out=None, workspace=None):
+    """Gradients of delta_rule from its inputs, do (the gradient of o) and dstate
+    (the gradient of the last states, None: zeros): (dq, dk, dv, dg, dbeta, the
+    gradient of the first states).  out: those six tensors to write to."""
+    desc, n = _delta_inputs(q, k, v, g, beta, scale)
+    desc.n_seq = _delta_offsets(offsets)
+    h, hk, d = desc.heads, desc.heads_k, desc.d_head
+    _delta_state("state", state, desc)
+    _delta_state("dstate", dstate, desc)
+    if out is None:
+        like = dict(dtype=q.dtype, device=q.device)
+        f32 = dict(dtype=torch.float32, device=q.device)
+        out = (torch.empty((n, hk, d), **like), torch.empty((n, hk, d), **like),
+               torch.empty((n, h, d), **like), torch.empty((n, h), **f32),
+               torch.empty((n, h), **f32), torch.empty((desc.n_seq, h, d, d), **f32))
+    if len(out) != 6:
+        raise ZmError("out: the six tensors dq, dk, dv, dg, dbeta, dstate")
+    dq, dk, dv, dg, dbeta, dstart = out
+    desc.ld_o = _heads_rows("do", do, n, h, d, q.dtype)
+    lds = [_heads_rows("dq", dq, n, hk, d, q.dtype), _heads_rows("dk", dk, n, hk, d, q.dtype),
+           _heads_rows("dv", dv, n, h, d, q.dtype)]
+    for name, t in (("dg", dg), ("dbeta", dbeta)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
+            raise ZmError(f"{name} must be contiguous fp32 [{n}, {h}]")
+    _delta_state("the first states' gradient", dstart, desc)
+    _same_gpu(q, do, k, v, g, beta, state, dstate, offsets, *out, workspace)
+    need = delta_rule_backward_workspace_size(desc, n)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None \
+        else workspace
+    with _on_device(q.device):
+        st = load_library().zm_delta_rule_backward(
+            ctypes.byref(desc), n, _ptr(offsets), _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+            _ptr(beta), _ptr(state), _ptr(dstate), _ptr(dq), lds[0], _ptr(dk), lds[1], _ptr(dv),
+            lds[2], _ptr(dg), _ptr(dbeta), _ptr(dstart), _ptr(ws), _ws_bytes(ws),
+            _stream(q.device))
+    _check(st, "zm_delta_rule_backward")
+    return out
 
 
 def set_profile_events(events):

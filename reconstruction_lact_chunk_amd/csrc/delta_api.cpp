@@ -115,6 +115,47 @@ ForwardWs forward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, cons
   return f;
 }
 
+struct BackwardWs {
+  DeltaArgs a;
+  float *trans, *starts, *ends, *e;   // segments
+  float *m_in, *d_m, *u, *x, *dq, *dk;
+  size_t bytes;
+};
+
+BackwardWs backward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, const int* offsets, void* ws) {
+  BackwardWs f{};
+  Carve c{(char*)ws};
+  f.a.sq = seqs(d, p, n, offsets, c);
+  const size_t slots = (size_t)p.n_chunks * d->heads, tile = (size_t)kTriFrags * kFragElems;
+  const size_t dd = (size_t)d->d_head * d->d_head, rows = (size_t)n * d->heads * d->d_head;
+  f.a.t_frags = c.take<uint16_t>(slots * 3 * tile);
+  f.a.tt_frags = c.take<uint16_t>(slots * 3 * tile);
+  f.a.pt_frags = c.take<uint16_t>(slots * 3 * tile);
+  f.a.rows = c.take<float>(slots * 3 * kChunk);
+  if (p.split) {
+    const size_t states = (size_t)p.n_segs * d->heads * dd;
+    f.trans = c.take<float>(3 * states);
+    f.starts = c.take<float>(states);
+    f.ends = c.take<float>(states);
+    f.e = c.take<float>(states);
+  }
+  f.m_in = c.take<float>(slots * dd);
+  f.d_m = c.take<float>(slots * dd);
+  f.u = c.take<float>(rows);
+  f.x = c.take<float>(rows);
+  if (d->heads != d->heads_k) {
+    f.dq = c.take<float>(rows);
+    f.dk = c.take<float>(rows);
+  }
+  f.bytes = c.at;
+  f.a.heads = d->heads;
+  f.a.heads_k = d->heads_k;
+  f.a.d = d->d_head;
+  f.a.scale = d->scale;
+  f.a.f32 = d->io_dtype == ZM_F32;
+  return f;
+}
+
 int check_counts(const zm_delta_desc* d, int64_t n) {
   if (n < 0 || n > kMaxDeltaTokens || (d->n_seq == 0 && n > 0)) return ZM_ERR_INVALID_ARG;
   const int64_t chunks = (n + (int64_t)(kChunk - 1) * d->n_seq) / kChunk;
@@ -188,7 +229,7 @@ int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* offsets, 
   if (p.split) {
     s.trans = f.trans;
     ZM_HIP(launch_delta_scan(f.a, s, st));
-    ZM_HIP(launch_delta_join(f.a, s, f.starts, st));
+    ZM_HIP(launch_delta_join(f.a, DeltaJoinArgs{state_in, f.trans, 2, nullptr, f.starts}, st));
     s.trans = nullptr;
     s.seg_start = f.starts;
   }
@@ -220,6 +261,82 @@ int zm_delta_rule_step(const zm_delta_desc* desc, const void* q, const void* k, 
   a.scale = desc->scale;
   a.f32 = desc->io_dtype == ZM_F32;
   ZM_HIP(launch_delta_step(a, (hipStream_t)stream));
+  return ZM_OK;
+}
+
+int zm_delta_rule_backward_workspace_size(const zm_delta_desc* desc, int64_t n, size_t* bytes) {
+  if (!bytes) return ZM_ERR_INVALID_ARG;
+  ZM_TRY(check_delta(desc));
+  ZM_TRY(check_counts(desc, n));
+  *bytes = backward_ws(desc, delta_plan(desc, n), n, nullptr, nullptr).bytes;
+  return ZM_OK;
+}
+
+int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* offsets, const void* d_o,
+                           const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           const float* state_in, const float* dstate_out, void* dq, int64_t ld_dq,
+                           void* dk, int64_t ld_dk, void* dv, int64_t ld_dv, float* dg, float* dbeta,
+                           float* dstate_in, void* workspace, size_t workspace_bytes, void* stream) {
+  ZM_TRY(check_delta(desc));
+  ZM_TRY(check_counts(desc, n));
+  ZM_TRY(check_inputs(desc, n, offsets, q, k, v, g, beta));
+  const int64_t wk = (int64_t)desc->heads_k * desc->d_head, wv = (int64_t)desc->heads * desc->d_head;
+  if (ld_dq < wk || ld_dk < wk || ld_dv < wv || ld_dq % 8 || ld_dk % 8 || ld_dv % 8) return ZM_ERR_INVALID_ARG;
+  if (n > 0) {
+    ZM_TRY(check_ptr(d_o, 16));
+    ZM_TRY(check_ptr(dq, 16));
+    ZM_TRY(check_ptr(dk, 16));
+    ZM_TRY(check_ptr(dv, 16));
+    ZM_TRY(check_ptr(dg, 4));
+    ZM_TRY(check_ptr(dbeta, 4));
+  }
+  if (!aligned(state_in, 16) || !aligned(dstate_out, 16) || !aligned(dstate_in, 16)) return ZM_ERR_INVALID_ARG;
+  const DeltaPlan p = delta_plan(desc, n);
+  BackwardWs f = backward_ws(desc, p, n, offsets, workspace);
+  ZM_TRY(check_workspace(workspace, workspace_bytes, f.bytes));
+  if (desc->n_seq == 0) return ZM_OK;
+  set_inputs(f.a, desc, q, k, v, g, beta);
+  const hipStream_t st = (hipStream_t)stream;
+  if (f.a.sq.chunks) ZM_HIP(launch_delta_table(f.a.sq, st));
+  ZM_HIP(launch_delta_prep(f.a, true, st));
+  DeltaScanArgs s{};
+  s.state_in = state_in;
+  DeltaGradArgs r{};
+  r.d_o = DeltaTokens{d_o, desc->ld_o};
+  r.dstate_out = dstate_out;
+  if (p.split) {
+    s.trans = f.trans;
+    s.both = true;
+    ZM_HIP(launch_delta_scan(f.a, s, st));
+    ZM_HIP(launch_delta_join(f.a, DeltaJoinArgs{state_in, f.trans, 3, nullptr, f.starts}, st));
+    s.trans = nullptr;
+    s.seg_start = f.starts;
+    r.e_out = f.e;
+    ZM_HIP(launch_delta_reverse(f.a, r, st));
+    ZM_HIP(launch_delta_join(f.a, DeltaJoinArgs{dstate_out, f.trans, 3, f.e, f.ends}, st));
+    r.e_out = nullptr;
+    r.seg_end = f.ends;
+  }
+  s.m_out = f.m_in;
+  s.u_out = f.u;
+  ZM_HIP(launch_delta_scan(f.a, s, st));
+  r.dstate_in = dstate_in;
+  r.m_in = f.m_in;
+  r.d_m = f.d_m;
+  r.u = f.u;
+  r.x = f.x;
+  r.dv = dv;
+  r.ld_dv = ld_dv;
+  r.dq = dq;
+  r.dk = dk;
+  r.ld_dq = ld_dq;
+  r.ld_dk = ld_dk;
+  r.dq_part = f.dq;
+  r.dk_part = f.dk;
+  r.dg = dg;
+  r.dbeta = dbeta;
+  ZM_HIP(launch_delta_reverse(f.a, r, st));
+  ZM_HIP(launch_delta_grads(f.a, r, st));
   return ZM_OK;
 }
 

@@ -72,7 +72,9 @@ struct DeltaScanArgs {
   const float* state_in;    // [n_seq][heads][d][d] or null (zeros)
   float* state_out;         // the same, or null
   const float* seg_start;   // [n_segs][heads][d][d]: states at the segments' starts, or null
-  float* trans;             // [n_segs][heads][2][d][d]: N as [d_k][d_k], B as a state (pass of transitions)
+  float* trans;             // pass of transitions: [n_segs][heads][2 or 3][d][d]: N by rows, B as a
+                            // state and, with both, N by columns
+  bool both;
   void* o;
   int64_t ld_o;
   float* m_out;             // [n_chunks][heads][d][d]: M at each chunk's start (backward), as [d_k][d_v]
@@ -208,15 +210,48 @@ __device__ __forceinline__ Parts<NP> zero_parts() {
   return z;
 }
 
+struct DeltaJoinArgs {
+  const float* init;     // [n_seq][heads][d][d] or null
+  const float* trans;
+  int stride;            // matrices to a segment of trans
+  const float* e;        // the way back: what a segment adds, else null
+  float* to;             // [n_segs][heads][d][d]
+};
+
+// Backward: buffers that the reverse pass and the chunks' gradients share, and outputs.
+struct DeltaGradArgs {
+  DeltaTokens d_o;           // gradient of o
+  const float* dstate_out;   // gradient of the last states, or null
+  float* dstate_in;          // receives the gradient of the first states, or null
+  const float* seg_end;      // [n_segs][heads][d][d]: gradients of the states at the segments' ends, or null
+  float* e_out;              // [n_segs][heads][d][d]: pass of transitions only
+  const float* m_in;         // [n_chunks][heads][d][d] M at each chunk's start, as [d_k][d_v]
+  float* d_m;                // the same of the gradient of M at each chunk's end
+  const float* u;            // [n][heads][d]
+  float* x;                  // [n][heads][d]: gradient of beta o R
+  void* dv;
+  int64_t ld_dv;
+  void* dq;                  // with one value head to a key head, else null
+  void* dk;
+  int64_t ld_dq, ld_dk;
+  float* dq_part;            // [n][heads][d] otherwise
+  float* dk_part;
+  float* dg;                 // [n][heads]
+  float* dbeta;
+};
+
 // ---- launchers --------------------------------------------------------------------
 // The tables of chunks and segments (n_seq > 1).
 hipError_t launch_delta_table(const DeltaSeqs& s, hipStream_t st);
 // T and P (backward: T, T^T, P^T) and the row factors of every chunk and head.
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t st);
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st);
-// The states at the segments' starts from their transitions (s.trans).
-hipError_t launch_delta_join(const DeltaArgs& a, const DeltaScanArgs& s, float* starts,
-                             hipStream_t st);
+// The states at the segments' starts (gradients at their ends) from their transitions.
+hipError_t launch_delta_join(const DeltaArgs& a, const DeltaJoinArgs& j, hipStream_t st);
+// Backward through the chunks of each segment, last first: d_m, x, dv, dstate_in.
+hipError_t launch_delta_reverse(const DeltaArgs& a, const DeltaGradArgs& s, hipStream_t st);
+// dq, dk, dg, dbeta of every chunk and head from u, x, m_in, d_m.
+hipError_t launch_delta_grads(const DeltaArgs& a, const DeltaGradArgs& s, hipStream_t st);
 struct DeltaStepArgs {
   DeltaTokens q, k, v;
   const float* g;

@@ -5,80 +5,11 @@
 // operand tiles.  M, R and U stay in registers: each is the result of one product
 // and the right operand of the next.  Columns 2 c and 2 c + 1 of a wave belong to
 // lane c's two column tiles, so tokens go in and out as pairs.
-#include "delta_rule.h"
+#include "delta_scan.h"
 
 namespace zm {
 
 namespace {
-
-template <int D, bool F32>
-struct ScanCfg {
-  static constexpr int NT = Tok<F32>::NT;
-  static constexpr int PITCH = D + 16;
-  static constexpr int TILE = kChunk * PITCH;   // one part of K or Q
-  static constexpr int WAVES = D / 32;
-  static constexpr int THREADS = 64 * WAVES;
-};
-
-// K (or Q) of the chunk into its LDS parts; rows past `count` are zero.
-template <int D, bool F32>
-__device__ __forceinline__ void stage(uint16_t* lds, const typename Tok<F32>::T* src, int64_t ld,
-                                      int count) {
-  using C = ScanCfg<D, F32>;
-  constexpr int CPR = D / 8;
-  for (int i = threadIdx.x; i < kChunk * CPR; i += C::THREADS) {
-    const int row = i / CPR, col = 8 * (i % CPR);
-    Parts<C::NT> p = zero_parts<C::NT>();
-    if (row < count) p = load8(src + (int64_t)row * ld + col);
-#pragma unroll
-    for (int k = 0; k < C::NT; ++k) *(bf16x8*)(lds + k * C::TILE + row * C::PITCH + col) = p.p[k];
-  }
-}
-
-template <int D, bool F32>
-__device__ __forceinline__ Parts<Tok<F32>::NT> lds_row(const uint16_t* lds, int row, int col) {
-  using C = ScanCfg<D, F32>;
-  Parts<C::NT> p;
-#pragma unroll
-  for (int k = 0; k < C::NT; ++k) p.p[k] = *(const bf16x8*)(lds + k * C::TILE + row * C::PITCH + col);
-  return p;
-}
-
-// Rows dim_row(mt, .) of the transpose, slots = tokens of step ts.
-template <int D, bool F32>
-__device__ __forceinline__ Parts<Tok<F32>::NT> lds_col(const uint16_t* lds, int mt, int ts, int g,
-                                                       int c) {
-  using C = ScanCfg<D, F32>;
-  Parts<C::NT> p;
-  const int row = 32 * ts + dtau(g, c >> 2), col = 32 * (mt >> 1) + 8 * (c & 3) + 4 * (mt & 1);
-#pragma unroll
-  for (int k = 0; k < C::NT; ++k) {
-    const uint16_t* at = lds + k * C::TILE + row * C::PITCH + col;
-    p.p[k] = __builtin_shufflevector(delta_read_tr(at), delta_read_tr(at + 8 * C::PITCH), 0, 1, 2, 3,
-                                     4, 5, 6, 7);
-  }
-  return p;
-}
-
-template <int NP>
-__device__ __forceinline__ Parts<NP> frag(const uint16_t* f, int i, int lane) {
-  Parts<NP> p;
-#pragma unroll
-  for (int k = 0; k < NP; ++k)
-    p.p[k] = *(const bf16x8*)(f + (k * kTriFrags + i) * kFragElems + lane * 8);
-  return p;
-}
-
-// A pair of neighbouring columns of one token.
-__device__ __forceinline__ f32x2 load_pair(const uint16_t* p) {
-  const unsigned w = *(const unsigned*)p;
-  return f32x2{bf16lo(w), bf16hi(w)};
-}
-__device__ __forceinline__ f32x2 load_pair(const float* p) { return *(const f32x2*)p; }
-__device__ __forceinline__ void store_pair(uint16_t* p, float a, float b) {
-  *(unsigned*)p = pack_bf16x2(a, b);
-}
-__device__ __forceinline__ void store_pair(float* p, float a, float b) { *(f32x2*)p = f32x2{a, b}; }
 
 // MODE 0: outputs and the last state.  MODE 1 (backward): M at every chunk's start
 // and U instead of the outputs.  MODE 2: the segment's transition: blocks of the
@@ -102,7 +33,8 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
   const int si = MODE == kTransition ? blk >> 1 : blk;
   const int4 sg = delta_seg(a.sq, si);
   if (sg.y < 0) return;
-  if (MODE == kTransition && (sg.w & 2)) return;  // nothing follows the last segment
+  // nothing follows the last segment; its N serves the way back
+  if (MODE == kTransition && (sg.w & 2) && !(unit && sa.both)) return;
   const int hk = h / (a.heads / a.heads_k);
   const int dv = 32 * (threadIdx.x >> 6) + 2 * c;  // of the lane's pair of columns
 
@@ -279,9 +211,17 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
   }
 
   float* out = nullptr;
-  if (MODE == kTransition) out = sa.trans + (((int64_t)si * a.heads + h) * 2 + 1) * dd;
-  if (unit) {  // N by rows, as the join reads it
-    out -= dd;
+  if (MODE == kTransition)
+    out = sa.trans + ((int64_t)si * a.heads + h) * (sa.both ? 3 : 2) * dd + (unit ? 2 : 1) * dd;
+  if (unit) {  // N by rows for the join, and by columns for the one on the way back
+    if (sa.both) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+          *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+    }
+    out -= 2 * dd;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -300,46 +240,48 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
   }
 }
 
-// The states at the segments' starts: M <- N M + B along each sequence.  A wave has
-// 16 columns of one (sequence, head); the blocks of a sequence's first segment
-// go through all of its segments.
-template <int D>
-__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a, DeltaScanArgs sa, float* starts) {
+// The states at the segments' starts, M <- N M + B along each sequence, or (REV) the
+// gradients at the segments' ends, M <- N^T M + E from its last segment back.  A
+// wave has 16 columns of one (sequence, head); the blocks of a sequence's first
+// (last) segment go through all of its segments.
+template <int D, bool REV>
+__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a, DeltaJoinArgs ja) {
   constexpr int KS = D / 32, MT = D / 16, SL = D / 16;
   const int lane = threadIdx.x, g = lane >> 4, c = lane & 15;
   const int dv = 16 * (blockIdx.x % SL) + c;
   const int h = (blockIdx.x / SL) % a.heads;
   int si = blockIdx.x / SL / a.heads;
   int4 sg = delta_seg(a.sq, si);
-  if (sg.y < 0 || !(sg.w & 1)) return;
+  if (sg.y < 0 || !(sg.w & (REV ? 2 : 1))) return;
   const int64_t dd = (int64_t)D * D;
   f32x4 m[MT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     m[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (sa.state_in)
-      m[mt] = *(const f32x4*)(sa.state_in + ((int64_t)sg.z * a.heads + h) * dd + (int64_t)dv * D +
+    if (ja.init)
+      m[mt] = *(const f32x4*)(ja.init + ((int64_t)sg.z * a.heads + h) * dd + (int64_t)dv * D +
                               dim_row(mt, 4 * g));
   }
   while (true) {
-    float* const to = starts + ((int64_t)si * a.heads + h) * dd + (int64_t)dv * D;
+    const int64_t at = (int64_t)si * a.heads + h;
+    float* const to = ja.to + at * dd + (int64_t)dv * D;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) *(f32x4*)(to + dim_row(mt, 4 * g)) = m[mt];
-    if (sg.w & 2) return;
-    const float* const nn = sa.trans + ((int64_t)si * a.heads + h) * 2 * dd;
+    if (sg.w & (REV ? 1 : 2)) return;
+    const float* const nn = ja.trans + at * ja.stride * dd + (REV ? 2 * dd : 0);
+    const float* const add = (REV ? ja.e + at * dd : nn + dd) + (int64_t)dv * D;
     Parts<3> b[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s) b[s] = split_tiles<3>(m[2 * s], m[2 * s + 1]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-      m[mt] = *(const f32x4*)(nn + dd + (int64_t)dv * D + dim_row(mt, 4 * g));
+    for (int mt = 0; mt < MT; ++mt) m[mt] = *(const f32x4*)(add + dim_row(mt, 4 * g));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int s = 0; s < KS; ++s)
         mma<2>(m[mt], load8(nn + (int64_t)dim_row(mt, c) * D + 32 * s + 8 * g), b[s]);
-    ++si;
-    if (si >= a.sq.n_segs) return;
+    si += REV ? -1 : 1;
+    if (si < 0 || si >= a.sq.n_segs) return;
     sg = delta_seg(a.sq, si);
   }
 }
@@ -366,11 +308,15 @@ hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStre
   return a.f32 ? scan_any<64, true>(a, s, st) : scan_any<64, false>(a, s, st);
 }
 
-hipError_t launch_delta_join(const DeltaArgs& a, const DeltaScanArgs& s, float* starts,
-                             hipStream_t st) {
+hipError_t launch_delta_join(const DeltaArgs& a, const DeltaJoinArgs& j, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads * (a.d / 16))), blk(64);
-  if (a.d == 128) hipLaunchKernelGGL((k_delta_join<128>), grid, blk, 0, st, a, s, starts);
-  else hipLaunchKernelGGL((k_delta_join<64>), grid, blk, 0, st, a, s, starts);
+  if (a.d == 128) {
+    if (j.e) hipLaunchKernelGGL((k_delta_join<128, true>), grid, blk, 0, st, a, j);
+    else hipLaunchKernelGGL((k_delta_join<128, false>), grid, blk, 0, st, a, j);
+  } else {
+    if (j.e) hipLaunchKernelGGL((k_delta_join<64, true>), grid, blk, 0, st, a, j);
+    else hipLaunchKernelGGL((k_delta_join<64, false>), grid, blk, 0, st, a, j);
+  }
   return hipGetLastError();
 }
 
