@@ -98,9 +98,11 @@ ForwardWs forward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, cons
   Carve c{(char*)ws};
   f.a.sq = seqs(d, p, n, offsets, c);
   const size_t slots = (size_t)p.n_chunks * d->heads, tile = (size_t)kTriFrags * kFragElems;
-  f.a.t_frags = c.take<uint16_t>(slots * 3 * tile);
-  f.a.p_frags = c.take<uint16_t>(slots * (d->io_dtype == ZM_F32 ? 3 : 2) * tile);
-  f.a.rows = c.take<float>(slots * 3 * kChunk);
+  if (d->io_dtype == ZM_F32) {
+    f.a.t_frags = c.take<uint16_t>(slots * 3 * tile);
+    f.a.p_frags = c.take<uint16_t>(slots * 3 * tile);
+    f.a.rows = c.take<float>(slots * 3 * kChunk);
+  }
   if (p.split) {
     const size_t states = (size_t)p.n_segs * d->heads * d->d_head * d->d_head;
     f.trans = c.take<float>(2 * states);
@@ -220,7 +222,8 @@ int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* offsets, 
   set_inputs(f.a, desc, q, k, v, g, beta);
   const hipStream_t st = (hipStream_t)stream;
   if (f.a.sq.chunks) ZM_HIP(launch_delta_table(f.a.sq, st));
-  ZM_HIP(launch_delta_prep(f.a, false, st));
+  const auto scan = f.a.f32 ? launch_delta_scan : launch_delta_fused;
+  if (f.a.f32) ZM_HIP(launch_delta_prep(f.a, false, st));
   DeltaScanArgs s{};
   s.state_in = state_in;
   s.state_out = state_out;
@@ -228,12 +231,12 @@ int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* offsets, 
   s.ld_o = desc->ld_o;
   if (p.split) {
     s.trans = f.trans;
-    ZM_HIP(launch_delta_scan(f.a, s, st));
+    ZM_HIP(scan(f.a, s, st));
     ZM_HIP(launch_delta_join(f.a, DeltaJoinArgs{state_in, f.trans, 2, nullptr, f.starts}, st));
     s.trans = nullptr;
     s.seg_start = f.starts;
   }
-  ZM_HIP(launch_delta_scan(f.a, s, st));
+  ZM_HIP(scan(f.a, s, st));
   return ZM_OK;
 }
 
@@ -299,6 +302,7 @@ int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* 
   const hipStream_t st = (hipStream_t)stream;
   if (f.a.sq.chunks) ZM_HIP(launch_delta_table(f.a.sq, st));
   ZM_HIP(launch_delta_prep(f.a, true, st));
+  const auto scan = f.a.f32 ? launch_delta_scan : launch_delta_fused;
   DeltaScanArgs s{};
   s.state_in = state_in;
   DeltaGradArgs r{};
@@ -307,7 +311,7 @@ int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* 
   if (p.split) {
     s.trans = f.trans;
     s.both = true;
-    ZM_HIP(launch_delta_scan(f.a, s, st));
+    ZM_HIP(scan(f.a, s, st));
     ZM_HIP(launch_delta_join(f.a, DeltaJoinArgs{state_in, f.trans, 3, nullptr, f.starts}, st));
     s.trans = nullptr;
     s.seg_start = f.starts;
@@ -319,7 +323,7 @@ int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* 
   }
   s.m_out = f.m_in;
   s.u_out = f.u;
-  ZM_HIP(launch_delta_scan(f.a, s, st));
+  ZM_HIP(scan(f.a, s, st));
   r.dstate_in = dstate_in;
   r.m_in = f.m_in;
   r.d_m = f.d_m;

@@ -1,0 +1,689 @@
+// The chunks of a segment in order for bf16 tokens (delta_rule.h), one workgroup per
+// (segment, head) with two kinds of waves:
+//   D / 32 state waves: 32 columns of M (d_v) each and all its rows.  M, R and U stay
+//     in registers: each is the result of one product and the right operand of
+//     the next.  Columns 2 c and 2 c + 1 belong to lane c's two column tiles, so
+//     tokens go in and out as pairs.
+//   4 triangle waves, one chunk ahead: T = (I + A)^-1 and P by blocks of 16, wave i the
+//     block row i, left in LDS as operand tiles for the state waves.  They also
+//     start the direct loads of K and Q two chunks ahead.
+// Nothing of a chunk but q, k, v, o moves through memory.  The state waves are bound
+// by their own issue (matrix instructions and the splitting of fp32 operands into
+// bf16 parts); the triangle waves run in the gaps.
+#include "delta_rule.h"
+
+namespace zm {
+
+namespace {
+
+enum { kOutputs = 0, kKeep = 1, kTransition = 2 };
+
+constexpr int kAtPitch = 68;   // floats of a row of A^T in LDS
+constexpr int kDPitch = 20;    // floats of a row of a diagonal block's inverse
+// K tiles in LDS: this chunk's, the next one's, the one in flight; Q's third takes the
+// place of the first, whose last reader is done before its load starts.
+constexpr int kRingK = 3, kRingQ = 2;
+
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+
+template <int D, int MODE>
+struct FusedCfg {
+  static constexpr int SW = D / 32;             // state waves
+  static constexpr int TW = 4;                  // triangle waves
+  static constexpr int THREADS = 64 * (SW + TW);
+  static constexpr int GPR = D / 8;             // 16-byte granules of a row
+  static constexpr int TILE = kChunk * D;       // elements of a K or Q tile
+  static constexpr bool Q = MODE == kOutputs;
+  static constexpr int TRI = kTriFrags * kFragElems;  // elements of one part of a triangle
+  // byte offsets
+  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = kRingK * TILE * 2;
+  static constexpr int kOffT = kOffQ + (Q ? kRingQ * TILE * 2 : 0);
+  static constexpr int kOffP = kOffT + 3 * TRI * 2;
+  static constexpr int kOffV = kOffP + (Q ? 2 * TRI * 2 : 0);
+  static constexpr int kOffRows = kOffV + TILE * 2;                    // two chunks' factors
+  static constexpr int kOffAt = kOffRows + 2 * 3 * kChunk * 4;
+  static constexpr int kOffD = kOffAt + kChunk * kAtPitch * 4;
+  static constexpr int kOffDt = kOffD + 4 * 16 * kDPitch * 4;
+  static constexpr int kOffCs = kOffDt + 4 * 16 * kDPitch * 4;
+  static constexpr int BYTES = kOffCs + TW * kChunk * 8;
+  static_assert(BYTES <= 160 * 1024, "LDS");
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Tiles hold row r's granule p at place p ^ swizzle(r): row reads (16 rows of tile
+// order, two granules) and transposing reads spread over the banks.
+template <int D>
+__device__ __forceinline__ constexpr int swizzle(int r) {
+  return D == 128 ? ((r & 3) << 2) | (((r >> 4) & 1) << 1) : (((r >> 1) & 1) << 2) | (((r >> 4) & 1) << 1);
+}
+template <int D>
+__device__ __forceinline__ Parts<1> tile_row(const uint16_t* t, int row, int granule) {
+  return Parts<1>{{*(const bf16x8*)(t + row * D + 8 * (granule ^ swizzle<D>(row)))}};
+}
+// What one wave issues is in order, and a matrix instruction leaves room for two or
+// three others while it runs: these place `v` vector operations after each of `n`
+// matrix instructions, and keep the steps of a pipelined loop apart, which also
+// bounds what is in flight to the registers there are.
+template <int N, int V>
+__device__ __forceinline__ void weave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);  // vector
+  }
+}
+template <int N>
+__device__ __forceinline__ void weave_reads() {
+  __builtin_amdgcn_sched_group_barrier(0x100, N, 0);  // LDS reads
+}
+
+// LDS reads and writes of this wave are done, then the workgroup's barrier.  Loads
+// and stores of global memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+__device__ __forceinline__ void wait_direct_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
+template <int D, int MODE>
+__global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, DeltaScanArgs sa) {
+  using C = FusedCfg<D, MODE>;
+  constexpr int KS = D / 32, MT = D / 16;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[C::BYTES];
+  int blk = blockIdx.x;
+  const int h = blk % a.heads;
+  blk /= a.heads;
+  const bool unit = MODE == kTransition && (blk & 1);
+  const int si = MODE == kTransition ? blk >> 1 : blk;
+  const int4 sg = delta_seg(a.sq, si);
+  if (sg.y < 0) return;
+  // nothing follows the last segment; its N serves the way back
+  if (MODE == kTransition && (sg.w & 2) && !(unit && sa.both)) return;
+  const int n = sg.y;
+  const int hk = h / (a.heads / a.heads_k);
+  int64_t tok0 = 0;
+  int last = 0;  // tokens of the last chunk
+  if (n > 0) {
+    tok0 = delta_chunk(a.sq, sg.x).x;
+    last = delta_chunk(a.sq, sg.x + n - 1).y;
+  }
+  auto k_tile = [&](int j) { return (uint16_t*)(smem + C::kOffK) + (j % kRingK) * C::TILE; };
+  auto q_tile = [&](int j) { return (uint16_t*)(smem + C::kOffQ) + (j % kRingQ) * C::TILE; };
+  uint16_t* const tf = (uint16_t*)(smem + C::kOffT);
+  uint16_t* const pf = (uint16_t*)(smem + C::kOffP);
+  uint16_t* const vt = (uint16_t*)(smem + C::kOffV);
+  auto row_factors = [&](int j) { return (float*)(smem + C::kOffRows) + (j & 1) * 3 * kChunk; };
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+
+  // the tiles' upper triangles stay zero
+  for (int i = threadIdx.x; i < (C::kOffV - C::kOffT) / 16; i += C::THREADS)
+    *(u32x4*)(smem + C::kOffT + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+
+  if (wave >= C::SW) {
+    // ---- triangle waves: wave PW has block row PW of A and T and block row 3 - PW of P,
+    // five tiles each ----
+    const uint16_t* const kp = (const uint16_t*)a.k.p + tok0 * a.k.ld + hk * D;
+    const uint16_t* const qp = (const uint16_t*)a.q.p + tok0 * a.q.ld + hk * D;
+    const uint16_t* const vp = (const uint16_t*)a.v.p + tok0 * a.v.ld + h * D;
+    float* const at = (float*)(smem + C::kOffAt);
+    float* const dm = (float*)(smem + C::kOffD);
+    float* const dt = (float*)(smem + C::kOffDt);
+    auto triangle = [&](auto which) {
+      constexpr int PW = decltype(which)::value, PI = 3 - PW;
+      double* const cs = (double*)(smem + C::kOffCs) + PW * kChunk;
+
+      // Rows past the chunk's tokens take the last one's: finite where that is, and
+      // their beta of zero leaves them out.
+      auto load_tile = [&](const uint16_t* src, int64_t ld, uint16_t* dst, int j) {
+        const int top = (j == n - 1 ? last : kChunk) - 1;
+        constexpr int RPL = 64 / C::GPR, LOADS = kChunk / RPL / C::TW;  // rows of a load; loads of a wave
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          const int r0 = (PW * LOADS + i) * RPL, r = r0 + lane / C::GPR;
+          const int64_t row = (int64_t)kChunk * j + (r < top ? r : top);
+          const int col = 8 * ((lane % C::GPR) ^ swizzle<D>(r));
+          __builtin_amdgcn_global_load_lds((const void*)(src + row * ld + col), (lds_void*)(dst + r0 * D), 16, 0, 0);
+        }
+      };
+      auto load_k = [&](int j) { load_tile(kp, a.k.ld, k_tile(j), j); };
+      auto load_q = [&](int j) {
+        if (C::Q) load_tile(qp, a.q.ld, q_tile(j), j);
+      };
+      auto load_v = [&](int j) {
+        if (!unit) load_tile(vp, a.v.ld, vt, j);
+      };
+      float gn = 0.f, bn = 0.f;
+      auto load_gates = [&](int j) {
+        gn = bn = 0.f;
+        if (lane < (j == n - 1 ? last : kChunk)) {
+          const int64_t t = (tok0 + (int64_t)kChunk * j + lane) * a.heads + h;
+          gn = a.g[t];
+          bn = a.beta[t];
+        }
+      };
+      f32x4 tt[4], pt[4];  // T^T and P^T: rows are columns of T and P
+      auto tile = [&](const uint16_t* t, int block, Parts<1>* f) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) f[k] = tile_row<D>(t, 16 * block + c, 4 * k + g);
+      };
+      // K K^T, A^T and the diagonal block's inverse
+      auto factor = [&](int j) {
+        const uint16_t* const kt = k_tile(j);
+        const float be = bn;
+        double s = gn < kMinLogDecay ? kMinLogDecay : gn;
+        s *= 1.4426950408889634;  // exponents of two from here
+        if (j + 1 < n) load_gates(j + 1);
+        Parts<1> ki[KS];
+        tile(kt, PW, ki);
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+          const double o = __shfl_up(s, m, 64);
+          if (lane >= m) s += o;
+        }
+        cs[lane] = s;
+        f32x4 kk[4];
+#pragma unroll
+        for (int J = 0; J <= PW; ++J) {
+          kk[J] = f32x4{0.f, 0.f, 0.f, 0.f};
+          Parts<1> kj[KS];
+          if (J < PW) tile(kt, J, kj);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) mma<0>(kk[J], ki[k], J < PW ? kj[k] : ki[k]);
+        }
+        if (PW == 0) {
+          const double end = __shfl(s, 63, 64);
+          float* const r = row_factors(j);
+          r[lane] = __builtin_amdgcn_exp2f((float)s);
+          r[kChunk + lane] = __builtin_amdgcn_exp2f((float)(end - s));
+          r[2 * kChunk + lane] = be;
+        }
+        double ci[4];
+        float bi[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          ci[r] = cs[16 * PW + 4 * g + r];
+          bi[r] = __shfl(be, 16 * PW + 4 * g + r, 64);
+        }
+#pragma unroll
+        for (int J = PW; J >= 0; --J) {
+          const double cj = cs[16 * J + c];
+          f32x4 av;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            // above the diagonal the exponent may be positive: not taken
+            const float e = __builtin_amdgcn_exp2f((float)(ci[r] - cj));
+            av[r] = J < PW || 4 * g + r > c ? bi[r] * e * kk[J][r] : 0.f;
+          }
+          *(f32x4*)(at + (16 * J + c) * kAtPitch + 16 * PW + 4 * g) = av;
+        }
+        // row c of the inverse, from its end: a forward substitution, which (unlike a
+        // product of powers of A) stays exact where keys repeat
+        float x[16];
+        const float* const blk = at + 16 * PW * kAtPitch + 16 * PW;
+#pragma unroll
+        for (int i = 15; i >= 0; --i) {
+          f32x4 row[4];
+#pragma unroll
+          for (int q = 3; q >= 0; --q)
+            if (4 * q + 3 > i) row[q] = *(const f32x4*)(blk + i * kAtPitch + 4 * q);
+          // two chains: the newest entry last
+          float v = i == c ? 1.f : 0.f, y = 0.f;
+#pragma unroll
+          for (int q = 15; q > i; --q) {
+            if (q & 1) v = fmaf(-row[q / 4][q % 4], x[q], v);
+            else y = fmaf(-row[q / 4][q % 4], x[q], y);
+          }
+          x[i] = v + y;
+        }
+        if (g == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *(f32x4*)(dm + (16 * PW + c) * kDPitch + 4 * i) =
+                f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dt[(16 * PW + i) * kDPitch + c] = x[i];
+        }
+      };
+      // block row PW of T, transposed:  T_iw^T = -D_w^T sum_{w < j <= i} A_jw^T T_ij^T
+      // on fp32 matrix instructions whose results are the next right operands
+      auto solve = [&]() {
+        f32x4 y[4], av[4][4], dv[4];
+#pragma unroll
+        for (int w = 0; w < PW; ++w) {
+          y[w] = tt[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+          dv[w] = *(const f32x4*)(dt + (16 * w + c) * kDPitch + 4 * g);
+#pragma unroll
+          for (int j = w + 1; j <= PW; ++j) av[w][j] = *(const f32x4*)(at + (16 * w + c) * kAtPitch + 16 * j + 4 * g);
+        }
+        tt[PW] = *(const f32x4*)(dm + (16 * PW + c) * kDPitch + 4 * g);
+#pragma unroll
+        for (int j = PW; j >= 0; --j) {
+          if (j < PW) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              tt[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(-dv[j][r], y[j][r], tt[j], 0, 0, 0);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int w = j - 1; w >= 0; --w)
+              y[w] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[w][j][r], tt[j][r], y[w], 0, 0, 0);
+        }
+      };
+      // four slots of an operand tile's lane at a time; `row` the block row of x
+      auto store_tile = [&](uint16_t* to, int row, int J, const f32x4& x, int parts) {
+        const int it = 2 * (row >> 1) + (c >> 3), m = 8 * (row & 1) + 4 * ((c >> 2) & 1) + (c & 3);
+        uint16_t* const at2 =
+            to + low_frag(it, J >> 1) * kFragElems + (16 * (2 * (J & 1) + (g & 1)) + m) * 8 + 4 * (g >> 1);
+        float r[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          if (k >= parts) continue;
+          const u32x2 w = {pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
+          *(u32x2*)(at2 + k * C::TRI) = w;
+          r[0] -= bf16lo(w[0]);
+          r[1] -= bf16hi(w[0]);
+          r[2] -= bf16lo(w[1]);
+          r[3] -= bf16hi(w[1]);
+        }
+      };
+      auto store_t = [&]() {
+#pragma unroll
+        for (int J = 0; J <= PW; ++J) store_tile(tf, PW, J, tt[J], 3);
+      };
+      auto store_p = [&]() {
+        if (!C::Q) return;
+#pragma unroll
+        for (int J = 0; J <= PI; ++J) store_tile(pf, PI, J, pt[J], 2);
+      };
+      // Q K^T with its decays
+      auto scores = [&](int j) {
+        if (!C::Q) return;
+        const uint16_t* const kt = k_tile(j);
+        Parts<1> qi[KS];
+        tile(q_tile(j), PI, qi);
+        const double cp = cs[16 * PI + c];
+#pragma unroll
+        for (int J = 0; J <= PI; ++J) {
+          Parts<1> kj[KS];
+          tile(kt, J, kj);
+          f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < KS; ++k) mma<0>(p, kj[k], qi[k]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float e = __builtin_amdgcn_exp2f((float)(cp - cs[16 * J + 4 * g + r]));
+            pt[J][r] = J < PI || 4 * g + r <= c ? a.scale * e * p[r] : 0.f;
+          }
+        }
+      };
+
+      load_gates(0);
+      load_k(0);
+      load_q(0);
+      load_v(0);
+      if (n > 1) {
+        load_k(1);
+        load_q(1);
+      }
+      wait_direct_loads();
+      lds_barrier();
+      factor(0);
+      lds_barrier();
+      solve();
+      store_t();
+      scores(0);
+      for (int j = 0; j < n; ++j) {
+        wait_direct_loads();
+        lds_barrier();  // everything of chunk j but P, K and Q of chunk j + 1
+        store_p();      // chunk j's, first read after the next barriers
+        if (j + 1 < n) factor(j + 1);
+        if (j + 2 < n) load_k(j + 2);
+        lds_barrier();  // A^T and the diagonal blocks; chunk j's Q and V have been read
+        if (j + 1 < n) load_v(j + 1);
+        if (j + 2 < n) load_q(j + 2);
+        if (j + 1 < n) solve();
+        lds_barrier();  // chunk j's T has been read
+        if (j + 1 < n) {
+          store_t();
+          scores(j + 1);
+        }
+      }
+    };
+    if (n > 0) {
+      switch (wave - C::SW) {
+        case 0: triangle(Const<0>{}); break;
+        case 1: triangle(Const<1>{}); break;
+        case 2: triangle(Const<2>{}); break;
+        default: triangle(Const<3>{}); break;
+      }
+    }
+    return;
+  }
+
+  // ---- state waves ---------------------------------------------------------------
+  const int dv = 32 * wave + 2 * c;  // of the lane's pair of columns
+  f32x4 m[MT][2];
+  const int64_t dd = (int64_t)D * D;
+  const float* init = nullptr;
+  if (MODE != kTransition) {
+    if (sa.seg_start) init = sa.seg_start + ((int64_t)si * a.heads + h) * dd;
+    else if (sa.state_in) init = sa.state_in + ((int64_t)sg.z * a.heads + h) * dd;
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+      const int dk = dim_row(mt, 4 * g);
+      if (init) {
+        m[mt][ct] = *(const f32x4*)(init + (int64_t)(dv + ct) * D + dk);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[mt][ct][r] = unit && dk + r == dv + ct ? 1.f : 0.f;
+      }
+    }
+  // Token token_row(it, 4 g + r) is the lane's first one and a uniform number of
+  // rows on, so addresses are a scalar base and one 32-bit offset a lane.
+  const int lt = token_row(0, 4 * g);
+  const unsigned o_off = MODE == kOutputs ? (unsigned)(lt * sa.ld_o + dv) * 2u : 0u;
+  char* const op = (char*)sa.o + (tok0 * sa.ld_o + h * D) * 2;
+  // Byte offsets in LDS, formed anew for each chunk (pinned) rather than kept for
+  // every use.  The swizzle's upper bits stand alone in a granule's address, so a
+  // step along a row is an exclusive or and one down the rows an addition:
+  // row token_row(0, c), granule g of a K or Q tile
+  const unsigned row_off = (unsigned)(token_row(0, c) * D + 8 * (g ^ swizzle<D>(token_row(0, c)))) * 2u;
+  // the transposing read of row dtau(g, c / 4), granule c % 4 of a K tile
+  const int cr = dtau(g, c >> 2);
+  const unsigned col_off = (unsigned)(cr * D + 8 * ((c & 3) ^ swizzle<D>(cr))) * 2u;
+  // row token_row(0, 4 g), columns dv of the V tile
+  const unsigned v_off = (unsigned)(lt * D + 8 * ((dv / 8) ^ swizzle<D>(lt)) + dv % 8) * 2u + C::kOffV;
+  if (n > 0) {
+    lds_barrier();
+    lds_barrier();
+  }
+  for (int j = 0; j < n; ++j) {
+    const int count = j == n - 1 ? last : kChunk;
+    lds_barrier();
+    const uint16_t* const kt = k_tile(j);
+    const uint16_t* const qt = q_tile(j);
+    const float* const rows = row_factors(j);
+    if (MODE == kKeep) {
+      char* const mo = (char*)(sa.m_out + ((int64_t)(sg.x + j) * a.heads + h) * dd);
+      const unsigned m_off = (unsigned)(8 * g * D + dv) * 4u;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *(f32x2*)(mo + dim_row(mt, r) * D * 4 + m_off) = f32x2{m[mt][0][r], m[mt][1][r]};
+    }
+    // K M and Q M.  Operands are read during the products before theirs, products of
+    // one order go over all results in turn, and meanwhile the next step's part of M
+    // is split.
+    f32x4 km[4][2], qm[4][2];
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) km[it][ct] = qm[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+    unsigned ko = row_off + (unsigned)((const unsigned char*)kt - smem);
+    unsigned qo = row_off + (unsigned)((const unsigned char*)qt - smem);
+    unsigned co = col_off + (unsigned)((const unsigned char*)kt - smem), vo = v_off, lo = 16u * lane;
+    pin(ko);
+    pin(qo);
+    pin(co);
+    pin(vo);
+    pin(lo);
+    // rows of tile `it` at step s: the swizzle's high bits and s meet in bits of their own
+    auto row_at = [&](unsigned off, int it, int s) {
+      return *(const bf16x8*)(smem + ((off ^ (64u * s)) + (unsigned)token_row(it, 0) * D * 2));
+    };
+    bf16x8 kf[4], qf[4];
+    Parts<3> b[2], bn[2];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) kf[it] = row_at(ko, it, 0);
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(m[0][ct], m[1][ct]);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if (C::Q) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) qf[it] = row_at(qo, it, s);
+      }
+#pragma unroll
+      for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int ct = 0; ct < 2; ++ct) km[it][ct] = mfma_bf16(kf[it], b[ct].p[p], km[it][ct]);
+      if (s + 1 < KS) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) kf[it] = row_at(ko, it, s + 1);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) bn[ct] = split_tiles<3>(m[2 * s + 2][ct], m[2 * s + 3][ct]);
+      }
+      if (C::Q) {
+#pragma unroll
+        for (int h2 = 0; h2 < 4; h2 += 2)
+#pragma unroll
+          for (int p = 1; p >= 0; --p)
+#pragma unroll
+            for (int it = h2; it < h2 + 2; ++it)
+#pragma unroll
+              for (int ct = 0; ct < 2; ++ct) qm[it][ct] = mfma_bf16(qf[it], b[ct].p[p], qm[it][ct]);
+      }
+      if (s + 1 < KS) {
+        weave<8, 2>();
+        if (C::Q) weave_reads<2>();
+        weave<8, 2>();
+        if (C::Q) weave_reads<2>();
+        weave<8, 2>();
+        weave_reads<2>();
+        if (C::Q) weave<8, 3>();
+        weave_reads<2>();
+        if (C::Q) weave<8, 3>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) b[ct] = bn[ct];
+    }
+    // X = beta o (V - gam o K M), in km; O's first part
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int t0 = token_row(it, 4 * g);
+      const f32x4 gm = *(const f32x4*)(rows + t0), be = *(const f32x4*)(rows + 2 * kChunk + t0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        unsigned v = 0u;
+        if (!unit)
+          v = *(const unsigned*)(smem + ((vo ^ (64u * (D == 128 ? r : r >> 1))) + (token_row(it, r) * D * 2)));
+        km[it][0][r] = be[r] * fmaf(-gm[r], km[it][0][r], bf16lo(v));
+        km[it][1][r] = be[r] * fmaf(-gm[r], km[it][1][r], bf16hi(v));
+        if (C::Q) {
+          qm[it][0][r] *= a.scale * gm[r];
+          qm[it][1][r] *= a.scale * gm[r];
+        }
+      }
+    }
+    lds_barrier();
+    // U = T X
+    f32x4 u[4][2];
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) u[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      Parts<3> b[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(km[2 * ts][ct], km[2 * ts + 1][ct]);
+      bf16x8 ta[3][4];
+#pragma unroll
+      for (int k = 2; k >= 0; --k)
+#pragma unroll
+        for (int it = 2 * ts; it < 4; ++it)
+          ta[k][it] = *(const bf16x8*)(smem + C::kOffT + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
+#pragma unroll
+      for (int o = 2; o >= 0; --o)
+#pragma unroll
+        for (int p = o; p >= 0; --p)
+#pragma unroll
+          for (int it = 2 * ts; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) u[it][ct] = mfma_bf16(ta[p][it], b[ct].p[o - p], u[it][ct]);
+    }
+    lds_barrier();
+    if (MODE == kKeep) {
+      char* const uo = (char*)(sa.u_out + ((tok0 + (int64_t)kChunk * j) * a.heads + h) * D);
+      const unsigned u_off = (unsigned)(lt * a.heads * D + dv) * 4u;
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = token_row(it, r);
+          char* const at = uo + (int64_t)t * a.heads * D * 4;
+          if (lt + t < count) *(f32x2*)(at + u_off) = f32x2{u[it][0][r], u[it][1][r]};
+        }
+    }
+    if (C::Q) {
+      // O = scale gam o (Q M) + P U
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+        Parts<2> b[2];
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<2>(u[2 * ts][ct], u[2 * ts + 1][ct]);
+        bf16x8 pa[2][4];
+#pragma unroll
+        for (int k = 1; k >= 0; --k)
+#pragma unroll
+          for (int it = 2 * ts; it < 4; ++it)
+            pa[k][it] = *(const bf16x8*)(smem + C::kOffP + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
+#pragma unroll
+        for (int o = 1; o >= 0; --o)
+#pragma unroll
+          for (int p = o; p >= 0; --p)
+#pragma unroll
+            for (int it = 2 * ts; it < 4; ++it)
+#pragma unroll
+              for (int ct = 0; ct < 2; ++ct) qm[it][ct] = mfma_bf16(pa[p][it], b[ct].p[o - p], qm[it][ct]);
+      }
+    }
+    // M <- gam_C M + K^T (dec o U)
+    const float gl = rows[kChunk - 1];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[mt][ct][r] *= gl;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const f32x4 de = *(const f32x4*)(rows + kChunk + token_row(it, 4 * g));
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[it][ct][r] *= de[r];
+    }
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+      Parts<3> b[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(u[2 * ts][ct], u[2 * ts + 1][ct]);
+#pragma unroll
+      for (int m0 = 0; m0 < MT; m0 += 4) {
+        bf16x8 ka[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned at = (co ^ (64u * ((m0 + i) >> 1))) + (32 * ts * D + 4 * (i & 1)) * 2;
+          // 8 rows on: the same swizzle
+          ka[i] = __builtin_shufflevector(delta_read_tr((const uint16_t*)(smem + at)),
+                                          delta_read_tr((const uint16_t*)(smem + at + 8 * D * 2)), 0, 1, 2, 3, 4,
+                                          5, 6, 7);
+        }
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) m[m0 + i][ct] = mfma_bf16(ka[i], b[ct].p[p], m[m0 + i][ct]);
+      }
+    }
+    if (C::Q) {
+      char* const at = op + (int64_t)kChunk * j * sa.ld_o * 2;
+      unsigned off = o_off, first = lt;
+      pin(off);
+      pin(first);
+      if (count == kChunk) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            *(unsigned*)(at + token_row(it, r) * sa.ld_o * 2 + off) =
+                pack_bf16x2(qm[it][0][r], qm[it][1][r]);
+      } else {
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if ((int)first + token_row(it, r) < count)
+              *(unsigned*)(at + token_row(it, r) * sa.ld_o * 2 + off) =
+                  pack_bf16x2(qm[it][0][r], qm[it][1][r]);
+      }
+    }
+  }
+
+  float* out = nullptr;
+  if (MODE == kTransition)
+    out = sa.trans + ((int64_t)si * a.heads + h) * (sa.both ? 3 : 2) * dd + (unit ? 2 : 1) * dd;
+  if (unit) {  // N by rows for the join, and by columns for the one on the way back
+    if (sa.both) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+          *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+    }
+    out -= 2 * dd;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *(f32x2*)(out + (int64_t)dim_row(mt, 4 * g + r) * D + dv) = f32x2{m[mt][0][r], m[mt][1][r]};
+    return;
+  }
+  if (MODE != kTransition && (sg.w & 2) && sa.state_out)
+    out = sa.state_out + ((int64_t)sg.z * a.heads + h) * dd;
+  if (out) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+        *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+  }
+}
+
+template <int D>
+hipError_t fused_any(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st) {
+  const int64_t blocks = (int64_t)a.sq.n_segs * a.heads;
+  const dim3 blk(64 * (D / 32 + 4));
+  if (s.trans)
+    hipLaunchKernelGGL((k_delta_fused<D, kTransition>), dim3((unsigned)(2 * blocks)), blk, 0, st, a, s);
+  else if (s.m_out)
+    hipLaunchKernelGGL((k_delta_fused<D, kKeep>), dim3((unsigned)blocks), blk, 0, st, a, s);
+  else
+    hipLaunchKernelGGL((k_delta_fused<D, kOutputs>), dim3((unsigned)blocks), blk, 0, st, a, s);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_fused(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st) {
+  return a.d == 128 ? fused_any<128>(a, s, st) : fused_any<64>(a, s, st);
+}
+
+}  // namespace zm

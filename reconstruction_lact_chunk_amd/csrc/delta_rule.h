@@ -245,7 +245,10 @@ struct DeltaGradArgs {
 hipError_t launch_delta_table(const DeltaSeqs& s, hipStream_t st);
 // T and P (backward: T, T^T, P^T) and the row factors of every chunk and head.
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t st);
+// fp32 tokens: the chunks in order from the tiles of launch_delta_prep; bf16 tokens:
+// the same with the triangles formed on the way (no tiles needed).
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st);
+hipError_t launch_delta_fused(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st);
 // The states at the segments' starts (gradients at their ends) from their transitions.
 hipError_t launch_delta_join(const DeltaArgs& a, const DeltaJoinArgs& j, hipStream_t st);
 // Backward through the chunks of each segment, last first: d_m, x, dv, dstate_in.
