@@ -1,9 +1,8 @@
 // The chunks of a segment in order for bf16 tokens (delta_rule.h), one workgroup per
 // (segment, head) with two kinds of waves:
-//   D / 32 state waves: 32 columns of M (d_v) each and all its rows.  M, R and U stay
+//   D / 16 state waves: 16 columns of M (d_v) each and all its rows.  M, R and U stay
 //     in registers: each is the result of one product and the right operand of
-//     the next.  Columns 2 c and 2 c + 1 belong to lane c's two column tiles, so
-//     tokens go in and out as pairs.
+//     the next.
 //   4 triangle waves, one chunk ahead: T = (I + A)^-1 and P by blocks of 16, wave i the
 //     block row i, left in LDS as operand tiles for the state waves.  They also
 //     start the direct loads of K and Q two chunks ahead.
@@ -31,7 +30,7 @@ struct Const {
 
 template <int D, int MODE>
 struct FusedCfg {
-  static constexpr int SW = D / 32;             // state waves
+  static constexpr int SW = D / 16;             // state waves
   static constexpr int TW = 4;                  // triangle waves
   static constexpr int THREADS = 64 * (SW + TW);
   static constexpr int GPR = D / 8;             // 16-byte granules of a row
@@ -65,23 +64,6 @@ template <int D>
 __device__ __forceinline__ Parts<1> tile_row(const uint16_t* t, int row, int granule) {
   return Parts<1>{{*(const bf16x8*)(t + row * D + 8 * (granule ^ swizzle<D>(row)))}};
 }
-// What one wave issues is in order, and a matrix instruction leaves room for two or
-// three others while it runs: these place `v` vector operations after each of `n`
-// matrix instructions, and keep the steps of a pipelined loop apart, which also
-// bounds what is in flight to the registers there are.
-template <int N, int V>
-__device__ __forceinline__ void weave() {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
-    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);  // vector
-  }
-}
-template <int N>
-__device__ __forceinline__ void weave_reads() {
-  __builtin_amdgcn_sched_group_barrier(0x100, N, 0);  // LDS reads
-}
-
 // LDS reads and writes of this wave are done, then the workgroup's barrier.  Loads
 // and stores of global memory stay in flight.
 __device__ __forceinline__ void lds_barrier() {
@@ -93,19 +75,15 @@ __device__ __forceinline__ void lds_barrier() {
 __device__ __forceinline__ void wait_direct_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
 
 template <int D, int MODE>
-__global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, DeltaScanArgs sa) {
+__global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, DeltaScanArgs sa) {
   using C = FusedCfg<D, MODE>;
   constexpr int KS = D / 32, MT = D / 16;
   __shared__ __attribute__((aligned(16))) unsigned char smem[C::BYTES];
-  int blk = blockIdx.x;
-  const int h = blk % a.heads;
-  blk /= a.heads;
-  const bool unit = MODE == kTransition && (blk & 1);
-  const int si = MODE == kTransition ? blk >> 1 : blk;
+  const int h = blockIdx.x % a.heads, si = blockIdx.x / a.heads;
   const int4 sg = delta_seg(a.sq, si);
   if (sg.y < 0) return;
   // nothing follows the last segment; its N serves the way back
-  if (MODE == kTransition && (sg.w & 2) && !(unit && sa.both)) return;
+  if (MODE == kTransition && (sg.w & 2) && !sa.both) return;
   const int n = sg.y;
   const int hk = h / (a.heads / a.heads_k);
   int64_t tok0 = 0;
@@ -141,24 +119,48 @@ __global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, 
 
       // Rows past the chunk's tokens take the last one's: finite where that is, and
       // their beta of zero leaves them out.
-      auto load_tile = [&](const uint16_t* src, int64_t ld, uint16_t* dst, int j) {
-        const int top = (j == n - 1 ? last : kChunk) - 1;
-        constexpr int RPL = 64 / C::GPR, LOADS = kChunk / RPL / C::TW;  // rows of a load; loads of a wave
+      // A lane's place in a load is a 32-bit offset from the load's first row, one of
+      // two as the swizzle takes bit 4 of the row.
+      constexpr int RPL = 64 / C::GPR, LOADS = kChunk / RPL / C::TW;  // rows of a load; loads of a wave
+      const int lr = lane / C::GPR;
+      struct Source {
+        const char* base;
+        int64_t ld;       // bytes
+        unsigned off[2];
+      };
+      auto source = [&](const uint16_t* p, int64_t ld) {
+        Source r{(const char*)p, ld * 2, {0u, 0u}};
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-          const int r0 = (PW * LOADS + i) * RPL, r = r0 + lane / C::GPR;
-          const int64_t row = (int64_t)kChunk * j + (r < top ? r : top);
-          const int col = 8 * ((lane % C::GPR) ^ swizzle<D>(r));
-          __builtin_amdgcn_global_load_lds((const void*)(src + row * ld + col), (lds_void*)(dst + r0 * D), 16, 0, 0);
+        for (int i = 0; i < 2; ++i)
+          r.off[i] = (unsigned)(lr * ld + 8 * ((lane % C::GPR) ^ swizzle<D>(lr + 16 * i))) * 2u;
+        return r;
+      };
+      auto load_tile = [&](const Source& s, uint16_t* dst, int j) {
+        if (j < n - 1 || last == kChunk) {
+#pragma unroll
+          for (int i = 0; i < LOADS; ++i) {
+            const int r0 = (PW * LOADS + i) * RPL;
+            const char* const from = s.base + ((int64_t)kChunk * j + r0) * s.ld;
+            __builtin_amdgcn_global_load_lds((const void*)(from + s.off[(r0 >> 4) & 1]), (lds_void*)(dst + r0 * D), 16,
+                                             0, 0);
+          }
+        } else {
+          const int top = last - 1;
+#pragma unroll 1
+          for (int i = 0; i < LOADS; ++i) {
+            const int r0 = (PW * LOADS + i) * RPL, r = r0 + lr;
+            const char* const from = s.base + ((int64_t)kChunk * j + (r < top ? r : top)) * s.ld;
+            const int col = 8 * ((lane % C::GPR) ^ swizzle<D>(r));
+            __builtin_amdgcn_global_load_lds((const void*)(from + 2 * col), (lds_void*)(dst + r0 * D), 16, 0, 0);
+          }
         }
       };
-      auto load_k = [&](int j) { load_tile(kp, a.k.ld, k_tile(j), j); };
+      const Source ks = source(kp, a.k.ld), qs = C::Q ? source(qp, a.q.ld) : ks, vs = source(vp, a.v.ld);
+      auto load_k = [&](int j) { load_tile(ks, k_tile(j), j); };
       auto load_q = [&](int j) {
-        if (C::Q) load_tile(qp, a.q.ld, q_tile(j), j);
+        if (C::Q) load_tile(qs, q_tile(j), j);
       };
-      auto load_v = [&](int j) {
-        if (!unit) load_tile(vp, a.v.ld, vt, j);
-      };
+      auto load_v = [&](int j) { load_tile(vs, vt, j); };
       float gn = 0.f, bn = 0.f;
       auto load_gates = [&](int j) {
         gn = bn = 0.f;
@@ -325,6 +327,7 @@ __global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, 
         }
       };
 
+      __builtin_amdgcn_s_setprio(2);
       load_gates(0);
       load_k(0);
       load_q(0);
@@ -369,26 +372,23 @@ __global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, 
   }
 
   // ---- state waves ---------------------------------------------------------------
-  const int dv = 32 * wave + 2 * c;  // of the lane's pair of columns
-  f32x4 m[MT][2];
+  const int dv = 16 * wave + c;  // the lane's column
   const int64_t dd = (int64_t)D * D;
+  f32x4 m[MT], e[MODE == kTransition ? MT : 1];  // M; the second run of a transition's
   const float* init = nullptr;
   if (MODE != kTransition) {
     if (sa.seg_start) init = sa.seg_start + ((int64_t)si * a.heads + h) * dd;
     else if (sa.state_in) init = sa.state_in + ((int64_t)sg.z * a.heads + h) * dd;
   }
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < MT; ++mt) {
+    const int dk = dim_row(mt, 4 * g);
+    m[mt] = init ? *(const f32x4*)(init + (int64_t)dv * D + dk) : f32x4{0.f, 0.f, 0.f, 0.f};
+    if (MODE == kTransition) {
 #pragma unroll
-    for (int ct = 0; ct < 2; ++ct) {
-      const int dk = dim_row(mt, 4 * g);
-      if (init) {
-        m[mt][ct] = *(const f32x4*)(init + (int64_t)(dv + ct) * D + dk);
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[mt][ct][r] = unit && dk + r == dv + ct ? 1.f : 0.f;
-      }
+      for (int r = 0; r < 4; ++r) e[mt][r] = dk + r == dv ? 1.f : 0.f;
     }
+  }
   // Token token_row(it, 4 g + r) is the lane's first one and a uniform number of
   // rows on, so addresses are a scalar base and one 32-bit offset a lane.
   const int lt = token_row(0, 4 * g);
@@ -402,38 +402,19 @@ __global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, 
   // the transposing read of row dtau(g, c / 4), granule c % 4 of a K tile
   const int cr = dtau(g, c >> 2);
   const unsigned col_off = (unsigned)(cr * D + 8 * ((c & 3) ^ swizzle<D>(cr))) * 2u;
-  // row token_row(0, 4 g), columns dv of the V tile
+  // row token_row(0, 4 g), column dv of the V tile
   const unsigned v_off = (unsigned)(lt * D + 8 * ((dv / 8) ^ swizzle<D>(lt)) + dv % 8) * 2u + C::kOffV;
+
   if (n > 0) {
     lds_barrier();
     lds_barrier();
   }
   for (int j = 0; j < n; ++j) {
     const int count = j == n - 1 ? last : kChunk;
-    lds_barrier();
-    const uint16_t* const kt = k_tile(j);
-    const uint16_t* const qt = q_tile(j);
     const float* const rows = row_factors(j);
-    if (MODE == kKeep) {
-      char* const mo = (char*)(sa.m_out + ((int64_t)(sg.x + j) * a.heads + h) * dd);
-      const unsigned m_off = (unsigned)(8 * g * D + dv) * 4u;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          *(f32x2*)(mo + dim_row(mt, r) * D * 4 + m_off) = f32x2{m[mt][0][r], m[mt][1][r]};
-    }
-    // K M and Q M.  Operands are read during the products before theirs, products of
-    // one order go over all results in turn, and meanwhile the next step's part of M
-    // is split.
-    f32x4 km[4][2], qm[4][2];
-#pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct) km[it][ct] = qm[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-    unsigned ko = row_off + (unsigned)((const unsigned char*)kt - smem);
-    unsigned qo = row_off + (unsigned)((const unsigned char*)qt - smem);
-    unsigned co = col_off + (unsigned)((const unsigned char*)kt - smem), vo = v_off, lo = 16u * lane;
+    unsigned ko = row_off + (unsigned)((const unsigned char*)k_tile(j) - smem);
+    unsigned qo = row_off + (unsigned)((const unsigned char*)q_tile(j) - smem);
+    unsigned co = col_off + (unsigned)((const unsigned char*)k_tile(j) - smem), vo = v_off, lo = 16u * lane;
     pin(ko);
     pin(qo);
     pin(co);
@@ -443,101 +424,159 @@ __global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, 
     auto row_at = [&](unsigned off, int it, int s) {
       return *(const bf16x8*)(smem + ((off ^ (64u * s)) + (unsigned)token_row(it, 0) * D * 2));
     };
-    bf16x8 kf[4], qf[4];
-    Parts<3> b[2], bn[2];
+    // K M and Q M, the products of one order over all results in turn
+    f32x4 km[4], qm[4];
+    auto read_m = [&](const f32x4* mm, bool with_q) {
 #pragma unroll
-    for (int it = 0; it < 4; ++it) kf[it] = row_at(ko, it, 0);
-#pragma unroll
-    for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(m[0][ct], m[1][ct]);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      if (C::Q) {
-#pragma unroll
-        for (int it = 0; it < 4; ++it) qf[it] = row_at(qo, it, s);
+      for (int it = 0; it < 4; ++it) {
+        km[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (with_q) qm[it] = km[it];
       }
 #pragma unroll
-      for (int p = 2; p >= 0; --p)
+      for (int s = 0; s < KS; ++s) {
+        const Parts<3> b = split_tiles<3>(mm[2 * s], mm[2 * s + 1]);
+        bf16x8 kf[4], qf[4];
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
+        for (int it = 0; it < 4; ++it) kf[it] = row_at(ko, it, s);
+        if (with_q) {
 #pragma unroll
-          for (int ct = 0; ct < 2; ++ct) km[it][ct] = mfma_bf16(kf[it], b[ct].p[p], km[it][ct]);
-      if (s + 1 < KS) {
+          for (int it = 0; it < 4; ++it) qf[it] = row_at(qo, it, s);
+        }
 #pragma unroll
-        for (int it = 0; it < 4; ++it) kf[it] = row_at(ko, it, s + 1);
+        for (int p = 2; p >= 0; --p)
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) bn[ct] = split_tiles<3>(m[2 * s + 2][ct], m[2 * s + 3][ct]);
-      }
-      if (C::Q) {
-#pragma unroll
-        for (int h2 = 0; h2 < 4; h2 += 2)
+          for (int it = 0; it < 4; ++it) km[it] = mfma_bf16(kf[it], b.p[p], km[it]);
+        if (with_q) {
 #pragma unroll
           for (int p = 1; p >= 0; --p)
 #pragma unroll
-            for (int it = h2; it < h2 + 2; ++it)
-#pragma unroll
-              for (int ct = 0; ct < 2; ++ct) qm[it][ct] = mfma_bf16(qf[it], b[ct].p[p], qm[it][ct]);
+            for (int it = 0; it < 4; ++it) qm[it] = mfma_bf16(qf[it], b.p[p], qm[it]);
+        }
+        // two runs' states leave no room for more than a step in flight
+        if (MODE == kTransition) __builtin_amdgcn_sched_barrier(0);
       }
-      if (s + 1 < KS) {
-        weave<8, 2>();
-        if (C::Q) weave_reads<2>();
-        weave<8, 2>();
-        if (C::Q) weave_reads<2>();
-        weave<8, 2>();
-        weave_reads<2>();
-        if (C::Q) weave<8, 3>();
-        weave_reads<2>();
-        if (C::Q) weave<8, 3>();
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    };
+    // X = beta o (V - gam o K M), in km
+    auto form_x = [&](bool with_v) {
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct) b[ct] = bn[ct];
-    }
-    // X = beta o (V - gam o K M), in km; O's first part
+      for (int it = 0; it < 4; ++it) {
+        const int t0 = token_row(it, 4 * g);
+        const f32x4 gm = *(const f32x4*)(rows + t0), be = *(const f32x4*)(rows + 2 * kChunk + t0);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int t0 = token_row(it, 4 * g);
-      const f32x4 gm = *(const f32x4*)(rows + t0), be = *(const f32x4*)(rows + 2 * kChunk + t0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        unsigned v = 0u;
-        if (!unit)
-          v = *(const unsigned*)(smem + ((vo ^ (64u * (D == 128 ? r : r >> 1))) + (token_row(it, r) * D * 2)));
-        km[it][0][r] = be[r] * fmaf(-gm[r], km[it][0][r], bf16lo(v));
-        km[it][1][r] = be[r] * fmaf(-gm[r], km[it][1][r], bf16hi(v));
-        if (C::Q) {
-          qm[it][0][r] *= a.scale * gm[r];
-          qm[it][1][r] *= a.scale * gm[r];
+        for (int r = 0; r < 4; ++r) {
+          float v = 0.f;
+          if (with_v)
+            v = __uint_as_float((unsigned)*(const uint16_t*)(smem + ((vo ^ (64u * (D == 128 ? r : r >> 1))) +
+                                                                    (token_row(it, r) * D * 2)))
+                                << 16);
+          km[it][r] = be[r] * fmaf(-gm[r], km[it][r], v);
         }
       }
-    }
-    lds_barrier();
-    // U = T X
-    f32x4 u[4][2];
+    };
+    // U = T X, part by part of T
+    f32x4 u[4];
+    auto apply_t = [&]() {
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+      for (int it = 0; it < 4; ++it) u[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct) u[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int ts = 0; ts < 2; ++ts) {
+        const Parts<3> b = split_tiles<3>(km[2 * ts], km[2 * ts + 1]);
 #pragma unroll
-    for (int ts = 0; ts < 2; ++ts) {
-      Parts<3> b[2];
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(km[2 * ts][ct], km[2 * ts + 1][ct]);
-      bf16x8 ta[3][4];
-#pragma unroll
-      for (int k = 2; k >= 0; --k)
-#pragma unroll
-        for (int it = 2 * ts; it < 4; ++it)
-          ta[k][it] = *(const bf16x8*)(smem + C::kOffT + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
-#pragma unroll
-      for (int o = 2; o >= 0; --o)
-#pragma unroll
-        for (int p = o; p >= 0; --p)
+        for (int k = 2; k >= 0; --k) {
+          bf16x8 f[4];
 #pragma unroll
           for (int it = 2 * ts; it < 4; ++it)
+            f[it] = *(const bf16x8*)(smem + C::kOffT + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) u[it][ct] = mfma_bf16(ta[p][it], b[ct].p[o - p], u[it][ct]);
-    }
+          for (int p = 2 - k; p >= 0; --p)
+#pragma unroll
+            for (int it = 2 * ts; it < 4; ++it) u[it] = mfma_bf16(f[it], b.p[p], u[it]);
+        }
+      }
+    };
+    // O = scale gam o (Q M) + P U
+    auto outputs = [&]() {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const f32x4 gm = *(const f32x4*)(rows + token_row(it, 4 * g));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) qm[it][r] *= a.scale * gm[r];
+      }
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+        const Parts<2> b = split_tiles<2>(u[2 * ts], u[2 * ts + 1]);
+        bf16x8 f[2][4];
+#pragma unroll
+        for (int k = 1; k >= 0; --k)
+#pragma unroll
+          for (int it = 2 * ts; it < 4; ++it)
+            f[k][it] = *(const bf16x8*)(smem + C::kOffP + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
+#pragma unroll
+        for (int o = 1; o >= 0; --o)
+#pragma unroll
+          for (int p = o; p >= 0; --p)
+#pragma unroll
+            for (int it = 2 * ts; it < 4; ++it) qm[it] = mfma_bf16(f[p][it], b.p[o - p], qm[it]);
+      }
+    };
+    // M <- gam_C M + K^T (dec o U), a half of the chunk's tokens at a time
+    auto decay = [&](f32x4* mm) {
+      const float gl = rows[kChunk - 1];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mm[mt][r] *= gl;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const f32x4 de = *(const f32x4*)(rows + kChunk + token_row(it, 4 * g));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[it][r] *= de[r];
+      }
+    };
+    auto advance = [&](f32x4* mm, int ts) {
+      const Parts<3> b = split_tiles<3>(u[2 * ts], u[2 * ts + 1]);
+#pragma unroll
+      for (int m0 = 0; m0 < MT; m0 += 4) {
+        bf16x8 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned at = (co ^ (64u * ((m0 + i) >> 1))) + (32 * ts * D + 4 * (i & 1)) * 2;
+          // 8 rows on: the same swizzle
+          f[i] = __builtin_shufflevector(delta_read_tr((const uint16_t*)(smem + at)),
+                                         delta_read_tr((const uint16_t*)(smem + at + 8 * D * 2)), 0, 1, 2, 3, 4, 5, 6,
+                                         7);
+        }
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mm[m0 + i] = mfma_bf16(f[i], b.p[p], mm[m0 + i]);
+      }
+    };
+
     lds_barrier();
+    if (MODE == kKeep) {
+      char* const mo = (char*)(sa.m_out + ((int64_t)(sg.x + j) * a.heads + h) * dd);
+      const unsigned m_off = (unsigned)(8 * g * D + dv) * 4u;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) *(float*)(mo + dim_row(mt, r) * D * 4 + m_off) = m[mt][r];
+    }
+    read_m(m, C::Q);
+    form_x(true);
+    apply_t();
+    lds_barrier();
+    if (MODE == kTransition) {
+      decay(m);
+      advance(m, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      advance(m, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      read_m(e, false);
+      form_x(false);
+      apply_t();
+      lds_barrier();
+    }
     if (MODE == kKeep) {
       char* const uo = (char*)(sa.u_out + ((tok0 + (int64_t)kChunk * j) * a.heads + h) * D);
       const unsigned u_off = (unsigned)(lt * a.heads * D + dv) * 4u;
@@ -547,73 +586,15 @@ __global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, 
         for (int r = 0; r < 4; ++r) {
           const int t = token_row(it, r);
           char* const at = uo + (int64_t)t * a.heads * D * 4;
-          if (lt + t < count) *(f32x2*)(at + u_off) = f32x2{u[it][0][r], u[it][1][r]};
+          if (lt + t < count) *(float*)(at + u_off) = u[it][r];
         }
     }
-    if (C::Q) {
-      // O = scale gam o (Q M) + P U
-#pragma unroll
-      for (int ts = 0; ts < 2; ++ts) {
-        Parts<2> b[2];
-#pragma unroll
-        for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<2>(u[2 * ts][ct], u[2 * ts + 1][ct]);
-        bf16x8 pa[2][4];
-#pragma unroll
-        for (int k = 1; k >= 0; --k)
-#pragma unroll
-          for (int it = 2 * ts; it < 4; ++it)
-            pa[k][it] = *(const bf16x8*)(smem + C::kOffP + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
-#pragma unroll
-        for (int o = 1; o >= 0; --o)
-#pragma unroll
-          for (int p = o; p >= 0; --p)
-#pragma unroll
-            for (int it = 2 * ts; it < 4; ++it)
-#pragma unroll
-              for (int ct = 0; ct < 2; ++ct) qm[it][ct] = mfma_bf16(pa[p][it], b[ct].p[o - p], qm[it][ct]);
-      }
-    }
-    // M <- gam_C M + K^T (dec o U)
-    const float gl = rows[kChunk - 1];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[mt][ct][r] *= gl;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const f32x4 de = *(const f32x4*)(rows + kChunk + token_row(it, 4 * g));
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) u[it][ct][r] *= de[r];
-    }
-#pragma unroll
-    for (int ts = 0; ts < 2; ++ts) {
-      Parts<3> b[2];
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(u[2 * ts][ct], u[2 * ts + 1][ct]);
-#pragma unroll
-      for (int m0 = 0; m0 < MT; m0 += 4) {
-        bf16x8 ka[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const unsigned at = (co ^ (64u * ((m0 + i) >> 1))) + (32 * ts * D + 4 * (i & 1)) * 2;
-          // 8 rows on: the same swizzle
-          ka[i] = __builtin_shufflevector(delta_read_tr((const uint16_t*)(smem + at)),
-                                          delta_read_tr((const uint16_t*)(smem + at + 8 * D * 2)), 0, 1, 2, 3, 4,
-                                          5, 6, 7);
-        }
-#pragma unroll
-        for (int p = 2; p >= 0; --p)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) m[m0 + i][ct] = mfma_bf16(ka[i], b[ct].p[p], m[m0 + i][ct]);
-      }
-    }
-    if (C::Q) {
+    if (MODE == kOutputs) outputs();
+    f32x4* const mm = MODE == kTransition ? e : m;
+    decay(mm);
+    advance(mm, 0);
+    if (MODE != kTransition) lds_barrier();
+    if (MODE == kOutputs) {
       char* const at = op + (int64_t)kChunk * j * sa.ld_o * 2;
       unsigned off = o_off, first = lt;
       pin(off);
@@ -623,60 +604,46 @@ __global__ __launch_bounds__(64 * (D / 32 + 4)) void k_delta_fused(DeltaArgs a, 
         for (int it = 0; it < 4; ++it)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            *(unsigned*)(at + token_row(it, r) * sa.ld_o * 2 + off) =
-                pack_bf16x2(qm[it][0][r], qm[it][1][r]);
+            *(uint16_t*)(at + token_row(it, r) * sa.ld_o * 2 + off) = to_bf16(qm[it][r]);
       } else {
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if ((int)first + token_row(it, r) < count)
-              *(unsigned*)(at + token_row(it, r) * sa.ld_o * 2 + off) =
-                  pack_bf16x2(qm[it][0][r], qm[it][1][r]);
+              *(uint16_t*)(at + token_row(it, r) * sa.ld_o * 2 + off) = to_bf16(qm[it][r]);
       }
     }
+    advance(mm, 1);
   }
 
-  float* out = nullptr;
-  if (MODE == kTransition)
-    out = sa.trans + ((int64_t)si * a.heads + h) * (sa.both ? 3 : 2) * dd + (unit ? 2 : 1) * dd;
-  if (unit) {  // N by rows for the join, and by columns for the one on the way back
-    if (sa.both) {
+  if (MODE == kTransition) {
+    float* const to = sa.trans + ((int64_t)si * a.heads + h) * (sa.both ? 3 : 2) * dd;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      const int dk = dim_row(mt, 4 * g);
+      // N by rows for the join, B as a state, and N by columns for the join on the way back
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct)
-          *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+      for (int r = 0; r < 4; ++r) to[(int64_t)(dk + r) * D + dv] = e[mt][r];
+      *(f32x4*)(to + dd + (int64_t)dv * D + dk) = m[mt];
+      if (sa.both) *(f32x4*)(to + 2 * dd + (int64_t)dv * D + dk) = e[mt];
     }
-    out -= 2 * dd;
+  } else if ((sg.w & 2) && sa.state_out) {
+    float* const out = sa.state_out + ((int64_t)sg.z * a.heads + h) * dd + (int64_t)dv * D;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        *(f32x2*)(out + (int64_t)dim_row(mt, 4 * g + r) * D + dv) = f32x2{m[mt][0][r], m[mt][1][r]};
-    return;
-  }
-  if (MODE != kTransition && (sg.w & 2) && sa.state_out)
-    out = sa.state_out + ((int64_t)sg.z * a.heads + h) * dd;
-  if (out) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct)
-        *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+    for (int mt = 0; mt < MT; ++mt) *(f32x4*)(out + dim_row(mt, 4 * g)) = m[mt];
   }
 }
 
 template <int D>
 hipError_t fused_any(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st) {
-  const int64_t blocks = (int64_t)a.sq.n_segs * a.heads;
-  const dim3 blk(64 * (D / 32 + 4));
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(64 * (D / 16 + 4));
   if (s.trans)
-    hipLaunchKernelGGL((k_delta_fused<D, kTransition>), dim3((unsigned)(2 * blocks)), blk, 0, st, a, s);
+    hipLaunchKernelGGL((k_delta_fused<D, kTransition>), grid, blk, 0, st, a, s);
   else if (s.m_out)
-    hipLaunchKernelGGL((k_delta_fused<D, kKeep>), dim3((unsigned)blocks), blk, 0, st, a, s);
+    hipLaunchKernelGGL((k_delta_fused<D, kKeep>), grid, blk, 0, st, a, s);
   else
-    hipLaunchKernelGGL((k_delta_fused<D, kOutputs>), dim3((unsigned)blocks), blk, 0, st, a, s);
+    hipLaunchKernelGGL((k_delta_fused<D, kOutputs>), grid, blk, 0, st, a, s);
   return hipGetLastError();
 }
 
