@@ -42,12 +42,12 @@ DeltaPlan delta_plan(const zm_delta_desc* d, int64_t n) {
   p.n_chunks = (int)((n + (int64_t)(kChunk - 1) * d->n_seq) / kChunk);
   // One workgroup goes through a whole sequence of one head while these are
   // enough for half the compute units; with fewer, segments of at least
-  // kMinSegChunks chunks for two workgroups to each.
+  // kMinSegChunks chunks for one workgroup to each.
   constexpr int kMinSegChunks = 8;
   const int64_t units = (int64_t)d->n_seq * d->heads;
   int64_t seg = p.n_chunks > 0 ? p.n_chunks : 1;
   if (units < kTargetWgs / 2) {
-    seg = ceil_div((int64_t)p.n_chunks * d->heads, 2 * kTargetWgs);
+    seg = ceil_div((int64_t)p.n_chunks * d->heads, kTargetWgs);
     if (seg < kMinSegChunks) seg = kMinSegChunks;
   }
   p.seg_chunks = (int)seg;
@@ -161,7 +161,7 @@ BackwardWs backward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, co
 int check_counts(const zm_delta_desc* d, int64_t n) {
   if (n < 0 || n > kMaxDeltaTokens || (d->n_seq == 0 && n > 0)) return ZM_ERR_INVALID_ARG;
   const int64_t chunks = (n + (int64_t)(kChunk - 1) * d->n_seq) / kChunk;
-  // segments: at most one to a chunk and one to a sequence, a block for 16 columns each
+  // a block to each (chunk or segment, head), of 512 threads at most and the join's 8 a segment
   if ((chunks + d->n_seq) * d->heads * 2 > kMaxDeltaBlocks) return ZM_ERR_UNSUPPORTED;
   return ZM_OK;
 }

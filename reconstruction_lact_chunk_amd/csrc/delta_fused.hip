@@ -9,6 +9,14 @@
 // Nothing of a chunk but q, k, v, o moves through memory.  The state waves are bound
 // by their own issue (matrix instructions and the splitting of fp32 operands into
 // bf16 parts); the triangle waves run in the gaps.
+//
+// Decays are taken out where they can be.  With a running exponent s (the state is
+// 2^s M^) and U^ = U / 2^(s + c_i), c in powers of two,
+//   U^ = T^ (V / 2^(s + c_i) - K M^),  T^ = (I + strictly_lower(b_i k_i.k_j))^-1 diag(b),
+//   O = scale 2^(s + c_i) (Q M^ + lower(Q K^T) U^),  M^ <- M^ + K^T U^,  s <- s + c_C:
+// the same numbers up to powers of two, so nothing is lost while |s + c_i| stays
+// under kMaxShift.  A chunk that would leave that range takes 2^s into M^ first; one
+// whose own decay is over it (a reset) is formed with the decays in place.
 #include "delta_rule.h"
 
 namespace zm {
@@ -22,6 +30,12 @@ constexpr int kDPitch = 20;    // floats of a row of a diagonal block's inverse
 // K tiles in LDS: this chunk's, the next one's, the one in flight; Q's third takes the
 // place of the first, whose last reader is done before its load starts.
 constexpr int kRingK = 3, kRingQ = 2;
+constexpr float kMaxShift = 60.f;  // products of 2^60 and what a model holds stay finite
+// Row factors of a chunk in LDS: V's, O's, and those of a chunk formed with its decays,
+// then scalars.
+enum { kRowV = 0, kRowO = 64, kRowGam = 128, kRowDec = 192, kRowEnd = 256 };
+enum { kFlags = kRowEnd, kPre, kLast, kScale0, kScale1, kRowFloats = kRowEnd + 8 };
+enum { kGated = 1, kShift = 2 };
 
 template <int V>
 struct Const {
@@ -44,11 +58,12 @@ struct FusedCfg {
   static constexpr int kOffP = kOffT + 3 * TRI * 2;
   static constexpr int kOffV = kOffP + (Q ? 2 * TRI * 2 : 0);
   static constexpr int kOffRows = kOffV + TILE * 2;                    // two chunks' factors
-  static constexpr int kOffAt = kOffRows + 2 * 3 * kChunk * 4;
+  static constexpr int kOffAt = kOffRows + 2 * kRowFloats * 4;
   static constexpr int kOffD = kOffAt + kChunk * kAtPitch * 4;
   static constexpr int kOffDt = kOffD + 4 * 16 * kDPitch * 4;
   static constexpr int kOffCs = kOffDt + 4 * 16 * kDPitch * 4;
-  static constexpr int BYTES = kOffCs + TW * kChunk * 8;
+  static constexpr int kOffBe = kOffCs + TW * kChunk * 8;
+  static constexpr int BYTES = kOffBe + TW * kChunk * 4;
   static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
@@ -64,6 +79,22 @@ template <int D>
 __device__ __forceinline__ Parts<1> tile_row(const uint16_t* t, int row, int granule) {
   return Parts<1>{{*(const bf16x8*)(t + row * D + 8 * (granule ^ swizzle<D>(row)))}};
 }
+// What one wave issues is in order, and a matrix instruction leaves room for others
+// while it runs: these place V vector operations after each of N matrix
+// instructions, and LDS reads between such groups, ahead of their use.
+template <int N, int V>
+__device__ __forceinline__ void weave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);  // vector
+  }
+}
+template <int N>
+__device__ __forceinline__ void weave_reads() {
+  __builtin_amdgcn_sched_group_barrier(0x100, N, 0);  // LDS reads
+}
+
 // LDS reads and writes of this wave are done, then the workgroup's barrier.  Loads
 // and stores of global memory stay in flight.
 __device__ __forceinline__ void lds_barrier() {
@@ -97,7 +128,7 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
   uint16_t* const tf = (uint16_t*)(smem + C::kOffT);
   uint16_t* const pf = (uint16_t*)(smem + C::kOffP);
   uint16_t* const vt = (uint16_t*)(smem + C::kOffV);
-  auto row_factors = [&](int j) { return (float*)(smem + C::kOffRows) + (j & 1) * 3 * kChunk; };
+  auto row_factors = [&](int j) { return (float*)(smem + C::kOffRows) + (j & 1) * kRowFloats; };
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
 
   // the tiles' upper triangles stay zero
@@ -115,7 +146,10 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
     float* const dt = (float*)(smem + C::kOffDt);
     auto triangle = [&](auto which) {
       constexpr int PW = decltype(which)::value, PI = 3 - PW;
-      double* const cs = (double*)(smem + C::kOffCs) + PW * kChunk;
+      double* const cs = (double*)(smem + C::kOffCs) + PW * kChunk;  // the wave's own
+      float* const bs = (float*)(smem + C::kOffBe) + PW * kChunk;
+      double shift = 0.0;   // s, the same in every triangle wave
+      bool gated = false;   // of the chunk at hand
 
       // Rows past the chunk's tokens take the last one's: finite where that is, and
       // their beta of zero leaves them out.
@@ -184,12 +218,13 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
         if (j + 1 < n) load_gates(j + 1);
         Parts<1> ki[KS];
         tile(kt, PW, ki);
+        // sums in 64 bits: a strong decay among weak ones must not blur their differences
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
           const double o = __shfl_up(s, m, 64);
           if (lane >= m) s += o;
         }
-        cs[lane] = s;
+        bs[lane] = be;
         f32x4 kk[4];
 #pragma unroll
         for (int J = 0; J <= PW; ++J) {
@@ -199,29 +234,45 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
 #pragma unroll
           for (int k = 0; k < KS; ++k) mma<0>(kk[J], ki[k], J < PW ? kj[k] : ki[k]);
         }
+        // the chunk's form (a NaN decay keeps the decays in place)
+        gated = __any(!(fabsf((float)s) <= kMaxShift));
+        const bool move = gated ? shift != 0.0 : __any(!(fabsf((float)(shift + s)) <= kMaxShift));
+        const double from = shift, end = __shfl(s, 63, 64);
+        if (move) shift = 0.0;
         if (PW == 0) {
-          const double end = __shfl(s, 63, 64);
           float* const r = row_factors(j);
-          r[lane] = __builtin_amdgcn_exp2f((float)s);
-          r[kChunk + lane] = __builtin_amdgcn_exp2f((float)(end - s));
-          r[2 * kChunk + lane] = be;
+          const float at = (float)(shift + s);
+          const float up = __builtin_amdgcn_exp2f(at);
+          r[kRowV + lane] = gated ? 1.f : __builtin_amdgcn_exp2f(-at);
+          r[kRowO + lane] = gated ? 1.f : C::Q ? a.scale * up : up;
+          if (gated) {
+            r[kRowGam + lane] = up;
+            r[kRowDec + lane] = __builtin_amdgcn_exp2f((float)(end - s));
+          }
+          if (lane == 0) {
+            ((unsigned*)r)[kFlags] = (gated ? kGated : 0) | (move ? kShift : 0);
+            r[kPre] = __builtin_amdgcn_exp2f((float)from);
+            r[kLast] = __builtin_amdgcn_exp2f((float)end);
+            r[kScale0] = __builtin_amdgcn_exp2f((float)shift);
+            r[kScale1] = gated ? 1.f : __builtin_amdgcn_exp2f((float)(shift + end));
+          }
         }
-        double ci[4];
-        float bi[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          ci[r] = cs[16 * PW + 4 * g + r];
-          bi[r] = __shfl(be, 16 * PW + 4 * g + r, 64);
-        }
+        if (gated) cs[lane] = s;
+        else shift += end;
+        const f32x4 bi = *(const f32x4*)(bs + 16 * PW + 4 * g);
 #pragma unroll
         for (int J = PW; J >= 0; --J) {
-          const double cj = cs[16 * J + c];
           f32x4 av;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            // above the diagonal the exponent may be positive: not taken
-            const float e = __builtin_amdgcn_exp2f((float)(ci[r] - cj));
-            av[r] = J < PW || 4 * g + r > c ? bi[r] * e * kk[J][r] : 0.f;
+          for (int r = 0; r < 4; ++r) av[r] = J < PW || 4 * g + r > c ? bi[r] * kk[J][r] : 0.f;
+          if (gated) {
+            const double cj = cs[16 * J + c];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              // above the diagonal the exponent may be positive: not taken
+              const float e = __builtin_amdgcn_exp2f((float)(cs[16 * PW + 4 * g + r] - cj));
+              if (J < PW || 4 * g + r > c) av[r] *= e;
+            }
           }
           *(f32x4*)(at + (16 * J + c) * kAtPitch + 16 * PW + 4 * g) = av;
         }
@@ -296,22 +347,22 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
           r[3] -= bf16hi(w[1]);
         }
       };
+      // T diag(b)
       auto store_t = [&]() {
 #pragma unroll
-        for (int J = 0; J <= PW; ++J) store_tile(tf, PW, J, tt[J], 3);
+        for (int J = 0; J <= PW; ++J) store_tile(tf, PW, J, tt[J] * *(const f32x4*)(bs + 16 * J + 4 * g), 3);
       };
       auto store_p = [&]() {
         if (!C::Q) return;
 #pragma unroll
         for (int J = 0; J <= PI; ++J) store_tile(pf, PI, J, pt[J], 2);
       };
-      // Q K^T with its decays
+      // lower(Q K^T), or P with its decays
       auto scores = [&](int j) {
         if (!C::Q) return;
         const uint16_t* const kt = k_tile(j);
         Parts<1> qi[KS];
         tile(q_tile(j), PI, qi);
-        const double cp = cs[16 * PI + c];
 #pragma unroll
         for (int J = 0; J <= PI; ++J) {
           Parts<1> kj[KS];
@@ -320,9 +371,14 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
 #pragma unroll
           for (int k = 0; k < KS; ++k) mma<0>(p, kj[k], qi[k]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float e = __builtin_amdgcn_exp2f((float)(cp - cs[16 * J + 4 * g + r]));
-            pt[J][r] = J < PI || 4 * g + r <= c ? a.scale * e * p[r] : 0.f;
+          for (int r = 0; r < 4; ++r) pt[J][r] = J < PI || 4 * g + r <= c ? p[r] : 0.f;
+          if (gated) {
+            const double cp = cs[16 * PI + c];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float e = __builtin_amdgcn_exp2f((float)(cp - cs[16 * J + 4 * g + r]));
+              if (J < PI || 4 * g + r <= c) pt[J][r] *= a.scale * e;
+            }
           }
         }
       };
@@ -410,6 +466,7 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
     lds_barrier();
   }
   for (int j = 0; j < n; ++j) {
+    lds_barrier();
     const int count = j == n - 1 ? last : kChunk;
     const float* const rows = row_factors(j);
     unsigned ko = row_off + (unsigned)((const unsigned char*)k_tile(j) - smem);
@@ -424,20 +481,23 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
     auto row_at = [&](unsigned off, int it, int s) {
       return *(const bf16x8*)(smem + ((off ^ (64u * s)) + (unsigned)token_row(it, 0) * D * 2));
     };
-    // K M and Q M, the products of one order over all results in turn
+    const unsigned flags = __builtin_amdgcn_readfirstlane(((const unsigned*)rows)[kFlags]);
+    // K M and Q M, the products of one order over all results in turn; operands are
+    // read and M's next part is split during the step before theirs
     f32x4 km[4], qm[4];
     auto read_m = [&](const f32x4* mm, bool with_q) {
+      bf16x8 kf[4], qf[4];
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         km[it] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (with_q) qm[it] = km[it];
+        kf[it] = row_at(ko, it, 0);
       }
+      Parts<3> b = split_tiles<3>(mm[0], mm[1]);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const Parts<3> b = split_tiles<3>(mm[2 * s], mm[2 * s + 1]);
-        bf16x8 kf[4], qf[4];
-#pragma unroll
-        for (int it = 0; it < 4; ++it) kf[it] = row_at(ko, it, s);
+        const bool more = s + 1 < KS;
+        Parts<3> next = b;
         if (with_q) {
 #pragma unroll
           for (int it = 0; it < 4; ++it) qf[it] = row_at(qo, it, s);
@@ -446,121 +506,167 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int it = 0; it < 4; ++it) km[it] = mfma_bf16(kf[it], b.p[p], km[it]);
+        if (more) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it) kf[it] = row_at(ko, it, s + 1);
+          next = split_tiles<3>(mm[2 * s + 2], mm[2 * s + 3]);
+        }
         if (with_q) {
 #pragma unroll
           for (int p = 1; p >= 0; --p)
 #pragma unroll
             for (int it = 0; it < 4; ++it) qm[it] = mfma_bf16(qf[it], b.p[p], qm[it]);
         }
-        // two runs' states leave no room for more than a step in flight
-        if (MODE == kTransition) __builtin_amdgcn_sched_barrier(0);
+        if (with_q) weave_reads<4>();
+        weave<12, 2>();
+        if (more) weave_reads<4>();
+        if (with_q) weave<8, 3>();
+        __builtin_amdgcn_sched_barrier(0);
+        b = next;
       }
     };
-    // X = beta o (V - gam o K M), in km
+    // X = V o its factor - K M (with decays: gam o K M), in km
     auto form_x = [&](bool with_v) {
+      if (flags & kGated) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) km[it] *= *(const f32x4*)(rows + kRowGam + token_row(it, 4 * g));
+      }
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const int t0 = token_row(it, 4 * g);
-        const f32x4 gm = *(const f32x4*)(rows + t0), be = *(const f32x4*)(rows + 2 * kChunk + t0);
+        if (!with_v) {
+          km[it] = -km[it];
+          continue;
+        }
+        const f32x4 fv = *(const f32x4*)(rows + kRowV + token_row(it, 4 * g));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float v = 0.f;
-          if (with_v)
-            v = __uint_as_float((unsigned)*(const uint16_t*)(smem + ((vo ^ (64u * (D == 128 ? r : r >> 1))) +
-                                                                    (token_row(it, r) * D * 2)))
-                                << 16);
-          km[it][r] = be[r] * fmaf(-gm[r], km[it][r], v);
+          const float v =
+              __uint_as_float((unsigned)*(const uint16_t*)(smem + ((vo ^ (64u * (D == 128 ? r : r >> 1))) +
+                                                                  (token_row(it, r) * D * 2)))
+                              << 16);
+          km[it][r] = fmaf(v, fv[r], -km[it][r]);
         }
       }
     };
     // U = T X, part by part of T
     f32x4 u[4];
+    auto t_part = [&](int ts, int k, bf16x8* f) {
+#pragma unroll
+      for (int it = 2 * ts; it < 4; ++it)
+        f[it] = *(const bf16x8*)(smem + C::kOffT + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
+    };
     auto apply_t = [&]() {
+      bf16x8 fa[4], fb[4];
+      auto products = [&](int ts, int k, const bf16x8* f, const Parts<3>& x) {
+#pragma unroll
+        for (int p = 2 - k; p >= 0; --p)
+#pragma unroll
+          for (int it = 2 * ts; it < 4; ++it) u[it] = mfma_bf16(f[it], x.p[p], u[it]);
+      };
+      t_part(0, 2, fa);
+      t_part(0, 1, fb);
 #pragma unroll
       for (int it = 0; it < 4; ++it) u[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ts = 0; ts < 2; ++ts) {
-        const Parts<3> b = split_tiles<3>(km[2 * ts], km[2 * ts + 1]);
-#pragma unroll
-        for (int k = 2; k >= 0; --k) {
-          bf16x8 f[4];
-#pragma unroll
-          for (int it = 2 * ts; it < 4; ++it)
-            f[it] = *(const bf16x8*)(smem + C::kOffT + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
-#pragma unroll
-          for (int p = 2 - k; p >= 0; --p)
-#pragma unroll
-            for (int it = 2 * ts; it < 4; ++it) u[it] = mfma_bf16(f[it], b.p[p], u[it]);
-        }
-      }
+      const Parts<3> x0 = split_tiles<3>(km[0], km[1]);
+      products(0, 2, fa, x0);
+      t_part(0, 0, fa);
+      const Parts<3> x1 = split_tiles<3>(km[2], km[3]);
+      products(0, 1, fb, x0);
+      t_part(1, 2, fb);
+      products(0, 0, fa, x0);
+      weave_reads<8>();
+      weave<4, 2>();
+      weave_reads<4>();
+      weave<8, 2>();
+      weave_reads<2>();
+      weave<12, 2>();
+      __builtin_amdgcn_sched_barrier(0);
+      bf16x8 fc[4];
+      t_part(1, 1, fa);
+      t_part(1, 0, fc);
+      products(1, 2, fb, x1);
+      products(1, 1, fa, x1);
+      products(1, 0, fc, x1);
+      weave_reads<4>();
     };
-    // O = scale gam o (Q M) + P U
-    auto outputs = [&]() {
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const f32x4 gm = *(const f32x4*)(rows + token_row(it, 4 * g));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) qm[it][r] *= a.scale * gm[r];
-      }
-#pragma unroll
-      for (int ts = 0; ts < 2; ++ts) {
-        const Parts<2> b = split_tiles<2>(u[2 * ts], u[2 * ts + 1]);
-        bf16x8 f[2][4];
-#pragma unroll
-        for (int k = 1; k >= 0; --k)
-#pragma unroll
-          for (int it = 2 * ts; it < 4; ++it)
-            f[k][it] = *(const bf16x8*)(smem + C::kOffP + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
-#pragma unroll
-        for (int o = 1; o >= 0; --o)
-#pragma unroll
-          for (int p = o; p >= 0; --p)
-#pragma unroll
-            for (int it = 2 * ts; it < 4; ++it) qm[it] = mfma_bf16(f[p][it], b.p[o - p], qm[it]);
-      }
-    };
-    // M <- gam_C M + K^T (dec o U), a half of the chunk's tokens at a time
+    // a chunk formed with its decays: M and Q M take theirs
     auto decay = [&](f32x4* mm) {
-      const float gl = rows[kChunk - 1];
+      if (!(flags & kGated)) return;
+      const float gl = rows[kLast];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt) mm[mt] *= gl;
+      if (C::Q) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mm[mt][r] *= gl;
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const f32x4 de = *(const f32x4*)(rows + kChunk + token_row(it, 4 * g));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) u[it][r] *= de[r];
+        for (int it = 0; it < 4; ++it) qm[it] *= *(const f32x4*)(rows + kRowGam + token_row(it, 4 * g)) * a.scale;
       }
     };
-    auto advance = [&](f32x4* mm, int ts) {
-      const Parts<3> b = split_tiles<3>(u[2 * ts], u[2 * ts + 1]);
+    // the parts of half ts of U that go into M, and those for O
+    Parts<3> ub;
+    Parts<2> ob;
+    auto split_u = [&](int ts) {
+      if (flags & kGated) {
+        if (C::Q) ob = split_tiles<2>(u[2 * ts], u[2 * ts + 1]);
 #pragma unroll
-      for (int m0 = 0; m0 < MT; m0 += 4) {
-        bf16x8 f[4];
+        for (int it = 2 * ts; it < 2 * ts + 2; ++it) u[it] *= *(const f32x4*)(rows + kRowDec + token_row(it, 4 * g));
+      }
+      ub = split_tiles<3>(u[2 * ts], u[2 * ts + 1]);
+      if (C::Q && !(flags & kGated)) ob = Parts<2>{{ub.p[0], ub.p[1]}};
+    };
+    // Q M + P U
+    auto outputs = [&](int ts) {
+      bf16x8 f[2][4];
+#pragma unroll
+      for (int k = 1; k >= 0; --k)
+#pragma unroll
+        for (int it = 2 * ts; it < 4; ++it)
+          f[k][it] = *(const bf16x8*)(smem + C::kOffP + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
+#pragma unroll
+      for (int o = 1; o >= 0; --o)
+#pragma unroll
+        for (int p = o; p >= 0; --p)
+#pragma unroll
+          for (int it = 2 * ts; it < 4; ++it) qm[it] = mfma_bf16(f[p][it], ob.p[o - p], qm[it]);
+    };
+    // M += K^T U, a half of the chunk's tokens at a time
+    auto advance = [&](f32x4* mm, int ts) {
+      bf16x8 f[2][4];
+      auto fetch = [&](int m0, bf16x8* to) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const unsigned at = (co ^ (64u * ((m0 + i) >> 1))) + (32 * ts * D + 4 * (i & 1)) * 2;
           // 8 rows on: the same swizzle
-          f[i] = __builtin_shufflevector(delta_read_tr((const uint16_t*)(smem + at)),
-                                         delta_read_tr((const uint16_t*)(smem + at + 8 * D * 2)), 0, 1, 2, 3, 4, 5, 6,
-                                         7);
+          to[i] = __builtin_shufflevector(delta_read_tr((const uint16_t*)(smem + at)),
+                                          delta_read_tr((const uint16_t*)(smem + at + 8 * D * 2)), 0, 1, 2, 3, 4, 5, 6,
+                                          7);
         }
+      };
+      fetch(0, f[0]);
+#pragma unroll
+      for (int m0 = 0; m0 < MT; m0 += 4) {
+        if (m0 + 4 < MT) fetch(m0 + 4, f[(m0 / 4 + 1) & 1]);
 #pragma unroll
         for (int p = 2; p >= 0; --p)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mm[m0 + i] = mfma_bf16(f[i], b.p[p], mm[m0 + i]);
+          for (int i = 0; i < 4; ++i) mm[m0 + i] = mfma_bf16(f[(m0 / 4) & 1][i], ub.p[p], mm[m0 + i]);
       }
     };
 
-    lds_barrier();
+    if (flags & kShift) {  // 2^s goes into the state
+      const float f = rows[kPre];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        m[mt] *= f;
+        if (MODE == kTransition) e[mt] *= f;
+      }
+    }
     if (MODE == kKeep) {
+      const float f = rows[kScale0];
       char* const mo = (char*)(sa.m_out + ((int64_t)(sg.x + j) * a.heads + h) * dd);
       const unsigned m_off = (unsigned)(8 * g * D + dv) * 4u;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) *(float*)(mo + dim_row(mt, r) * D * 4 + m_off) = m[mt][r];
+        for (int r = 0; r < 4; ++r) *(float*)(mo + dim_row(mt, r) * D * 4 + m_off) = f * m[mt][r];
     }
     read_m(m, C::Q);
     form_x(true);
@@ -568,8 +674,10 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
     lds_barrier();
     if (MODE == kTransition) {
       decay(m);
+      split_u(0);
       advance(m, 0);
       __builtin_amdgcn_sched_barrier(0);
+      split_u(1);
       advance(m, 1);
       __builtin_amdgcn_sched_barrier(0);
       read_m(e, false);
@@ -581,24 +689,31 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
       char* const uo = (char*)(sa.u_out + ((tok0 + (int64_t)kChunk * j) * a.heads + h) * D);
       const unsigned u_off = (unsigned)(lt * a.heads * D + dv) * 4u;
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+      for (int it = 0; it < 4; ++it) {
+        const f32x4 fo = *(const f32x4*)(rows + kRowO + token_row(it, 4 * g));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = token_row(it, r);
           char* const at = uo + (int64_t)t * a.heads * D * 4;
-          if (lt + t < count) *(float*)(at + u_off) = u[it][r];
+          if (lt + t < count) *(float*)(at + u_off) = fo[r] * u[it][r];
         }
+      }
     }
-    if (MODE == kOutputs) outputs();
     f32x4* const mm = MODE == kTransition ? e : m;
     decay(mm);
+    split_u(0);
+    if (C::Q) outputs(0);
     advance(mm, 0);
     if (MODE != kTransition) lds_barrier();
+    split_u(1);
+    if (C::Q) outputs(1);
     if (MODE == kOutputs) {
       char* const at = op + (int64_t)kChunk * j * sa.ld_o * 2;
       unsigned off = o_off, first = lt;
       pin(off);
       pin(first);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) qm[it] *= *(const f32x4*)(rows + kRowO + token_row(it, 4 * g));
       if (count == kChunk) {
 #pragma unroll
         for (int it = 0; it < 4; ++it)
@@ -615,6 +730,14 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
       }
     }
     advance(mm, 1);
+    if (j == n - 1) {
+      const float f = rows[kScale1];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        m[mt] *= f;
+        if (MODE == kTransition) e[mt] *= f;
+      }
+    }
   }
 
   if (MODE == kTransition) {

@@ -241,48 +241,59 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
 }
 
 // The states at the segments' starts, M <- N M + B along each sequence, or (REV) the
-// gradients at the segments' ends, M <- N^T M + E from its last segment back.  A
-// wave has 16 columns of one (sequence, head); the blocks of a sequence's first
-// (last) segment go through all of its segments.
+// gradients at the segments' ends, M <- N^T M + E from its last segment back.  The
+// blocks of a sequence's first (last) segment go through all of its segments, one
+// for each 16 columns of a head; wave w forms rows dim_row(w, .).  Each step is one
+// product that waits for the step before, so all else is out of the way: N's rows
+// are loaded and split a step ahead, and M passes between the waves as operand
+// parts in LDS.
 template <int D, bool REV>
-__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a, DeltaJoinArgs ja) {
-  constexpr int KS = D / 32, MT = D / 16, SL = D / 16;
-  const int lane = threadIdx.x, g = lane >> 4, c = lane & 15;
+__global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs ja) {
+  constexpr int KS = D / 32, SL = D / 16;
+  __shared__ __attribute__((aligned(16))) uint16_t mp[2][KS][3][kFragElems];
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int dv = 16 * (blockIdx.x % SL) + c;
   const int h = (blockIdx.x / SL) % a.heads;
   int si = blockIdx.x / SL / a.heads;
   int4 sg = delta_seg(a.sq, si);
   if (sg.y < 0 || !(sg.w & (REV ? 2 : 1))) return;
   const int64_t dd = (int64_t)D * D;
-  f32x4 m[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    m[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (ja.init)
-      m[mt] = *(const f32x4*)(ja.init + ((int64_t)sg.z * a.heads + h) * dd + (int64_t)dv * D +
-                              dim_row(mt, 4 * g));
-  }
-  while (true) {
-    const int64_t at = (int64_t)si * a.heads + h;
-    float* const to = ja.to + at * dd + (int64_t)dv * D;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) *(f32x4*)(to + dim_row(mt, 4 * g)) = m[mt];
-    if (sg.w & (REV ? 1 : 2)) return;
+  const int64_t col = (int64_t)dv * D + dim_row(w, 4 * g);
+  f32x4 m = {0.f, 0.f, 0.f, 0.f}, add = m;
+  if (ja.init) m = *(const f32x4*)(ja.init + ((int64_t)sg.z * a.heads + h) * dd + col);
+  Parts<3> row[KS];
+  auto load = [&](int at_seg) {
+    const int64_t at = (int64_t)at_seg * a.heads + h;
     const float* const nn = ja.trans + at * ja.stride * dd + (REV ? 2 * dd : 0);
-    const float* const add = (REV ? ja.e + at * dd : nn + dd) + (int64_t)dv * D;
-    Parts<3> b[KS];
+    add = *(const f32x4*)((REV ? ja.e + at * dd : ja.trans + at * ja.stride * dd + dd) + col);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) b[s] = split_tiles<3>(m[2 * s], m[2 * s + 1]);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) m[mt] = *(const f32x4*)(add + dim_row(mt, 4 * g));
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        mma<2>(m[mt], load8(nn + (int64_t)dim_row(mt, c) * D + 32 * s + 8 * g), b[s]);
+    for (int s = 0; s < KS; ++s) row[s] = load8(nn + (int64_t)dim_row(w, c) * D + 32 * s + 8 * g);
+  };
+  if (!(sg.w & (REV ? 1 : 2))) load(si);
+  for (int turn = 0;; turn ^= 1) {
+    *(f32x4*)(ja.to + ((int64_t)si * a.heads + h) * dd + col) = m;
+    if (sg.w & (REV ? 1 : 2)) return;
     si += REV ? -1 : 1;
     if (si < 0 || si >= a.sq.n_segs) return;
     sg = delta_seg(a.sq, si);
+    float x[8] = {m[0], m[1], m[2], m[3], 0.f, 0.f, 0.f, 0.f};
+    const Parts<3> p = split8<3>(x);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const u32x4 v = __builtin_bit_cast(u32x4, p.p[k]);
+      *(u32x2*)(mp[turn][w >> 1][k] + lane * 8 + 4 * (w & 1)) = u32x2{v[0], v[1]};
+    }
+    __syncthreads();  // the other buffer's readers are past it too
+    f32x4 acc[2] = {add, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      Parts<3> b;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) b.p[k] = *(const bf16x8*)(mp[turn][s][k] + lane * 8);
+      mma<2>(acc[s & 1], row[s], b);
+    }
+    if (!(sg.w & (REV ? 1 : 2))) load(si);
+    m = acc[0] + acc[1];
   }
 }
 
@@ -309,7 +320,7 @@ hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStre
 }
 
 hipError_t launch_delta_join(const DeltaArgs& a, const DeltaJoinArgs& j, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads * (a.d / 16))), blk(64);
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads * (a.d / 16))), blk(4 * a.d);
   if (a.d == 128) {
     if (j.e) hipLaunchKernelGGL((k_delta_join<128, true>), grid, blk, 0, st, a, j);
     else hipLaunchKernelGGL((k_delta_join<128, false>), grid, blk, 0, st, a, j);
