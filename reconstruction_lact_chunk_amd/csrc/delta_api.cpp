@@ -40,13 +40,16 @@ struct DeltaPlan {
 DeltaPlan delta_plan(const zm_delta_desc* d, int64_t n) {
   DeltaPlan p;
   p.n_chunks = (int)((n + (int64_t)(kChunk - 1) * d->n_seq) / kChunk);
-  // One workgroup goes through a whole sequence of one head while these are
-  // enough for half the compute units; with fewer, segments of at least
-  // kMinSegChunks chunks for one workgroup to each.
-  constexpr int kMinSegChunks = 8;
+  // One workgroup goes through a whole sequence of one head while these are enough
+  // for half the compute units, or while the sequences are short; else a workgroup to
+  // each segment of at least kMinSegChunks chunks, about kTargetWgs of them.
+  // Measured with 8 heads of 128, us whole / in segments: bf16 512 tokens 54 / 62,
+  // 640 65 / 65, 1560 151 / 83 (segments of 8 chunks: 138); fp32 384 tokens 96 / 88,
+  // 512 121 / 92; backward bf16 512 tokens 139 / 145, 1560 347 / 194.
+  constexpr int kMinSegChunks = 2, kSplitChunks = 8;
   const int64_t units = (int64_t)d->n_seq * d->heads;
   int64_t seg = p.n_chunks > 0 ? p.n_chunks : 1;
-  if (units < kTargetWgs / 2) {
+  if (units < kTargetWgs / 2 && p.n_chunks >= (int64_t)kSplitChunks * d->n_seq) {
     seg = ceil_div((int64_t)p.n_chunks * d->heads, kTargetWgs);
     if (seg < kMinSegChunks) seg = kMinSegChunks;
   }
@@ -130,7 +133,7 @@ BackwardWs backward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, co
   f.a.sq = seqs(d, p, n, offsets, c);
   const size_t slots = (size_t)p.n_chunks * d->heads, tile = (size_t)kTriFrags * kFragElems;
   const size_t dd = (size_t)d->d_head * d->d_head, rows = (size_t)n * d->heads * d->d_head;
-  f.a.t_frags = c.take<uint16_t>(slots * 3 * tile);
+  if (d->io_dtype == ZM_F32) f.a.t_frags = c.take<uint16_t>(slots * 3 * tile);
   f.a.tt_frags = c.take<uint16_t>(slots * 3 * tile);
   f.a.pt_frags = c.take<uint16_t>(slots * 3 * tile);
   f.a.rows = c.take<float>(slots * 3 * kChunk);
@@ -285,6 +288,7 @@ int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* 
   ZM_TRY(check_inputs(desc, n, offsets, q, k, v, g, beta));
   const int64_t wk = (int64_t)desc->heads_k * desc->d_head, wv = (int64_t)desc->heads * desc->d_head;
   if (ld_dq < wk || ld_dk < wk || ld_dv < wv || ld_dq % 8 || ld_dk % 8 || ld_dv % 8) return ZM_ERR_INVALID_ARG;
+  if (ld_dq > kMaxDeltaLd || ld_dk > kMaxDeltaLd || ld_dv > kMaxDeltaLd) return ZM_ERR_INVALID_ARG;
   if (n > 0) {
     ZM_TRY(check_ptr(d_o, 16));
     ZM_TRY(check_ptr(dq, 16));

@@ -95,14 +95,6 @@ __device__ __forceinline__ void weave_reads() {
   __builtin_amdgcn_sched_group_barrier(0x100, N, 0);  // LDS reads
 }
 
-// LDS reads and writes of this wave are done, then the workgroup's barrier.  Loads
-// and stores of global memory stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 __device__ __forceinline__ void wait_direct_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
 
 template <int D, int MODE>

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
     for (int i = 0; i < k; ++i) {
       const int f = i * s.seg_chunks;
       s.segs[s0 + i] = int4{c0 + f, c - f < s.seg_chunks ? c - f : s.seg_chunks, b,
-                            (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0)};
+                            (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0) | k << 2};
     }
     c0 += c;
     s0 += k;
@@ -233,8 +233,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
   if constexpr (BWD)
     write_frags<3, true>(mp, a.pt_frags + slot * 3 * kTriFrags * kFragElems);
   else
-    write_frags<NT == 1 ? 2 : 3, false>(
-        mp, a.p_frags + slot * (NT == 1 ? 2 : 3) * kTriFrags * kFragElems);
+    write_frags<3, false>(mp, a.p_frags + slot * 3 * kTriFrags * kFragElems);
   __syncthreads();
   f32x4 tc[4];
 #pragma unroll
@@ -269,20 +268,16 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) mp[(16 * i + 4 * g + r) * kPitch + 16 * w + c] = tc[i][r];
   __syncthreads();
-  write_frags<3, false>(mp, a.t_frags + slot * 3 * kTriFrags * kFragElems);
+  if constexpr (F32) write_frags<3, false>(mp, a.t_frags + slot * 3 * kTriFrags * kFragElems);
   if constexpr (BWD) write_frags<3, true>(mp, a.tt_frags + slot * 3 * kTriFrags * kFragElems);
 }
 
-template <bool BWD>
-hipError_t prep_any(const DeltaArgs& a, hipStream_t st) {
+template <int D>
+hipError_t prep_any(const DeltaArgs& a, bool backward, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)a.sq.n_chunks * a.heads)), blk(256);
-  if (a.d == 128) {
-    if (a.f32) hipLaunchKernelGGL((k_delta_prep<128, true, BWD>), grid, blk, 0, st, a);
-    else hipLaunchKernelGGL((k_delta_prep<128, false, BWD>), grid, blk, 0, st, a);
-  } else {
-    if (a.f32) hipLaunchKernelGGL((k_delta_prep<64, true, BWD>), grid, blk, 0, st, a);
-    else hipLaunchKernelGGL((k_delta_prep<64, false, BWD>), grid, blk, 0, st, a);
-  }
+  if (!backward) hipLaunchKernelGGL((k_delta_prep<D, true, false>), grid, blk, 0, st, a);
+  else if (a.f32) hipLaunchKernelGGL((k_delta_prep<D, true, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((k_delta_prep<D, false, true>), grid, blk, 0, st, a);
   return hipGetLastError();
 }
 
@@ -295,7 +290,7 @@ hipError_t launch_delta_table(const DeltaSeqs& s, hipStream_t st) {
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t st) {
   if (a.sq.n_chunks == 0) return hipSuccess;
-  return backward ? prep_any<true>(a, st) : prep_any<false>(a, st);
+  return a.d == 128 ? prep_any<128>(a, backward, st) : prep_any<64>(a, backward, st);
 }
 
 }  // namespace zm

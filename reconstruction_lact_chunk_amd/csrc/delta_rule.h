@@ -8,8 +8,10 @@
 //   A = strictly_lower(b_i G_ij k_i.k_j),  T = (I + A)^-1,  P = scale lower(G_ij q_i.k_j)
 //   R = V - gam o (K M),  U = T (b o R),  O = scale gam o (Q M) + P U,
 //   M' = gam_C M + K^T (dec o U).
-// T and P do not depend on M: delta_prep.hip forms them for all chunks at once,
-// delta_scan.hip goes through the chunks of a sequence in order.
+// T and P do not depend on M.  fp32 tokens: delta_prep.hip forms them for all chunks
+// at once, delta_scan.hip goes through the chunks of a sequence in order; bf16
+// tokens: delta_fused.hip does both side by side.  A long sequence of few heads is cut
+// into segments, whose transitions M -> N M + B are joined before the outputs.
 //
 // Matrix products run on v_mfma_f32_16x16x32_bf16.  An operand held in fp32
 // (M, U, T, P, fp32 tokens) enters as a sum of bf16 parts: three parts carry 24
@@ -39,7 +41,8 @@ constexpr float kMinLogDecay = -128.f; // exp of less is 0 in fp32
 struct DeltaSeqs {
   const int* offsets;    // [n_seq + 1] or null: one sequence of all n tokens
   int4* chunks;          // {first token, tokens, sequence, 0}, null without a table
-  int4* segs;            // {first chunk, chunks (-1: unused), sequence, 1 first | 2 last}
+  int4* segs;            // {first chunk, chunks (-1: unused), sequence,
+                         //  1 first | 2 last | 4 * segments of the sequence}
   int* first_chunk;      // [n_seq + 1] scratch of the table's kernel
   int* begin;            // [n_seq + 1] scratch: clamped offsets
   int n, n_seq;
@@ -62,7 +65,7 @@ struct DeltaArgs {
   bool f32;
   // per (chunk, head): operand tiles and row factors
   uint16_t* t_frags;    // [3][kTriFrags][kFragElems] parts of T
-  uint16_t* p_frags;    // parts of P (2 for bf16 io, 3 for fp32)
+  uint16_t* p_frags;    // parts of P (these two: fp32 forward)
   uint16_t* tt_frags;   // parts of T^T, P^T (backward)
   uint16_t* pt_frags;
   float* rows;          // [3][kChunk] gam, dec, beta
@@ -108,7 +111,7 @@ __device__ __forceinline__ int4 delta_seg(const DeltaSeqs& s, int si) {
   if (si >= segs) return int4{0, -1, 0, 0};
   const int f = si * s.seg_chunks;
   const int c = chunks - f < s.seg_chunks ? chunks - f : s.seg_chunks;
-  return int4{f, c, 0, (si == 0 ? 1 : 0) | (si == segs - 1 ? 2 : 0)};
+  return int4{f, c, 0, (si == 0 ? 1 : 0) | (si == segs - 1 ? 2 : 0) | segs << 2};
 }
 
 // Token of slot e of lane group g in a 32-token step (and, for row m = 4 g' + i of
@@ -182,6 +185,15 @@ __device__ __forceinline__ dbf16x4 delta_read_tr(const uint16_t* p) {
       (lds_dbf16x4*)((__attribute__((address_space(3))) void*)(p)));
 }
 
+// LDS reads and writes of this wave are done, then the workgroup's barrier.  Loads
+// and stores of global memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Token element type and the parts it takes.
 template <bool F32>
 struct Tok {
@@ -243,7 +255,7 @@ struct DeltaGradArgs {
 // ---- launchers --------------------------------------------------------------------
 // The tables of chunks and segments (n_seq > 1).
 hipError_t launch_delta_table(const DeltaSeqs& s, hipStream_t st);
-// T and P (backward: T, T^T, P^T) and the row factors of every chunk and head.
+// T and P (backward: T of fp32 tokens, T^T, P^T) and the row factors of every chunk and head.
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t st);
 // fp32 tokens: the chunks in order from the tiles of launch_delta_prep; bf16 tokens:
 // the same with the triangles formed on the way (no tiles needed).

@@ -11,17 +11,14 @@ struct ScanCfg {
   static constexpr int NT = Tok<F32>::NT;
   static constexpr int PITCH = D + 16;
   static constexpr int TILE = kChunk * PITCH;   // one part of K or Q
-  static constexpr int WAVES = D / 32;
-  static constexpr int THREADS = 64 * WAVES;
 };
 
-// K (or Q) of the chunk into its LDS parts; rows past `count` are zero.
-template <int D, bool F32>
-__device__ __forceinline__ void stage(uint16_t* lds, const typename Tok<F32>::T* src, int64_t ld,
-                                      int count) {
-  using C = ScanCfg<D, F32>;
+// fp32 K (or Q) of the chunk into its LDS parts; rows past `count` are zero.
+template <int D>
+__device__ __forceinline__ void stage(uint16_t* lds, const float* src, int64_t ld, int count) {
+  using C = ScanCfg<D, true>;
   constexpr int CPR = D / 8;
-  for (int i = threadIdx.x; i < kChunk * CPR; i += C::THREADS) {
+  for (int i = threadIdx.x; i < kChunk * CPR; i += 2 * D) {
     const int row = i / CPR, col = 8 * (i % CPR);
     Parts<C::NT> p = zero_parts<C::NT>();
     if (row < count) p = load8(src + (int64_t)row * ld + col);
@@ -63,16 +60,5 @@ __device__ __forceinline__ Parts<NP> frag(const uint16_t* f, int i, int lane) {
     p.p[k] = *(const bf16x8*)(f + (k * kTriFrags + i) * kFragElems + lane * 8);
   return p;
 }
-
-// A pair of neighbouring columns of one token.
-__device__ __forceinline__ f32x2 load_pair(const uint16_t* p) {
-  const unsigned w = *(const unsigned*)p;
-  return f32x2{bf16lo(w), bf16hi(w)};
-}
-__device__ __forceinline__ f32x2 load_pair(const float* p) { return *(const f32x2*)p; }
-__device__ __forceinline__ void store_pair(uint16_t* p, float a, float b) {
-  *(unsigned*)p = pack_bf16x2(a, b);
-}
-__device__ __forceinline__ void store_pair(float* p, float a, float b) { *(f32x2*)p = f32x2{a, b}; }
 
 }  // namespace zm

@@ -1,5 +1,5 @@
-// The chunks of a segment in order: one workgroup per (segment, head), each wave
-// 32 columns of M (d_v) and all its rows (delta_rule.h).  A wave's columns need
+// fp32 tokens: the chunks of a segment in order, one workgroup per (segment, head),
+// each wave 32 columns of M (d_v) and all its rows (delta_rule.h).  A wave's columns need
 // nothing from the other waves but the operands they share: K and Q, read from
 // LDS in rows and, for K^T, through the transposing read; T and P, read as
 // operand tiles.  M, R and U stay in registers: each is the result of one product
@@ -17,11 +17,10 @@ namespace {
 // from the identity, so M_end = N M_start + B.
 enum { kOutputs = 0, kKeep = 1, kTransition = 2 };
 
-template <int D, bool F32, int MODE>
+template <int D, int MODE>
 __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanArgs sa) {
-  using C = ScanCfg<D, F32>;
-  using T = typename Tok<F32>::T;
-  constexpr int NT = C::NT, KS = D / 32, MT = D / 16, NO = NT == 1 ? 2 : 3;
+  using C = ScanCfg<D, true>;
+  constexpr int NT = C::NT, KS = D / 32, MT = D / 16;
   __shared__ __attribute__((aligned(16))) uint16_t lds[(MODE == kOutputs ? 2 : 1) * NT * C::TILE];
   uint16_t* const kl = lds;
   uint16_t* const ql = lds + NT * C::TILE;  // kOutputs only
@@ -64,12 +63,12 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
     const int count = ch.y;
     const int64_t slot = (int64_t)ci * a.heads + h;
     const uint16_t* const tf = a.t_frags + slot * 3 * kTriFrags * kFragElems;
-    const uint16_t* const pf = a.p_frags + slot * NO * kTriFrags * kFragElems;
+    const uint16_t* const pf = a.p_frags + slot * 3 * kTriFrags * kFragElems;
     const float* const rows = a.rows + slot * 3 * kChunk;
     __syncthreads();
-    stage<D, F32>(kl, (const T*)a.k.p + (int64_t)ch.x * a.k.ld + hk * D, a.k.ld, count);
+    stage<D>(kl, (const float*)a.k.p + (int64_t)ch.x * a.k.ld + hk * D, a.k.ld, count);
     if (MODE == kOutputs)
-      stage<D, F32>(ql, (const T*)a.q.p + (int64_t)ch.x * a.q.ld + hk * D, a.q.ld, count);
+      stage<D>(ql, (const float*)a.q.p + (int64_t)ch.x * a.q.ld + hk * D, a.q.ld, count);
     __syncthreads();
 
     if (MODE == kKeep) {
@@ -96,18 +95,18 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         const int row = token_row(it, c), col = 32 * s + 8 * g;
-        const auto ka = lds_row<D, F32>(kl, row, col);
+        const auto ka = lds_row<D, true>(kl, row, col);
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) mma<2>(km[it][ct], ka, b[ct]);
         if (MODE == kOutputs) {
-          const auto qa = lds_row<D, F32>(ql, row, col);
+          const auto qa = lds_row<D, true>(ql, row, col);
 #pragma unroll
-          for (int ct = 0; ct < 2; ++ct) mma<NO - 1>(qm[it][ct], qa, b[ct]);
+          for (int ct = 0; ct < 2; ++ct) mma<2>(qm[it][ct], qa, b[ct]);
         }
       }
     }
     // X = beta o (V - gam o K M), in km
-    const T* const vp = (const T*)a.v.p + (int64_t)ch.x * a.v.ld + h * D + dv;
+    const float* const vp = (const float*)a.v.p + (int64_t)ch.x * a.v.ld + h * D + dv;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int t0 = token_row(it, 4 * g);
@@ -115,7 +114,7 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         f32x2 v = {0.f, 0.f};
-        if (!unit && t0 + r < count) v = load_pair(vp + (int64_t)(t0 + r) * a.v.ld);
+        if (!unit && t0 + r < count) v = *(const f32x2*)(vp + (int64_t)(t0 + r) * a.v.ld);
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) km[it][ct][r] = be[r] * fmaf(-gm[r], km[it][ct][r], v[ct]);
       }
@@ -161,23 +160,23 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
       }
 #pragma unroll
       for (int ts = 0; ts < 2; ++ts) {
-        Parts<NO> b[2];
+        Parts<3> b[2];
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<NO>(u[2 * ts][ct], u[2 * ts + 1][ct]);
+        for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(u[2 * ts][ct], u[2 * ts + 1][ct]);
 #pragma unroll
         for (int it = 2 * ts; it < 4; ++it) {
-          const auto pa = frag<NO>(pf, low_frag(it, ts), lane);
+          const auto pa = frag<3>(pf, low_frag(it, ts), lane);
 #pragma unroll
-          for (int ct = 0; ct < 2; ++ct) mma<NO - 1>(qm[it][ct], pa, b[ct]);
+          for (int ct = 0; ct < 2; ++ct) mma<2>(qm[it][ct], pa, b[ct]);
         }
       }
-      T* const op = (T*)sa.o + (int64_t)ch.x * sa.ld_o + h * D + dv;
+      float* const op = (float*)sa.o + (int64_t)ch.x * sa.ld_o + h * D + dv;
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = token_row(it, 4 * g + r);
-          if (t < count) store_pair(op + (int64_t)t * sa.ld_o, qm[it][0][r], qm[it][1][r]);
+          if (t < count) *(f32x2*)(op + (int64_t)t * sa.ld_o) = f32x2{qm[it][0][r], qm[it][1][r]};
         }
     }
     // M <- gam_C M + K^T (dec o U)
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
       for (int ct = 0; ct < 2; ++ct) b[ct] = split_tiles<3>(u[2 * ts][ct], u[2 * ts + 1][ct]);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const auto ka = lds_col<D, F32>(kl, mt, ts, g, c);
+        const auto ka = lds_col<D, true>(kl, mt, ts, g, c);
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) mma<2>(m[mt][ct], ka, b[ct]);
       }
@@ -255,68 +254,79 @@ __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs
   const int dv = 16 * (blockIdx.x % SL) + c;
   const int h = (blockIdx.x / SL) % a.heads;
   int si = blockIdx.x / SL / a.heads;
-  int4 sg = delta_seg(a.sq, si);
+  const int4 sg = delta_seg(a.sq, si);
   if (sg.y < 0 || !(sg.w & (REV ? 2 : 1))) return;
   const int64_t dd = (int64_t)D * D;
   const int64_t col = (int64_t)dv * D + dim_row(w, 4 * g);
-  f32x4 m = {0.f, 0.f, 0.f, 0.f}, add = m;
+  int turn = 0;
+  f32x4 m = {0.f, 0.f, 0.f, 0.f};
   if (ja.init) m = *(const f32x4*)(ja.init + ((int64_t)sg.z * a.heads + h) * dd + col);
-  Parts<3> row[KS];
-  auto load = [&](int at_seg) {
-    const int64_t at = (int64_t)at_seg * a.heads + h;
-    const float* const nn = ja.trans + at * ja.stride * dd + (REV ? 2 * dd : 0);
-    add = *(const f32x4*)((REV ? ja.e + at * dd : ja.trans + at * ja.stride * dd + dd) + col);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) row[s] = load8(nn + (int64_t)dim_row(w, c) * D + 32 * s + 8 * g);
-  };
-  if (!(sg.w & (REV ? 1 : 2))) load(si);
-  for (int turn = 0;; turn ^= 1) {
-    *(f32x4*)(ja.to + ((int64_t)si * a.heads + h) * dd + col) = m;
-    if (sg.w & (REV ? 1 : 2)) return;
-    si += REV ? -1 : 1;
-    if (si < 0 || si >= a.sq.n_segs) return;
-    sg = delta_seg(a.sq, si);
-    float x[8] = {m[0], m[1], m[2], m[3], 0.f, 0.f, 0.f, 0.f};
-    const Parts<3> p = split8<3>(x);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const u32x4 v = __builtin_bit_cast(u32x4, p.p[k]);
-      *(u32x2*)(mp[turn][w >> 1][k] + lane * 8 + 4 * (w & 1)) = u32x2{v[0], v[1]};
-    }
-    __syncthreads();  // the other buffer's readers are past it too
-    f32x4 acc[2] = {add, {0.f, 0.f, 0.f, 0.f}};
+  // N's rows and what is added, kAhead segments ahead
+  constexpr int kAhead = 3;
+  f32x4 raw[kAhead][2 * KS], add[kAhead];
+  auto load = [&](int slot, int at_seg) {
+    const int sj = clampi(at_seg, 0, a.sq.n_segs - 1);
+    const int64_t at = (int64_t)sj * a.heads + h;
+    const float* const nn = ja.trans + at * ja.stride * dd;
+    add[slot] = *(const f32x4*)((REV ? ja.e + at * dd : nn + dd) + col);
+    const float* const r = nn + (REV ? 2 * dd : 0) + (int64_t)dim_row(w, c) * D + 8 * g;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      Parts<3> b;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) b.p[k] = *(const bf16x8*)(mp[turn][s][k] + lane * 8);
-      mma<2>(acc[s & 1], row[s], b);
+      raw[slot][2 * s] = *(const f32x4*)(r + 32 * s);
+      raw[slot][2 * s + 1] = *(const f32x4*)(r + 32 * s + 4);
     }
-    if (!(sg.w & (REV ? 1 : 2))) load(si);
-    m = acc[0] + acc[1];
+  };
+  constexpr int kStep = REV ? -1 : 1;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i, si + kStep * i);  // past the sequence: not used
+  int left = sg.w >> 2;  // segments to go
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      *(f32x4*)(ja.to + ((int64_t)si * a.heads + h) * dd + col) = m;
+      if (--left <= 0) return;
+      si += kStep;
+      uint16_t(*const buf)[3][kFragElems] = mp[turn];
+      turn ^= 1;
+      float x[8] = {m[0], m[1], m[2], m[3], 0.f, 0.f, 0.f, 0.f};
+      const Parts<3> p = split8<3>(x);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const u32x4 v = __builtin_bit_cast(u32x4, p.p[k]);
+        *(u32x2*)(buf[w >> 1][k] + lane * 8 + 4 * (w & 1)) = u32x2{v[0], v[1]};
+      }
+      Parts<3> row[KS];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) row[s] = split_tiles<3>(raw[i][2 * s], raw[i][2 * s + 1]);
+      f32x4 acc[2] = {add[i], {0.f, 0.f, 0.f, 0.f}};
+      load(i, si + kStep * (kAhead - 1));
+      lds_barrier();  // the other buffer's readers are past it too
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        Parts<3> b;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) b.p[k] = *(const bf16x8*)(buf[s][k] + lane * 8);
+        mma<2>(acc[s & 1], row[s], b);
+      }
+      m = acc[0] + acc[1];
+    }
   }
 }
 
-template <int D, bool F32>
+template <int D>
 hipError_t scan_any(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st) {
-  using C = ScanCfg<D, F32>;
   const int64_t blocks = (int64_t)a.sq.n_segs * a.heads;
-  if (s.trans)
-    hipLaunchKernelGGL((k_delta_scan<D, F32, kTransition>), dim3((unsigned)(2 * blocks)),
-                       dim3(C::THREADS), 0, st, a, s);
-  else if (s.m_out)
-    hipLaunchKernelGGL((k_delta_scan<D, F32, kKeep>), dim3((unsigned)blocks), dim3(C::THREADS), 0, st, a, s);
-  else
-    hipLaunchKernelGGL((k_delta_scan<D, F32, kOutputs>), dim3((unsigned)blocks), dim3(C::THREADS),
-                       0, st, a, s);
+  const dim3 grid((unsigned)blocks), twice((unsigned)(2 * blocks)), blk(2 * D);
+  if (s.trans) hipLaunchKernelGGL((k_delta_scan<D, kTransition>), twice, blk, 0, st, a, s);
+  else if (s.m_out) hipLaunchKernelGGL((k_delta_scan<D, kKeep>), grid, blk, 0, st, a, s);
+  else hipLaunchKernelGGL((k_delta_scan<D, kOutputs>), grid, blk, 0, st, a, s);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStream_t st) {
-  if (a.d == 128) return a.f32 ? scan_any<128, true>(a, s, st) : scan_any<128, false>(a, s, st);
-  return a.f32 ? scan_any<64, true>(a, s, st) : scan_any<64, false>(a, s, st);
+  return a.d == 128 ? scan_any<128>(a, s, st) : scan_any<64>(a, s, st);
 }
 
 hipError_t launch_delta_join(const DeltaArgs& a, const DeltaJoinArgs& j, hipStream_t st) {
