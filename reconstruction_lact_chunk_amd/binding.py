@@ -6,6 +6,7 @@ If the library is missing, every call raises ZmError; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -199,11 +200,12 @@ _IO = {torch.bfloat16: BF16, torch.float32: F32}
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    """Handle of the device's current stream, without a torch.cuda.Stream around it (2 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check_weights(w1, w2, w3, device=True):
@@ -544,25 +546,18 @@ def _same_gpu(first, *others):
     """All on one GPU: checked after shapes and types, as for the other calls."""
     if not first.is_cuda:
         raise ZmError("tensors must be on the GPU")
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:  # -1 on the CPU
             raise ZmError(f"tensors must all be on {first.device}, got one on {t.device}")
 
 
-class _on_device:
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _on_device(device):
     """Makes a tensor's device the current one for a call, if it is not."""
-
-    def __init__(self, device):
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(
-            device)
-
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard:
-            self.guard.__exit__(*exc)
+    return _AS_IT_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _row_stride(x, width):
@@ -573,7 +568,7 @@ def _row_stride(x, width):
 
 
 def _vector(t, width, name):
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (width,)
+    if t is not None and (t.dtype != torch.float32 or t.shape != (width,)
                           or not t.is_contiguous()):
         raise ZmError(f"{name} must be a contiguous fp32 tensor of {width} elements")
 
@@ -587,7 +582,7 @@ def _norm_rows(name, t, like=None):
 
 
 def _norm_stats(stats, n):
-    if stats.dtype != torch.float32 or tuple(stats.shape) != (2, n) or not stats.is_contiguous():
+    if stats.dtype != torch.float32 or stats.shape != (2, n) or not stats.is_contiguous():
         raise ZmError(f"stats must be contiguous fp32 [2, {n}]")
 
 
@@ -658,7 +653,7 @@ def _heads_rows(name, t, n, heads, d, dtype):
     """Checks a [n, heads, d] token tensor and returns its token stride."""
     if t.dtype != dtype or dtype not in _IO:
         raise ZmError(f"{name}: dtype {t.dtype}, the call needs bf16 or fp32 throughout")
-    if tuple(t.shape) != (n, heads, d):
+    if t.shape != (n, heads, d):
         raise ZmError(f"{name}: shape {tuple(t.shape)} != [{n}, {heads}, {d}]")
     if n > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
         raise ZmError(f"{name}: token tensors need unit stride on d and d on heads")
@@ -684,7 +679,7 @@ def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_ou
     sec = [int(c) for c in sections]
     if not 1 <= len(sec) <= 4:
         raise ZmError("sections: one to four axes")
-    if pos.dtype not in (torch.int32, torch.float32) or tuple(pos.shape) != (n, len(sec)) \
+    if pos.dtype not in (torch.int32, torch.float32) or pos.shape != (n, len(sec)) \
             or not pos.is_contiguous():
         raise ZmError(f"pos must be contiguous int32 or fp32 [{n}, {len(sec)}]")
     _vector(freqs, sum(sec), "freqs")
@@ -720,7 +715,7 @@ def _delta_inputs(q, k, v, g, beta, scale):
     lds = [_heads_rows("q", q, n, hk, d, q.dtype), _heads_rows("k", k, n, hk, d, q.dtype),
            _heads_rows("v", v, n, h, d, q.dtype)]
     for name, t in (("g", g), ("beta", beta)):
-        if t.dtype != torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
+        if t.dtype != torch.float32 or t.shape != (n, h) or not t.is_contiguous():
             raise ZmError(f"{name} must be contiguous fp32 [{n}, {h}]")
     return DeltaDesc(h, hk, d, _IO[q.dtype], 1, float(d ** -0.5 if scale is None else scale), *lds,
                      h * d), n
@@ -738,7 +733,7 @@ def _delta_offsets(offsets):
 
 def _delta_state(name, t, desc):
     want = (desc.n_seq, desc.heads, desc.d_head, desc.d_head)
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != want
+    if t is not None and (t.dtype != torch.float32 or t.shape != want
                           or not t.is_contiguous()):
         raise ZmError(f"{name} must be contiguous fp32 {list(want)}")
 
@@ -833,7 +828,7 @@ def delta_rule_backward(do, q, k, v, g, beta, state=None, dstate=None, offsets=N
     lds = [_heads_rows("dq", dq, n, hk, d, q.dtype), _heads_rows("dk", dk, n, hk, d, q.dtype),
            _heads_rows("dv", dv, n, h, d, q.dtype)]
     for name, t in (("dg", dg), ("dbeta", dbeta)):
-        if t.dtype != torch.float32 or tuple(t.shape) != (n, h) or not t.is_contiguous():
+        if t.dtype != torch.float32 or t.shape != (n, h) or not t.is_contiguous():
             raise ZmError(f"{name} must be contiguous fp32 [{n}, {h}]")
     _delta_state("the first states' gradient", dstart, desc)
     _same_gpu(q, do, k, v, g, beta, state, dstate, offsets, *out, workspace)
