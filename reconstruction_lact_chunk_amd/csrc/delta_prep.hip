@@ -12,28 +12,34 @@ constexpr int kBlk = 336;      // floats of a 16 x 16 diagonal block (rows of 20
 
 // ---- tables -------------------------------------------------------------------
 // One workgroup: the clamped, nondecreasing offsets, the prefix sums of chunks
-// and segments, then every chunk's and segment's entry by a search in them.
+// and segments, then every chunk's and segment's entry by a search in them.  A chain
+// of dependent steps, so scans run within waves and the searches in LDS where the
+// sequences fit it.
+constexpr int kTableLds = 1024;  // sequences
+
 __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
-  __shared__ int sh[2][1024];
-  const int t = threadIdx.x, per = (s.n_seq + 1023) / 1024;
+  __shared__ int part[3][16], first_l[kTableLds + 1], begin_l[kTableLds + 1], segs_l;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, per = (s.n_seq + 1023) / 1024;
+  const bool in_lds = s.n_seq <= kTableLds;
   const int b0 = t * per, b1 = b0 + per < s.n_seq ? b0 + per : s.n_seq;
   // running maximum of the clamped ends
-  int top = t == 0 ? clampi(s.offsets[0], 0, s.n) : 0;
+  const int start = clampi(s.offsets[0], 0, s.n);
+  int top = start;
   for (int b = b0; b < b1; ++b) {
     const int e = clampi(s.offsets[b + 1], 0, s.n);
     if (e > top) top = e;
   }
-  int cur = 0;
-  sh[0][t] = top;
-  __syncthreads();
-  for (int w = 1; w < 1024; w *= 2, cur ^= 1) {
-    int v = sh[cur][t];
-    if (t >= w && sh[cur][t - w] > v) v = sh[cur][t - w];
-    sh[cur ^ 1][t] = v;
-    __syncthreads();
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const int o = __shfl_up(top, m, 64);
+    if (lane >= m && o > top) top = o;
   }
-  int run = t == 0 ? clampi(s.offsets[0], 0, s.n) : sh[cur][t - 1];
+  if (lane == 63) part[0][w] = top;
+  int run = __shfl_up(top, 1, 64);
+  if (lane == 0) run = start;
   __syncthreads();
+  for (int i = 0; i < w; ++i)
+    if (part[0][i] > run) run = part[0][i];
   const int run0 = run;
   int nc = 0, ns = 0;
   for (int b = b0; b < b1; ++b) {
@@ -44,27 +50,36 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
     ns += c > 0 ? (c + s.seg_chunks - 1) / s.seg_chunks : 1;
     run = e;
   }
-  int2 sum{nc, ns};
-  for (int which = 0; which < 2; ++which) {
-    cur = 0;
-    sh[0][t] = which ? ns : nc;
-    __syncthreads();
-    for (int w = 1; w < 1024; w *= 2, cur ^= 1) {
-      sh[cur ^ 1][t] = sh[cur][t] + (t >= w ? sh[cur][t - w] : 0);
-      __syncthreads();
+  int c0 = nc, s0 = ns;
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const int oc = __shfl_up(c0, m, 64), os = __shfl_up(s0, m, 64);
+    if (lane >= m) {
+      c0 += oc;
+      s0 += os;
     }
-    if (which) sum.y = sh[cur][t] - ns; else sum.x = sh[cur][t] - nc;
-    __syncthreads();
+  }
+  if (lane == 63) {
+    part[1][w] = c0;
+    part[2][w] = s0;
+  }
+  c0 -= nc;
+  s0 -= ns;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) {
+    c0 += part[1][i];
+    s0 += part[2][i];
   }
   // sequence by sequence: its first chunk, its begin and its segments
+  int* const first = in_lds ? first_l : s.first_chunk;
+  int* const begin = in_lds ? begin_l : s.begin;
   run = run0;
-  int c0 = sum.x, s0 = sum.y;
   for (int b = b0; b < b1; ++b) {
     int e = clampi(s.offsets[b + 1], 0, s.n);
     if (e < run) e = run;
     const int c = (int)(((int64_t)(e - run) + kChunk - 1) / kChunk);
-    s.first_chunk[b] = c0;
-    s.begin[b] = run;
+    first[b] = c0;
+    begin[b] = run;
     const int k = c > 0 ? (c + s.seg_chunks - 1) / s.seg_chunks : 1;
     for (int i = 0; i < k; ++i) {
       const int f = i * s.seg_chunks;
@@ -75,15 +90,15 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
     s0 += k;
     run = e;
     if (b == s.n_seq - 1) {
-      s.first_chunk[s.n_seq] = c0;
-      s.begin[s.n_seq] = e;
-      sh[0][0] = s0;
+      first[s.n_seq] = c0;
+      begin[s.n_seq] = e;
+      segs_l = s0;
     }
   }
   __syncthreads();
   __threadfence_block();
-  const int all = s.first_chunk[s.n_seq], segs = sh[0][0];
-  for (int i = segs + t; i < s.n_segs; i += 1024) s.segs[i] = int4{0, -1, 0, 0};
+  const int all = first[s.n_seq];
+  for (int i = segs_l + t; i < s.n_segs; i += 1024) s.segs[i] = int4{0, -1, 0, 0};
   for (int ci = t; ci < s.n_chunks; ci += 1024) {
     if (ci >= all) {
       s.chunks[ci] = int4{0, 0, 0, 0};
@@ -92,10 +107,10 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
     int lo = 0, hi = s.n_seq;  // the last sequence whose first chunk is at most ci
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s.first_chunk[mid] <= ci) lo = mid; else hi = mid;
+      if (first[mid] <= ci) lo = mid; else hi = mid;
     }
-    const int at = s.begin[lo] + kChunk * (ci - s.first_chunk[lo]);
-    const int left = s.begin[lo + 1] - at;
+    const int at = begin[lo] + kChunk * (ci - first[lo]);
+    const int left = begin[lo + 1] - at;
     s.chunks[ci] = int4{at, left < kChunk ? left : kChunk, lo, 0};
   }
 }

@@ -14,15 +14,22 @@ namespace zm {
 namespace {
 
 constexpr int kNormWaves = 4;  // waves of a workgroup
-constexpr int64_t kMaxNormBlocks = 1 << 22;  // more rows than these take are looped over
+// Workgroups of the forward pass: 4 to a compute unit go over the rows, gamma and beta
+// in registers and the next row read ahead.  40001 fp32 rows of 2048 (655 MB): 127 us,
+// 5.2 TB/s; 128 with 8, 133 with 6, 192 with a workgroup to every two rows, 220 with
+// that and gamma and beta read for every row.
+constexpr int64_t kMaxNormBlocks = kTargetWgs * 4;
 
 template <typename T>
 struct Piece;
 template <>
 struct Piece<uint16_t> {
   static constexpr int E = 8;
+  typedef u32x4 Raw;
   static __device__ __forceinline__ void load(const uint16_t* p, float* v) {
-    const u32x4 w = *(const u32x4*)p;
+    unpack(*(const u32x4*)p, v);
+  }
+  static __device__ __forceinline__ void unpack(u32x4 w, float* v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = bf16lo(w[i]);
@@ -39,8 +46,11 @@ struct Piece<uint16_t> {
 template <>
 struct Piece<float> {
   static constexpr int E = 4;
+  typedef f32x4 Raw;
   static __device__ __forceinline__ void load(const float* p, float* v) {
-    const f32x4 w = *(const f32x4*)p;
+    unpack(*(const f32x4*)p, v);
+  }
+  static __device__ __forceinline__ void unpack(f32x4 w, float* v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = w[i];
   }
@@ -74,29 +84,48 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm(
     const float* __restrict__ beta, float eps, T* y, int64_t ldy, float* __restrict__ stats,
     int width, int64_t n) {
   constexpr int E = Piece<T>::E, RPG = kNormWaves / WPR;
+  typedef typename Piece<T>::Raw Raw;
   __shared__ float red[4][kNormWaves];
   const int lane = threadIdx.x % (64 * WPR), row = threadIdx.x / (64 * WPR);
   const float inv = 1.f / (float)width;
-  int turn = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * RPG; t0 < n; t0 += (int64_t)gridDim.x * RPG, turn ^= 2) {
-    const int64_t t = t0 + row;
-    const bool live = t < n;  // a dead row's waves still meet the barriers
-    float v[NP][E];
+  const int64_t step = (int64_t)gridDim.x * RPG;
+  int64_t t0 = (int64_t)blockIdx.x * RPG;
+  Raw raw[NP];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const int c = E * (lane + 64 * WPR * p);
-      if (live && c < width) {
-        Piece<T>::load(x + t * ldx + c, v[p]);
+      if (t < n && c < width) raw[p] = *(const Raw*)(x + t * ldx + c);
+    }
+  };
+  fetch(t0 + row);
+  float gm[NP][E], bt[NP][E];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int c = E * (lane + 64 * WPR * p);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      gm[p][e] = gamma && c < width ? gamma[c + e] : 1.f;
+      bt[p][e] = beta && c < width ? beta[c + e] : 0.f;
+    }
+  }
+  int turn = 0;
+  for (; t0 < n; t0 += step, turn ^= 2) {
+    const int64_t t = t0 + row;  // a wave past the rows still meets the barriers
+    float v[NP][E];
+    float s = 0.f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      if (t < n && E * (lane + 64 * WPR * p) < width) {
+        Piece<T>::unpack(raw[p], v[p]);
       } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) v[p][e] = 0.f;
       }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
 #pragma unroll
       for (int e = 0; e < E; ++e) s += v[p][e];
+    }
+    fetch(t + step);
     const float mean = row_sum<WPR>(s, red[turn]) * inv;
     s = 0.f;
 #pragma unroll
@@ -109,7 +138,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm(
       }
     }
     const float r = 1.f / sqrtf(row_sum<WPR>(s, red[turn + 1]) * inv + eps);
-    if (!live) continue;
+    if (t >= n) continue;
     if (stats && lane == 0) {
       stats[t] = mean;
       stats[n + t] = r;
@@ -119,12 +148,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm(
       const int c = E * (lane + 64 * WPR * p);
       if (c >= width) break;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float o = v[p][e] * r;
-        if (gamma) o *= gamma[c + e];
-        if (beta) o += beta[c + e];
-        v[p][e] = o;
-      }
+      for (int e = 0; e < E; ++e) v[p][e] = fmaf(v[p][e] * r, gm[p][e], bt[p][e]);
       Piece<T>::store(y + t * ldy + c, v[p]);
     }
   }
@@ -229,21 +253,29 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm_backward(
   for (int c = threadIdx.x; c < 2 * width; c += 64 * kNormWaves) out[c] = sums[c];
 }
 
-// dgamma | dbeta from the slots: 16 columns x 16 groups of slots a workgroup,
-// each group's slots in order and then the groups in order.
-__global__ __launch_bounds__(256) void k_norm_param_sum(const float* __restrict__ part, int slots,
-                                                        int width, float* __restrict__ dgamma,
-                                                        float* __restrict__ dbeta) {
-  __shared__ float red[16][17];
+// dgamma | dbeta from the slots: 16 columns x 64 groups of slots a workgroup, each
+// group's slots in order and then the groups in order.
+__global__ __launch_bounds__(1024) void k_norm_param_sum(const float* __restrict__ part, int slots,
+                                                         int width, float* __restrict__ dgamma,
+                                                         float* __restrict__ dbeta) {
+  __shared__ float red[64][17];
   const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
   const int c = blockIdx.x * 16 + col;  // 2 * width is a multiple of 16
   float s = 0.f;
-  for (int i = grp; i < slots; i += 16) s += part[(int64_t)i * 2 * width + c];
+#pragma unroll 4
+  for (int i = grp; i < slots; i += 64) s += part[(int64_t)i * 2 * width + c];
   red[grp][col] = s;
+  __syncthreads();
+  if (grp < 8) {
+    s = red[8 * grp][col];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[8 * grp + i][col];
+    red[8 * grp][col] = s;
+  }
   __syncthreads();
   if (grp) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) s += red[i][col];
+  for (int i = 1; i < 8; ++i) s += red[8 * i][col];
   float* const out = c < width ? dgamma : dbeta;
   if (out) out[c < width ? c : c - width] = s;
 }
@@ -311,7 +343,7 @@ hipError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* 
     if (e != hipSuccess) return e;
   }
   if (!params) return hipSuccess;
-  hipLaunchKernelGGL(k_norm_param_sum, dim3(2 * width / 16), dim3(256), 0, st, part,
+  hipLaunchKernelGGL(k_norm_param_sum, dim3(2 * width / 16), dim3(1024), 0, st, part,
                      n > 0 ? norm_slots(n) : 0, width, dgamma, dbeta);
   return hipGetLastError();
 }
