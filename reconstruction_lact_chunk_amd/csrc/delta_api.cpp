@@ -80,6 +80,10 @@ DeltaSeqs seqs(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, const int*
   s.n_chunks = p.n_chunks;
   s.n_segs = p.n_segs;
   s.seg_chunks = p.seg_chunks;
+  // With more workgroups than compute units the long ones start first, so that they do
+  // not end last: 61 sequences of 6 to 24 chunks, 16 heads, 510 -> 430 us.
+  s.longest_first = !p.split && d->n_seq > 1 && d->n_seq <= kTableLds &&
+                    (int64_t)d->n_seq * d->heads > kTargetWgs;
   if (d->n_seq > 1) {
     s.chunks = c.take<int4>(p.n_chunks);
     s.segs = c.take<int4>(p.n_segs);

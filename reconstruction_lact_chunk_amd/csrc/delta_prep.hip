@@ -15,10 +15,9 @@ constexpr int kBlk = 336;      // floats of a 16 x 16 diagonal block (rows of 20
 // and segments, then every chunk's and segment's entry by a search in them.  A chain
 // of dependent steps, so scans run within waves and the searches in LDS where the
 // sequences fit it.
-constexpr int kTableLds = 1024;  // sequences
-
 __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
   __shared__ int part[3][16], first_l[kTableLds + 1], begin_l[kTableLds + 1], segs_l;
+  __shared__ int len_l[kTableLds];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, per = (s.n_seq + 1023) / 1024;
   const bool in_lds = s.n_seq <= kTableLds;
   const int b0 = t * per, b1 = b0 + per < s.n_seq ? b0 + per : s.n_seq;
@@ -50,6 +49,7 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
     ns += c > 0 ? (c + s.seg_chunks - 1) / s.seg_chunks : 1;
     run = e;
   }
+  if (s.longest_first && t < s.n_seq) len_l[t] = nc;
   int c0 = nc, s0 = ns;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
@@ -69,6 +69,11 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
   for (int i = 0; i < w; ++i) {
     c0 += part[1][i];
     s0 += part[2][i];
+  }
+  // where a sequence is one segment: its place by length, then by number
+  if (s.longest_first && t < s.n_seq) {
+    s0 = 0;
+    for (int b = 0; b < s.n_seq; ++b) s0 += len_l[b] > nc || (len_l[b] == nc && b < t);
   }
   // sequence by sequence: its first chunk, its begin and its segments
   int* const first = in_lds ? first_l : s.first_chunk;
@@ -92,7 +97,7 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
     if (b == s.n_seq - 1) {
       first[s.n_seq] = c0;
       begin[s.n_seq] = e;
-      segs_l = s0;
+      segs_l = s.longest_first ? s.n_seq : s0;
     }
   }
   __syncthreads();

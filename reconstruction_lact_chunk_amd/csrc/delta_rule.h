@@ -33,6 +33,7 @@ namespace zm {
 constexpr int kChunk = 64;             // tokens of a chunk
 constexpr int kTriFrags = 6;           // 16 x 32 operand tiles of a 64 x 64 triangle
 constexpr int kFragElems = 64 * 8;     // bf16 elements of one such tile
+constexpr int kTableLds = 1024;        // sequences that the table's kernel keeps in LDS
 constexpr float kMinLogDecay = -128.f; // exp of less is 0 in fp32
 
 // Where the sequences lie.  Without a table (one sequence) a chunk follows from
@@ -48,6 +49,7 @@ struct DeltaSeqs {
   int n, n_seq;
   int n_chunks, n_segs;  // upper bounds over every content of offsets
   int seg_chunks;        // chunks of a segment
+  bool longest_first;    // segments (one to a sequence) in the order of their chunks
 };
 
 struct DeltaTokens {
