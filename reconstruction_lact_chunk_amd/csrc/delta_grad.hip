@@ -290,7 +290,7 @@ __device__ __forceinline__ bf16x8 read_tr8(const uint16_t* at) {
 // slice.  The 16 x 16 tiles of the triangles go round the waves on the way; W and E
 // are then shared through LDS for the products with K and Q.
 template <int D, bool F32>
-__global__ __launch_bounds__(4 * D, 1) void k_delta_grads(DeltaArgs a, DeltaGradArgs s) {
+__global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGradArgs s) {
   using T = typename Tok<F32>::T;
   constexpr int NT = Tok<F32>::NT, KS = D / 32, MT = D / 16, NW = NT == 1 ? 2 : 3, THR = 4 * D;
   constexpr int SETS = 512 / THR, TPW = (12 + MT - 1) / MT;
@@ -345,18 +345,10 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_grads(DeltaArgs a, DeltaGrad
     mr[3] = *(const f32x4*)(m1 + 32 * sl + 4);
   };
   load(0);
-  if (w == 0) {
-    float gl = lane < count ? a.g[((int64_t)ch.x + lane) * a.heads + h] : 0.f;
-    if (gl < kMinLogDecay) gl = kMinLogDecay;
-    double sum = gl;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-      const double o = __shfl_up(sum, m, 64);
-      if (lane >= m) sum += o;
-    }
-    cs[lane] = sum;
-  }
-  if (threadIdx.x < 3 * kChunk) rows[threadIdx.x] = a.rows[slot * 3 * kChunk + threadIdx.x];
+  constexpr int SUMS = MT - 1;  // the wave of the sums over tokens: it has fewest tiles below
+  float gl = 0.f, rv = 0.f;
+  if (w == SUMS && lane < count) gl = a.g[((int64_t)ch.x + lane) * a.heads + h];
+  if (threadIdx.x < 3 * kChunk) rv = a.rows[slot * 3 * kChunk + threadIdx.x];
 
   f32x4 dq[4], dk[4], au[4];             // dims 16 w + 4 g + r, tokens 16 tt + c
   f32x4 pt[TPW], xt[TPW], kk[TPW], qk[TPW];  // U dO^T, U dX^T, K K^T, K Q^T: tokens j, i
@@ -385,6 +377,18 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_grads(DeltaArgs a, DeltaGrad
     for (int e = 0; e < 4; ++e) fr = fmaf(mr[0][e], mr[2][e], fmaf(mr[1][e], mr[3][e], fr));
     if (sl + 1 < KS) load(sl + 1);
     lds_barrier();
+    if (sl == 0) {  // out of the way of the first slice
+      if (threadIdx.x < 3 * kChunk) rows[threadIdx.x] = rv;
+      if (w == SUMS) {
+        double sum = gl < kMinLogDecay ? kMinLogDecay : gl;
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+          const double o = __shfl_up(sum, m, 64);
+          if (lane >= m) sum += o;
+        }
+        cs[lane] = sum;
+      }
+    }
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
       mma<2>(dq[tt], p0, slice_frag<NT>(buf + 6 * kSlice, tt, lane));
@@ -450,22 +454,18 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_grads(DeltaArgs a, DeltaGrad
     const int it = id >= 10 ? 2 * (id - 10) : (id < 1 ? 0 : (id < 3 ? 1 : (id < 6 ? 2 : 3)));
     const int jt = id >= 10 ? it + 1 : id - it * (it + 1) / 2;
     const int i = 16 * it + c;
+    const double sum_i = cs[i];
+    const float beta = rows[2 * kChunk + i];
     float wv[4], ev[4], si = 0.f, sx = 0.f, sj[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int j = 16 * jt + 4 * g + r;
-      wv[r] = ev[r] = sj[r] = 0.f;
-      if (j <= i) {
-        const float gd = expf((float)(cs[i] - cs[j]));
-        wv[r] = a.scale * gd * pt[n][r];
-        if (j < i) {
-          const float x = gd * xt[n][r];
-          ev[r] = -rows[2 * kChunk + i] * x;
-          sx = fmaf(x, kk[n][r], sx);
-          sj[r] = fmaf(wv[r], qk[n][r], ev[r] * kk[n][r]);
-          si += sj[r];
-        }
-      }
+      const float gd = expf(j <= i ? (float)(sum_i - cs[j]) : 0.f), x = j < i ? gd * xt[n][r] : 0.f;
+      wv[r] = j <= i ? a.scale * gd * pt[n][r] : 0.f;
+      ev[r] = -beta * x;
+      sx += j < i ? x * kk[n][r] : 0.f;
+      sj[r] = j < i ? fmaf(wv[r], qk[n][r], ev[r] * kk[n][r]) : 0.f;
+      si += sj[r];
     }
     const int at = (2 * it + (jt >> 1)) * kFragElems + (16 * (2 * (jt & 1) + (g >> 1)) + c) * 8 + 4 * (g & 1);
 #pragma unroll
@@ -564,7 +564,7 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_grads(DeltaArgs a, DeltaGrad
       store4(s.dk_part + (tok * a.heads + h) * D + col, dk[tt]);
     }
   }
-  if (w == 0) {
+  if (w == SUMS) {
     const int t = lane, it = t >> 4;
     float sq = 0.f, sx = 0.f, su = 0.f, sf = 0.f, xk = 0.f, tri = 0.f;
 #pragma unroll
@@ -574,11 +574,14 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_grads(DeltaArgs a, DeltaGrad
       su += red[2][i][t];
       sf += frs[i];
     }
-    for (int j = 0; j <= it; ++j) {
-      tri += tri_i[it * (it + 1) / 2 + j][t & 15];
-      xk += tri_x[it * (it + 1) / 2 + j][t & 15];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // its row of tiles, then its column
+      const int low = it * (it + 1) / 2 + (j <= it ? j : it), up = j < it ? it : j;
+      const float ti = tri_i[low][t & 15], tx = tri_x[low][t & 15], tj = tri_j[up * (up + 1) / 2 + it][t & 15];
+      tri += j <= it ? ti : 0.f;
+      xk += j <= it ? tx : 0.f;
+      tri -= j >= it ? tj : 0.f;
     }
-    for (int i = it; i < 4; ++i) tri -= tri_j[i * (i + 1) / 2 + it][t & 15];
     if (t < count) s.dbeta[((int64_t)ch.x + t) * a.heads + h] = xvs[t] - sx - xk;
     double sum = sq - rows[2 * kChunk + t] * sx - su + tri;
     float all = su;

@@ -251,9 +251,12 @@ __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs
   constexpr int KS = D / 32, SL = D / 16;
   __shared__ __attribute__((aligned(16))) uint16_t mp[2][KS][3][kFragElems];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int dv = 16 * (blockIdx.x % SL) + c;
-  const int h = (blockIdx.x / SL) % a.heads;
-  int si = blockIdx.x / SL / a.heads;
+  // the blocks of one segment and head 8 apart: on one XCD, whose L2 holds N for them
+  const int unit = 8 * (blockIdx.x / (8 * SL)) + blockIdx.x % 8;
+  const int dv = 16 * (blockIdx.x / 8 % SL) + c;
+  const int h = unit % a.heads;
+  int si = unit / a.heads;
+  if (si >= a.sq.n_segs) return;
   const int4 sg = delta_seg(a.sq, si);
   if (sg.y < 0 || !(sg.w & (REV ? 2 : 1))) return;
   const int64_t dd = (int64_t)D * D;
@@ -264,8 +267,7 @@ __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs
   // N's rows and what is added, kAhead segments ahead
   constexpr int kAhead = 3;
   f32x4 raw[kAhead][2 * KS], add[kAhead];
-  auto load = [&](int slot, int at_seg) {
-    const int sj = clampi(at_seg, 0, a.sq.n_segs - 1);
+  auto load = [&](int slot, int sj) {
     const int64_t at = (int64_t)sj * a.heads + h;
     const float* const nn = ja.trans + at * ja.stride * dd;
     add[slot] = *(const f32x4*)((REV ? ja.e + at * dd : nn + dd) + col);
@@ -277,9 +279,10 @@ __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs
     }
   };
   constexpr int kStep = REV ? -1 : 1;
+  int left = sg.w >> 2;  // segments to go: one product fewer
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(i, si + kStep * i);  // past the sequence: not used
-  int left = sg.w >> 2;  // segments to go
+  for (int i = 0; i < kAhead; ++i)
+    if (left > i + 1) load(i, si + kStep * i);
   while (true) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -299,7 +302,7 @@ __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs
 #pragma unroll
       for (int s = 0; s < KS; ++s) row[s] = split_tiles<3>(raw[i][2 * s], raw[i][2 * s + 1]);
       f32x4 acc[2] = {add[i], {0.f, 0.f, 0.f, 0.f}};
-      load(i, si + kStep * (kAhead - 1));
+      if (left > kAhead) load(i, si + kStep * kAhead - kStep);
       lds_barrier();  // the other buffer's readers are past it too
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
@@ -330,7 +333,8 @@ hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaScanArgs& s, hipStre
 }
 
 hipError_t launch_delta_join(const DeltaArgs& a, const DeltaJoinArgs& j, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads * (a.d / 16))), blk(4 * a.d);
+  const int64_t units = (int64_t)a.sq.n_segs * a.heads;
+  const dim3 grid((unsigned)(8 * ceil_div(units, 8) * (a.d / 16))), blk(4 * a.d);
   if (a.d == 128) {
     if (j.e) hipLaunchKernelGGL((k_delta_join<128, true>), grid, blk, 0, st, a, j);
     else hipLaunchKernelGGL((k_delta_join<128, false>), grid, blk, 0, st, a, j);
