@@ -306,7 +306,7 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
   const int4 ch = delta_chunk(a.sq, ci);
   const int count = ch.y;
   if (count == 0) return;
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int hk = h / (a.heads / a.heads_k);
   const int64_t slot = (int64_t)ci * a.heads + h, hd = (int64_t)a.heads * D;
   const T* const kp = (const T*)a.k.p + (int64_t)ch.x * a.k.ld + hk * D;
@@ -344,6 +344,30 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
     mr[2] = *(const f32x4*)(m1 + 32 * sl);
     mr[3] = *(const f32x4*)(m1 + 32 * sl + 4);
   };
+  auto put = [&](int sl) {
+    uint16_t* const buf = lds + (sl & 1) * BUF;
+    const bool live = st < count;
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) {
+      const bool second = SETS == 1 ? w >= 4 : i == 1;
+      const auto x = split_tiles<3>(xr[i][0], xr[i][1]);
+      put_frag(buf + (second ? 3 * kSlice : 0), w & 3, lane, live ? x : zero_parts<3>());
+      put_frag(second ? q_at(sl) : k_at(sl), w & 3, lane, live ? br[i].parts() : zero_parts<NT>());
+      if (second) {
+        put_frag(buf + 6 * kSlice, w & 3, lane, live ? cr[i].parts() : zero_parts<NT>());
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xv = fmaf(xr[i][e >> 2][e & 3], cr[i].at(e), xv);
+      }
+    }
+  };
+  Parts<3> p0, p1;
+  auto take = [&]() {
+    p0 = split_tiles<3>(mr[0], mr[1]);
+    p1 = split_tiles<3>(mr[2], mr[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) fr = fmaf(mr[0][e], mr[2][e], fmaf(mr[1][e], mr[3][e], fr));
+  };
   load(0);
   constexpr int SUMS = MT - 1;  // the wave of the sums over tokens: it has fewest tiles below
   float gl = 0.f, rv = 0.f;
@@ -356,26 +380,13 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
   for (int i = 0; i < 4; ++i) dq[i] = dk[i] = au[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < TPW; ++i) pt[i] = xt[i] = kk[i] = qk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  put(0);
+  take();
+  load(1);
+  // the next slice is split and written among this one's matrix instructions
 #pragma unroll
   for (int sl = 0; sl < KS; ++sl) {
     uint16_t* const buf = lds + (sl & 1) * BUF;
-#pragma unroll
-    for (int i = 0; i < SETS; ++i) {
-      const bool second = SETS == 1 ? w >= 4 : i == 1, live = st < count;
-      const auto x = live ? split_tiles<3>(xr[i][0], xr[i][1]) : zero_parts<3>();
-      put_frag(buf + (second ? 3 * kSlice : 0), w & 3, lane, x);
-      put_frag(second ? q_at(sl) : k_at(sl), w & 3, lane, live ? br[i].parts() : zero_parts<NT>());
-      if (second) {
-        put_frag(buf + 6 * kSlice, w & 3, lane, live ? cr[i].parts() : zero_parts<NT>());
-      } else if (live) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xv = fmaf(xr[i][e >> 2][e & 3], cr[i].at(e), xv);
-      }
-    }
-    const Parts<3> p0 = split_tiles<3>(mr[0], mr[1]), p1 = split_tiles<3>(mr[2], mr[3]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) fr = fmaf(mr[0][e], mr[2][e], fmaf(mr[1][e], mr[3][e], fr));
-    if (sl + 1 < KS) load(sl + 1);
     lds_barrier();
     if (sl == 0) {  // out of the way of the first slice
       if (threadIdx.x < 3 * kChunk) rows[threadIdx.x] = rv;
@@ -394,7 +405,10 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
       mma<2>(dq[tt], p0, slice_frag<NT>(buf + 6 * kSlice, tt, lane));
       mma<2>(dk[tt], p0, slice_frag<3>(buf, tt, lane));
       mma<2>(au[tt], p1, slice_frag<3>(buf + 3 * kSlice, tt, lane));
+      if (tt == 1 && sl + 1 < KS) put(sl + 1);
     }
+    if (sl + 1 < KS) take();
+    if (sl + 2 < KS) load(sl + 2);
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       const int id = w + MT * i, it = id < 1 ? 0 : (id < 3 ? 1 : (id < 6 ? 2 : 3));
@@ -496,7 +510,7 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
       for (int r = 0; r < 4; ++r) tri_j[id][4 * g + r] = sj[r];
     }
   }
-  xv = sum_groups(xv);
+  xv = sum_groups(st < count ? xv : 0.f);
   if (w < 4 && g == 0) xvs[16 * w + c] = xv;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) fr += __shfl_xor(fr, m, 64);
