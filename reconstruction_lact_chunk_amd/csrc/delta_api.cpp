@@ -150,8 +150,8 @@ BackwardWs backward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, co
   }
   f.m_in = c.take<float>(slots * dd);
   f.d_m = c.take<float>(slots * dd);
-  f.u = c.take<float>(rows);
-  f.x = c.take<float>(rows);
+  f.u = c.take<float>(slots * kChunk * d->d_head);
+  f.x = c.take<float>(slots * kChunk * d->d_head);
   if (d->heads != d->heads_k) {
     f.dq = c.take<float>(rows);
     f.dk = c.take<float>(rows);

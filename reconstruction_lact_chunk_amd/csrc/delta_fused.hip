@@ -654,11 +654,11 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
     if (MODE == kKeep) {
       const float f = rows[kScale0];
       char* const mo = (char*)(sa.m_out + ((int64_t)(sg.x + j) * a.heads + h) * dd);
-      const unsigned m_off = (unsigned)(8 * g * D + dv) * 4u;
+      const unsigned m_off = (unsigned)((dv >> 5) * D * 32 + 8 * g * 32 + (dv & 31)) * 4u;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) *(float*)(mo + dim_row(mt, r) * D * 4 + m_off) = f * m[mt][r];
+        for (int r = 0; r < 4; ++r) *(float*)(mo + dim_row(mt, r) * 128 + m_off) = f * m[mt][r];
     }
     read_m(m, C::Q);
     form_x(true);
@@ -678,16 +678,15 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
       lds_barrier();
     }
     if (MODE == kKeep) {
-      char* const uo = (char*)(sa.u_out + ((tok0 + (int64_t)kChunk * j) * a.heads + h) * D);
-      const unsigned u_off = (unsigned)(lt * a.heads * D + dv) * 4u;
+      char* const uo = (char*)(sa.u_out + ((int64_t)(sg.x + j) * a.heads + h) * kChunk * D);
+      const unsigned u_off = (unsigned)((dv >> 5) * kChunk * 32 + lt * 32 + (dv & 31)) * 4u;
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         const f32x4 fo = *(const f32x4*)(rows + kRowO + token_row(it, 4 * g));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = token_row(it, r);
-          char* const at = uo + (int64_t)t * a.heads * D * 4;
-          if (lt + t < count) *(float*)(at + u_off) = fo[r] * u[it][r];
+          if (lt + t < count) *(float*)(uo + t * 128 + u_off) = fo[r] * u[it][r];
         }
       }
     }

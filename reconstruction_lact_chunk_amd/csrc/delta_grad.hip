@@ -164,11 +164,11 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_reverse(DeltaArgs a, DeltaGr
 
     if (!TRANS) {
       float* const mo = s.d_m + slot * dd;
-      const int at = pinned(dim_row(0, 4 * g) * D + dv);
+      const int at = pinned((dv >> 5) * D * 32 + dim_row(0, 4 * g) * 32 + (dv & 31));
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) *elem(mo, at + (dim_row(mt, 0) + r) * D) = m[mt][r];
+        for (int r = 0; r < 4; ++r) *elem(mo, at + (dim_row(mt, 0) + r) * 32) = m[mt][r];
     }
     // dU = dec o (K dM') + P^T dO
     f32x4 du[4];
@@ -201,7 +201,7 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_reverse(DeltaArgs a, DeltaGr
     }
     // dV, and the factors of the state's step: scale gam o dO and -gam o beta o dX
     T* const vp = (T*)s.dv + first * s.ld_dv + h * D;
-    float* const xp = s.x + (first * a.heads + h) * D;
+    float* const xp = s.x + slot * kChunk * D + (dv >> 5) * kChunk * 32 + (dv & 31);
     const int tg = pinned(token_row(0, 4 * g));
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_reverse(DeltaArgs a, DeltaGr
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (!TRANS && t0 + r < count) {
-          *elem(xp, (t0 + r) * (unsigned)(a.heads * D) + dv) = x[it][r];
+          xp[(t0 + r) * 32] = x[it][r];
           store1(elem(vp, (t0 + r) * (unsigned)s.ld_dv + dv), be[r] * x[it][r]);
         }
         x[it][r] *= -gm[r] * be[r];
@@ -308,15 +308,15 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
   if (count == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int hk = h / (a.heads / a.heads_k);
-  const int64_t slot = (int64_t)ci * a.heads + h, hd = (int64_t)a.heads * D;
+  const int64_t slot = (int64_t)ci * a.heads + h;
   const T* const kp = (const T*)a.k.p + (int64_t)ch.x * a.k.ld + hk * D;
   const T* const qp = (const T*)a.q.p + (int64_t)ch.x * a.q.ld + hk * D;
   const T* const vp = (const T*)a.v.p + (int64_t)ch.x * a.v.ld + h * D;
   const T* const op = (const T*)s.d_o.p + (int64_t)ch.x * s.d_o.ld + h * D;
-  const float* const up = s.u + ((int64_t)ch.x * a.heads + h) * D;
-  const float* const xp = s.x + ((int64_t)ch.x * a.heads + h) * D;
-  const float* const m0 = s.m_in + slot * D * D + (16 * w + c) * D + 8 * g;
-  const float* const m1 = s.d_m + slot * D * D + (16 * w + c) * D + 8 * g;
+  const float* const up = s.u + slot * kChunk * D + 8 * g;
+  const float* const xp = s.x + slot * kChunk * D + 8 * g;
+  const float* const m0 = s.m_in + slot * D * D + (16 * w + c) * 32 + 8 * g;
+  const float* const m1 = s.d_m + slot * D * D + (16 * w + c) * 32 + 8 * g;
   auto k_at = [&](int sl) { return F32 ? lds + (sl & 1) * BUF + 9 * kSlice : lds + 2 * BUF + sl * kSlice; };
   auto q_at = [&](int sl) {
     return F32 ? lds + (sl & 1) * BUF + 12 * kSlice : lds + 2 * BUF + (KS + sl) * kSlice;
@@ -333,16 +333,16 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
 #pragma unroll
     for (int i = 0; i < SETS; ++i) {
       const bool second = SETS == 1 ? w >= 4 : i == 1;
-      const float* const f = (second ? up : xp) + srow * hd + col;
+      const float* const f = (second ? up : xp) + sl * kChunk * 32 + srow * 32;
       xr[i][0] = *(const f32x4*)f;
       xr[i][1] = *(const f32x4*)(f + 4);
       br[i].load((second ? qp + srow * a.q.ld : kp + srow * a.k.ld) + col);
       cr[i].load((second ? op + srow * s.d_o.ld : vp + srow * a.v.ld) + col);
     }
-    mr[0] = *(const f32x4*)(m0 + 32 * sl);
-    mr[1] = *(const f32x4*)(m0 + 32 * sl + 4);
-    mr[2] = *(const f32x4*)(m1 + 32 * sl);
-    mr[3] = *(const f32x4*)(m1 + 32 * sl + 4);
+    mr[0] = *(const f32x4*)(m0 + 32 * D * sl);
+    mr[1] = *(const f32x4*)(m0 + 32 * D * sl + 4);
+    mr[2] = *(const f32x4*)(m1 + 32 * D * sl);
+    mr[3] = *(const f32x4*)(m1 + 32 * D * sl + 4);
   };
   auto put = [&](int sl) {
     uint16_t* const buf = lds + (sl & 1) * BUF;

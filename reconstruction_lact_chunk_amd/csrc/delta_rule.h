@@ -82,8 +82,8 @@ struct DeltaScanArgs {
   bool both;
   void* o;
   int64_t ld_o;
-  float* m_out;             // [n_chunks][heads][d][d]: M at each chunk's start (backward), as [d_k][d_v]
-  float* u_out;             // [n][heads][d] (backward)
+  float* m_out;             // [n_chunks][heads][d][d]: M at each chunk's start (backward), as below
+  float* u_out;             // U (backward), as below
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
@@ -239,10 +239,12 @@ struct DeltaGradArgs {
   float* dstate_in;          // receives the gradient of the first states, or null
   const float* seg_end;      // [n_segs][heads][d][d]: gradients of the states at the segments' ends, or null
   float* e_out;              // [n_segs][heads][d][d]: pass of transitions only
-  const float* m_in;         // [n_chunks][heads][d][d] M at each chunk's start, as [d_k][d_v]
+  // Of a chunk and head, 32 columns of d_v after the other, as k_delta_grads takes them
+  // (rows of all of d_v would be read in pieces far apart):
+  const float* m_in;         // [n_chunks][heads][d / 32][d_k][32] M at each chunk's start
   float* d_m;                // the same of the gradient of M at each chunk's end
-  const float* u;            // [n][heads][d]
-  float* x;                  // [n][heads][d]: gradient of beta o R
+  const float* u;            // [n_chunks][heads][d / 32][kChunk][32]
+  float* x;                  // the same of the gradient of beta o R
   void* dv;
   int64_t ld_dv;
   void* dq;                  // with one value head to a key head, else null

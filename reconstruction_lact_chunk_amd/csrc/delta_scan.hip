@@ -77,7 +77,7 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          *(f32x2*)(mo + (int64_t)dim_row(mt, 4 * g + r) * D + dv) =
+          *(f32x2*)(mo + (dv >> 5) * D * 32 + dim_row(mt, 4 * g + r) * 32 + (dv & 31)) =
               f32x2{m[mt][0][r], m[mt][1][r]};
     }
 
@@ -138,14 +138,14 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
       }
     }
     if (MODE == kKeep) {
-      float* const uo = sa.u_out + ((int64_t)ch.x * a.heads + h) * D + dv;
+      float* const uo = sa.u_out + slot * kChunk * D + (dv >> 5) * kChunk * 32 + (dv & 31);
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = token_row(it, 4 * g + r);
           if (t < count)
-            *(f32x2*)(uo + (int64_t)t * a.heads * D) = f32x2{u[it][0][r], u[it][1][r]};
+            *(f32x2*)(uo + t * 32) = f32x2{u[it][0][r], u[it][1][r]};
         }
     }
     if (MODE == kOutputs) {
