@@ -736,11 +736,11 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int dk = dim_row(mt, 4 * g);
-      // N by rows for the join, B as a state, and N by columns for the join on the way back
+      // N and B for the join, and N's transpose for the one on the way back
 #pragma unroll
-      for (int r = 0; r < 4; ++r) to[(int64_t)(dk + r) * D + dv] = e[mt][r];
-      *(f32x4*)(to + dd + (int64_t)dv * D + dk) = m[mt];
-      if (sa.both) *(f32x4*)(to + 2 * dd + (int64_t)dv * D + dk) = e[mt];
+      for (int r = 0; r < 4; ++r) to[join_n<D>(dk + r, dv)] = e[mt][r];
+      *(f32x4*)(to + dd + join_b<D>(dv, mt, g)) = m[mt];
+      if (sa.both) *(f32x4*)(to + 2 * dd + join_n<D>(dv, dk)) = e[mt];
     }
   } else if ((sg.w & 2) && sa.state_out) {
     float* const out = sa.state_out + ((int64_t)sg.z * a.heads + h) * dd + (int64_t)dv * D;

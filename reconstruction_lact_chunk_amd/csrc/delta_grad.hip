@@ -237,7 +237,8 @@ __global__ __launch_bounds__(4 * D, 1) void k_delta_reverse(DeltaArgs a, DeltaGr
   else if ((sg.w & 1) && s.dstate_in) out = s.dstate_in + ((int64_t)sg.z * a.heads + h) * dd;
   if (out) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) *(f32x4*)(out + (int64_t)dv * D + dim_row(mt, 4 * g)) = m[mt];
+    for (int mt = 0; mt < MT; ++mt)
+      *(f32x4*)(out + (TRANS ? join_b<D>(dv, mt, g) : dv * D + dim_row(mt, 4 * g))) = m[mt];
   }
 }
 

@@ -77,8 +77,8 @@ struct DeltaScanArgs {
   const float* state_in;    // [n_seq][heads][d][d] or null (zeros)
   float* state_out;         // the same, or null
   const float* seg_start;   // [n_segs][heads][d][d]: states at the segments' starts, or null
-  float* trans;             // pass of transitions: [n_segs][heads][2 or 3][d][d]: N by rows, B as a
-                            // state and, with both, N by columns
+  float* trans;             // pass of transitions: [n_segs][heads][2 or 3][d][d]: N, B and, with both,
+                            // the transpose of N, as join_n and join_b place them
   bool both;
   void* o;
   int64_t ld_o;
@@ -129,6 +129,17 @@ __device__ __forceinline__ constexpr int token_row(int it, int m) {
 // Head dim of row m of state tile mt.
 __device__ __forceinline__ constexpr int dim_row(int mt, int m) {
   return 32 * (mt >> 1) + 8 * (m >> 2) + 4 * (mt & 1) + (m & 3);
+}
+// Where the join of segments finds element (row, col) of N, and the four of a state
+// from (dim_row(mt, 4 g), column dv): as one load of a wave each.
+template <int D>
+__device__ __forceinline__ int join_n(int row, int col) {
+  const int mt = 2 * (row >> 5) + ((row >> 2) & 1), m = 4 * ((row >> 3) & 3) + (row & 3);
+  return ((mt * (D / 16) + (col >> 5) * 2 + ((col >> 2) & 1)) * 64 + 16 * ((col >> 3) & 3) + m) * 4 + (col & 3);
+}
+template <int D>
+__device__ __forceinline__ int join_b(int dv, int mt, int g) {
+  return (((dv >> 4) * (D / 16) + mt) * 64 + 16 * g + (dv & 15)) * 4;
 }
 // Operand tile (it, ts) of a lower (T, P) or upper (transposed) triangle.
 __device__ __forceinline__ constexpr int low_frag(int it, int ts) { return it < 2 ? it : 2 * it - 2 + ts; }
@@ -228,7 +239,7 @@ struct DeltaJoinArgs {
   const float* init;     // [n_seq][heads][d][d] or null
   const float* trans;
   int stride;            // matrices to a segment of trans
-  const float* e;        // the way back: what a segment adds, else null
+  const float* e;        // the way back: what a segment adds (join_b), else null
   float* to;             // [n_segs][heads][d][d]
 };
 
@@ -238,7 +249,7 @@ struct DeltaGradArgs {
   const float* dstate_out;   // gradient of the last states, or null
   float* dstate_in;          // receives the gradient of the first states, or null
   const float* seg_end;      // [n_segs][heads][d][d]: gradients of the states at the segments' ends, or null
-  float* e_out;              // [n_segs][heads][d][d]: pass of transitions only
+  float* e_out;              // [n_segs][heads][d][d] (join_b): pass of transitions only
   // Of a chunk and head, 32 columns of d_v after the other, as k_delta_grads takes them
   // (rows of all of d_v would be read in pieces far apart):
   const float* m_in;         // [n_chunks][heads][d / 32][d_k][32] M at each chunk's start

@@ -212,30 +212,30 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
   float* out = nullptr;
   if (MODE == kTransition)
     out = sa.trans + ((int64_t)si * a.heads + h) * (sa.both ? 3 : 2) * dd + (unit ? 2 : 1) * dd;
-  if (unit) {  // N by rows for the join, and by columns for the one on the way back
+  if (unit) {  // N for the join, and its transpose for the one on the way back
     if (sa.both) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct)
-          *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+          *(f32x4*)(out + join_n<D>(dv + ct, dim_row(mt, 4 * g))) = m[mt][ct];
     }
     out -= 2 * dd;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        *(f32x2*)(out + (int64_t)dim_row(mt, 4 * g + r) * D + dv) = f32x2{m[mt][0][r], m[mt][1][r]};
+        *(f32x2*)(out + join_n<D>(dim_row(mt, 4 * g + r), dv)) = f32x2{m[mt][0][r], m[mt][1][r]};
     return;
   }
-  if (MODE == kTransition) {
-  } else if ((sg.w & 2) && sa.state_out) out = sa.state_out + ((int64_t)sg.z * a.heads + h) * dd;
+  if (MODE != kTransition && (sg.w & 2) && sa.state_out) out = sa.state_out + ((int64_t)sg.z * a.heads + h) * dd;
   if (out) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int ct = 0; ct < 2; ++ct)
-        *(f32x4*)(out + (int64_t)(dv + ct) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+        *(f32x4*)(out + (MODE == kTransition ? join_b<D>(dv + ct, mt, g)
+                                             : (dv + ct) * D + dim_row(mt, 4 * g))) = m[mt][ct];
   }
 }
 
@@ -244,12 +244,14 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
 // blocks of a sequence's first (last) segment go through all of its segments, one
 // for each 16 columns of a head; wave w forms rows dim_row(w, .).  Each step is one
 // product that waits for the step before, so all else is out of the way: N's rows
-// are loaded and split a step ahead, and M passes between the waves as operand
-// parts in LDS.
+// are loaded three steps ahead, M passes between the waves through LDS, and the
+// product takes both in fp32 (v_mfma_f32_16x16x4_f32, row 8 g + e of a 32-row step in
+// slot g of instruction e): twice the time on the matrix cores of bf16 parts, but
+// splitting N's rows, once for every 16 columns, took longer than that.
 template <int D, bool REV>
 __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs ja) {
   constexpr int KS = D / 32, SL = D / 16;
-  __shared__ __attribute__((aligned(16))) uint16_t mp[2][KS][3][kFragElems];
+  __shared__ __attribute__((aligned(16))) f32x4 mp[2][SL][64];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   // the blocks of one segment and head 8 apart: on one XCD, whose L2 holds N for them
   const int unit = 8 * (blockIdx.x / (8 * SL)) + blockIdx.x % 8;
@@ -270,13 +272,10 @@ __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs
   auto load = [&](int slot, int sj) {
     const int64_t at = (int64_t)sj * a.heads + h;
     const float* const nn = ja.trans + at * ja.stride * dd;
-    add[slot] = *(const f32x4*)((REV ? ja.e + at * dd : nn + dd) + col);
-    const float* const r = nn + (REV ? 2 * dd : 0) + (int64_t)dim_row(w, c) * D + 8 * g;
+    add[slot] = *(const f32x4*)((REV ? ja.e + at * dd : nn + dd) + join_b<D>(dv, w, g));
+    const float* const r = nn + (REV ? 2 * dd : 0) + (w * SL * 64 + lane) * 4;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      raw[slot][2 * s] = *(const f32x4*)(r + 32 * s);
-      raw[slot][2 * s + 1] = *(const f32x4*)(r + 32 * s + 4);
-    }
+    for (int s = 0; s < SL; ++s) raw[slot][s] = *(const f32x4*)(r + s * 256);
   };
   constexpr int kStep = REV ? -1 : 1;
   int left = sg.w >> 2;  // segments to go: one product fewer
@@ -289,29 +288,26 @@ __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs
       *(f32x4*)(ja.to + ((int64_t)si * a.heads + h) * dd + col) = m;
       if (--left <= 0) return;
       si += kStep;
-      uint16_t(*const buf)[3][kFragElems] = mp[turn];
+      f32x4(*const buf)[64] = mp[turn];
       turn ^= 1;
-      float x[8] = {m[0], m[1], m[2], m[3], 0.f, 0.f, 0.f, 0.f};
-      const Parts<3> p = split8<3>(x);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const u32x4 v = __builtin_bit_cast(u32x4, p.p[k]);
-        *(u32x2*)(buf[w >> 1][k] + lane * 8 + 4 * (w & 1)) = u32x2{v[0], v[1]};
-      }
-      Parts<3> row[KS];
-#pragma unroll
-      for (int s = 0; s < KS; ++s) row[s] = split_tiles<3>(raw[i][2 * s], raw[i][2 * s + 1]);
-      f32x4 acc[2] = {add[i], {0.f, 0.f, 0.f, 0.f}};
-      if (left > kAhead) load(i, si + kStep * kAhead - kStep);
+      buf[w][lane] = m;
       lds_barrier();  // the other buffer's readers are past it too
+      f32x4 acc[KS];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        Parts<3> b;
+      for (int s = 0; s < KS; ++s) acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+      acc[0] = add[i];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) b.p[k] = *(const bf16x8*)(buf[s][k] + lane * 8);
-        mma<2>(acc[s & 1], row[s], b);
-      }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+            acc[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(raw[i][2 * s + e][r], buf[2 * s + e][lane][r],
+                                                          acc[s], 0, 0, 0);
+      if (left > kAhead) load(i, si + kStep * kAhead - kStep);
       m = acc[0] + acc[1];
+#pragma unroll
+      for (int s = 2; s < KS; ++s) m += acc[s];
     }
   }
 }
