@@ -59,6 +59,20 @@ struct Piece<float> {
   }
 };
 
+// E elements of a vector from c on, or `other` without one and past its end.
+template <int E>
+__device__ __forceinline__ void load_or(const float* p, int c, int width, float other, float* v) {
+  f32x4 w[E / 4];
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) w[i] = f32x4{other, other, other, other};
+  if (p && c < width) {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) w[i] = *(const f32x4*)(p + c + 4 * i);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = w[e / 4][e % 4];
+}
+
 // Sum over the WPR waves of a row, the same bits in every lane.  red: one
 // float per wave, of two buffers that alternate from call to call, so that one
 // barrier a call is enough.
@@ -103,11 +117,8 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm(
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int c = E * (lane + 64 * WPR * p);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      gm[p][e] = gamma && c < width ? gamma[c + e] : 1.f;
-      bt[p][e] = beta && c < width ? beta[c + e] : 0.f;
-    }
+    load_or<E>(gamma, c, width, 1.f, gm[p]);
+    load_or<E>(beta, c, width, 0.f, bt[p]);
   }
   int turn = 0;
   for (; t0 < n; t0 += step, turn ^= 2) {
@@ -171,8 +182,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm_backward(
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int c = E * (lane + 64 * WPR * p);
-#pragma unroll
-    for (int e = 0; e < E; ++e) gm[p][e] = gamma && c < width ? gamma[c + e] : 1.f;
+    load_or<E>(gamma, c, width, 1.f, gm[p]);
   }
   const float inv = 1.f / (float)width;
   int turn = 0;

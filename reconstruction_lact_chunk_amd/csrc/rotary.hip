@@ -82,9 +82,8 @@ __device__ __forceinline__ void turn_group(const RotaryArgs& a, const RotaryPlan
   const bool turn = grp < pl.turned;
   const int p0 = grp * V;
   int c0, c1;  // first dims of the two runs of V elements
-  float co[V], si[V];
+  int ax = 0;  // of the first pair; a run of V > 1 pairs has one axis in layout 2 only
   if (turn) {
-    int ax = 0;  // of the first pair; a run of V > 1 pairs has one axis in layout 2 only
     while (ax + 1 < a.axes && p0 >= a.first[ax + 1]) ++ax;
     if (ADJ) {
       c0 = 2 * p0;
@@ -96,6 +95,21 @@ __device__ __forceinline__ void turn_group(const RotaryArgs& a, const RotaryPlan
       c0 = p0 + a.first[ax];
       c1 = p0 + a.first[ax + 1];
     }
+  } else {
+    c0 = 2 * a.pairs + (grp - pl.turned) * 2 * V;
+    c1 = c0 + V;
+  }
+  const int all = a.q.heads + a.k.heads;
+  const int h0 = blockIdx.y * pl.heads_each;
+  const int h1 = h0 + pl.heads_each < all ? h0 + pl.heads_each : all;
+  auto src = [&](int h) {
+    return h < a.q.heads ? (const T*)a.q.x + t * a.q.ldx + (int64_t)h * a.d
+                         : (const T*)a.k.x + t * a.k.ldx + (int64_t)(h - a.q.heads) * a.d;
+  };
+  // the first head's elements are on their way while the angles are formed
+  Vec<T, V> nu = load_v<T, V>(src(h0) + c0), nv = load_v<T, V>(src(h0) + c1);
+  float co[V], si[V];
+  if (turn) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       while (ax + 1 < a.axes && p0 + j >= a.first[ax + 1]) ++ax;
@@ -107,21 +121,17 @@ __device__ __forceinline__ void turn_group(const RotaryArgs& a, const RotaryPlan
       sincospif(2.f * f, &si[j], &co[j]);
       if (a.inverse) si[j] = -si[j];
     }
-  } else {
-    c0 = 2 * a.pairs + (grp - pl.turned) * 2 * V;
-    c1 = c0 + V;
   }
-  const int all = a.q.heads + a.k.heads;
-  const int h0 = blockIdx.y * pl.heads_each;
-  const int h1 = h0 + pl.heads_each < all ? h0 + pl.heads_each : all;
 #pragma unroll 4
   for (int h = h0; h < h1; ++h) {
     const bool isq = h < a.q.heads;
-    const T* x = isq ? (const T*)a.q.x + t * a.q.ldx + (int64_t)h * a.d
-                     : (const T*)a.k.x + t * a.k.ldx + (int64_t)(h - a.q.heads) * a.d;
     T* y = isq ? (T*)a.q.y + t * a.q.ldy + (int64_t)h * a.d
                : (T*)a.k.y + t * a.k.ldy + (int64_t)(h - a.q.heads) * a.d;
-    Vec<T, V> u = load_v<T, V>(x + c0), v = load_v<T, V>(x + c1);
+    Vec<T, V> u = nu, v = nv;
+    if (h + 1 < h1) {
+      nu = load_v<T, V>(src(h + 1) + c0);
+      nv = load_v<T, V>(src(h + 1) + c1);
+    }
     if (turn) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
