@@ -110,13 +110,23 @@ __device__ __forceinline__ void turn_group(const RotaryArgs& a, const RotaryPlan
   Vec<T, V> nu = load_v<T, V>(src(h0) + c0), nv = load_v<T, V>(src(h0) + c1);
   float co[V], si[V];
   if (turn) {
+    // all loads first: an axis picked pair by pair would wait for each on its own
+    int raw[4];
+    float fq[V];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = ((const int*)a.pos)[t * a.axes + (i < a.axes ? i : 0)];
+#pragma unroll
+    for (int j = 0; j < V; ++j) fq[j] = a.freqs[p0 + j];
+    double pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pos[i] = a.pos_f32 ? (double)__int_as_float(raw[i]) : (double)raw[i];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      while (ax + 1 < a.axes && p0 + j >= a.first[ax + 1]) ++ax;
-      const int64_t at = t * a.axes + ax;
-      const double pos = a.pos_f32 ? (double)((const float*)a.pos)[at]
-                                   : (double)((const int*)a.pos)[at];
-      const double rev = pos * (double)a.freqs[p0 + j] * 0.15915494309189533577;  // 1 / (2 pi)
+      double p = pos[0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i)
+        if (i < a.axes && p0 + j >= a.first[i]) p = pos[i];
+      const double rev = p * (double)fq[j] * 0.15915494309189533577;  // 1 / (2 pi)
       const float f = (float)(rev - rint(rev));
       sincospif(2.f * f, &si[j], &co[j]);
       if (a.inverse) si[j] = -si[j];
