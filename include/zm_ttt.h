@@ -353,6 +353,7 @@ ZM_API int zm_rotary(const zm_rotary_desc* desc, int64_t n, const void* pos, con
  * gradients of the 64 tokens that it is taken with (counted from its sequence's
  * first) and of later ones NaN in its heads, but not earlier chunks' outputs
  * and no other sequence's.
+ * Values of tokens and states stay below 2^60 in size (they are scaled by up to that).
  * States: fp32 [n_seq, heads, d_head (rows: v), d_head (k)], 16-byte aligned. */
 typedef struct zm_delta_desc {
   int32_t heads;      /* value heads, 1..64, a multiple of heads_k */

@@ -8,7 +8,11 @@
 //     start the direct loads of K and Q two chunks ahead.
 // Nothing of a chunk but q, k, v, o moves through memory.  The state waves are bound
 // by their own issue (matrix instructions and the splitting of fp32 operands into
-// bf16 parts); the triangle waves run in the gaps.
+// bf16 parts); the triangle waves run in the gaps.  Measured, 137400 tokens, 8 heads of
+// 128 in segments of 68 chunks: outputs 507 us, 7.5 us a chunk; transitions (two runs of
+// a state) 626 us, 9.2 us a chunk.  State waves of 32 columns, or on 32 x 32
+// instructions, came within 5% of it; triangles formed by a kernel of their own and read
+// back took 4 times as long.
 //
 // Decays are taken out where they can be.  With a running exponent s (the state is
 // 2^s M^) and U^ = U / 2^(s + c_i), c in powers of two,

@@ -4,7 +4,9 @@
 // LDS in rows and, for K^T, through the transposing read; T and P, read as
 // operand tiles.  M, R and U stay in registers: each is the result of one product
 // and the right operand of the next.  Columns 2 c and 2 c + 1 of a wave belong to
-// lane c's two column tiles, so tokens go in and out as pairs.
+// lane c's two column tiles, so tokens go in and out as pairs.  Bound by the latency
+// of a chunk's chain of products, one wave on each SIMD: 1374 tokens, 8 heads of 128 in
+// segments of 2 chunks 38 us, 17 more for the triangles' kernel.
 #include "delta_scan.h"
 
 namespace zm {
@@ -247,7 +249,8 @@ __global__ __launch_bounds__(2 * D, 1) void k_delta_scan(DeltaArgs a, DeltaScanA
 // are loaded three steps ahead, M passes between the waves through LDS, and the
 // product takes both in fp32 (v_mfma_f32_16x16x4_f32, row 8 g + e of a 32-row step in
 // slot g of instruction e): twice the time on the matrix cores of bf16 parts, but
-// splitting N's rows, once for every 16 columns, took longer than that.
+// splitting N's rows, once for every 16 columns, took as long.  N lies as it is
+// loaded: by rows each load touched sixteen lines and a step took 2.4 us instead of 1.8.
 template <int D, bool REV>
 __global__ __launch_bounds__(4 * D) void k_delta_join(DeltaArgs a, DeltaJoinArgs ja) {
   constexpr int KS = D / 32, SL = D / 16;
