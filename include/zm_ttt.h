@@ -372,7 +372,7 @@ ZM_API int zm_delta_rule_workspace_size(const zm_delta_desc* desc, int64_t n, si
 /* The rule over whole sequences, 64 tokens at a time (fp32 states, products of
  * 24 bits where they reach a state).  state_in: the states before the first tokens or NULL
  * (zeros); state_out: receives the states after the last ones, or NULL; it may
- * be state_in.  o must not overlap the inputs.  Bitwise reproducible; sequences
+ * be state_in.  o must not overlap the inputs (the same pointer is refused).  Bitwise reproducible; sequences
  * longer than some hundred tokens are cut into segments that run side by side
  * where few (sequence, head) pairs would leave the GPU idle, by a rule on n,
  * n_seq and heads alone. */
@@ -387,8 +387,8 @@ ZM_API int zm_delta_rule_step(const zm_delta_desc* desc, const void* q, const vo
                        const float* g, const float* beta, float* state, void* o, void* stream);
 
 /* Bytes of workspace of zm_delta_rule_backward for n tokens in desc->n_seq sequences
- * (about 2.5 states of a head to each 64 tokens: the states are formed again
- * and kept chunk by chunk). */
+ * (to each 64 tokens of a head about 3.5 states of 128 x 128, or 6 of 64 x 64: the
+ * states are formed again and kept chunk by chunk). */
 ZM_API int zm_delta_rule_backward_workspace_size(const zm_delta_desc* desc, int64_t n, size_t* bytes);
 
 /* The gradient of zm_delta_rule from its inputs alone: d_o [n, heads, d_head]
@@ -397,7 +397,7 @@ ZM_API int zm_delta_rule_backward_workspace_size(const zm_delta_desc* desc, int6
  * dv [n, heads, d_head] in the io type, dg, dbeta fp32 [n, heads] and
  * dstate_in (NULL: not wanted).  Token strides as in the descriptor.  Rows
  * outside every sequence are left as they were.  The outputs must not overlap the inputs
- * (dstate_in may be dstate_out).  Where g is below -128 (a reset) its gradient is
+ * or each other (the same pointer is refused; dstate_in may be dstate_out).  Where g is below -128 (a reset) its gradient is
  * zero up to rounding.  Bitwise reproducible. */
 ZM_API int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* offsets,
                   const void* d_o, const void* q, const void* k, const void* v, const float* g,

@@ -168,7 +168,8 @@ BackwardWs backward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, co
 int check_counts(const zm_delta_desc* d, int64_t n) {
   if (n < 0 || n > kMaxDeltaTokens || (d->n_seq == 0 && n > 0)) return ZM_ERR_INVALID_ARG;
   const int64_t chunks = (n + (int64_t)(kChunk - 1) * d->n_seq) / kChunk;
-  // a block to each (chunk or segment, head), of 512 threads at most and the join's 8 a segment
+  // a block to each (chunk or segment, head), of 768 threads at most (segments: a sequence
+  // has one, and takes part in both terms) or of 512; the join has few
   if ((chunks + d->n_seq) * d->heads * 2 > kMaxDeltaBlocks) return ZM_ERR_UNSUPPORTED;
   return ZM_OK;
 }
@@ -183,6 +184,12 @@ int check_inputs(const zm_delta_desc* d, int64_t n, const int* offsets, const vo
   ZM_TRY(check_ptr(v, 16));
   ZM_TRY(check_ptr(g, 4));
   return check_ptr(beta, 4);
+}
+
+// An output in an input's place would be read after it is written: by other heads'
+// workgroups, or by the second pass over segments.
+int check_apart(int64_t n, const void* out, const void* q, const void* k, const void* v, const void* d_o = nullptr) {
+  return n > 0 && (out == q || out == k || out == v || out == d_o) ? ZM_ERR_INVALID_ARG : ZM_OK;
 }
 
 void set_inputs(DeltaArgs& a, const zm_delta_desc* d, const void* q, const void* k, const void* v,
@@ -221,6 +228,7 @@ int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* offsets, 
   ZM_TRY(check_counts(desc, n));
   ZM_TRY(check_inputs(desc, n, offsets, q, k, v, g, beta));
   if (n > 0) ZM_TRY(check_ptr(o, 16));
+  ZM_TRY(check_apart(n, o, q, k, v));
   if (!aligned(state_in, 16) || !aligned(state_out, 16)) return ZM_ERR_INVALID_ARG;
   const DeltaPlan p = delta_plan(desc, n);
   ForwardWs f = forward_ws(desc, p, n, offsets, workspace);
@@ -255,6 +263,7 @@ int zm_delta_rule_step(const zm_delta_desc* desc, const void* q, const void* k, 
   ZM_TRY(check_inputs(desc, desc->n_seq, (const int*)256, q, k, v, g, beta));
   ZM_TRY(check_ptr(state, 16));
   ZM_TRY(check_ptr(o, 16));
+  ZM_TRY(check_apart(desc->n_seq, o, q, k, v));
   DeltaStepArgs a{};
   a.q = DeltaTokens{q, desc->ld_q};
   a.k = DeltaTokens{k, desc->ld_k};
@@ -300,6 +309,10 @@ int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* 
     ZM_TRY(check_ptr(dv, 16));
     ZM_TRY(check_ptr(dg, 4));
     ZM_TRY(check_ptr(dbeta, 4));
+    ZM_TRY(check_apart(n, dq, q, k, v, d_o));
+    ZM_TRY(check_apart(n, dk, q, k, v, d_o));
+    ZM_TRY(check_apart(n, dv, q, k, v, d_o));
+    if (dq == dk || dq == dv || dk == dv) return ZM_ERR_INVALID_ARG;
   }
   if (!aligned(state_in, 16) || !aligned(dstate_out, 16) || !aligned(dstate_in, 16)) return ZM_ERR_INVALID_ARG;
   const DeltaPlan p = delta_plan(desc, n);

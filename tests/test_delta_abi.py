@@ -13,6 +13,7 @@ pytestmark = pytest.mark.skipif(not os.path.exists(zm.LIB_PATH),
                                 reason="libzmttt.so not built (run the build first)")
 GOOD, OFF = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 8)
 ODD = ctypes.c_void_p((1 << 20) + 2)
+OUT = [ctypes.c_void_p((2 + i) << 20) for i in range(4)]
 INVALID, UNSUPPORTED, WORKSPACE = zm.ERR_INVALID_ARG, zm.ERR_UNSUPPORTED, zm.ERR_WORKSPACE
 
 
@@ -30,18 +31,18 @@ def desc(**kw):
 POINTERS = ("offsets", "q", "k", "v", "g", "beta")
 
 
-def forward(n=4, state=GOOD, state_out=GOOD, o=GOOD, ws=GOOD, size=1 << 40, **kw):
+def forward(n=4, state=GOOD, state_out=GOOD, o=OUT[0], ws=GOOD, size=1 << 40, **kw):
     p = {name: kw.pop(name, GOOD) for name in POINTERS}
     return lib().zm_delta_rule(ctypes.byref(desc(**kw)), n, *(p[x] for x in POINTERS), state, state_out, o, ws, size,
                                None)
 
 
-def step(state=GOOD, o=GOOD, **kw):
+def step(state=GOOD, o=OUT[0], **kw):
     p = {name: kw.pop(name, GOOD) for name in POINTERS[1:]}
     return lib().zm_delta_rule_step(ctypes.byref(desc(**kw)), *(p[x] for x in POINTERS[1:]), state, o, None)
 
 
-def backward(n=4, do=GOOD, state=GOOD, dstate=GOOD, dq=GOOD, ld_dq=128, dk=GOOD, ld_dk=128, dv=GOOD, ld_dv=256,
+def backward(n=4, do=GOOD, state=GOOD, dstate=GOOD, dq=OUT[0], ld_dq=128, dk=OUT[1], ld_dk=128, dv=OUT[2], ld_dv=256,
              dg=GOOD, dbeta=GOOD, dstart=GOOD, ws=GOOD, size=1 << 40, **kw):
     p = {name: kw.pop(name, GOOD) for name in POINTERS}
     return lib().zm_delta_rule_backward(ctypes.byref(desc(**kw)), n, p["offsets"], do,
@@ -74,6 +75,7 @@ MEMORY = [(dict(ws=None, n_seq=2), WORKSPACE), (dict(ws=ODD, n_seq=2), INVALID),
 @pytest.mark.parametrize("bad,want", DESCRIPTOR + INPUTS + COUNTS + MEMORY + [
     (dict(o=None), INVALID), (dict(o=OFF), INVALID), (dict(state=OFF), INVALID), (dict(state_out=OFF), INVALID),
     (dict(ws=None, io_dtype=zm.F32), WORKSPACE), (dict(ws=None, n=2000), WORKSPACE),
+    (dict(o=GOOD), INVALID), (dict(v=OUT[0]), INVALID),   # in place of an input
 ])
 def test_delta_rule_refusals(bad, want):
     assert forward(**bad) == want
@@ -81,7 +83,7 @@ def test_delta_rule_refusals(bad, want):
 
 @pytest.mark.parametrize("bad,want", DESCRIPTOR + INPUTS + [
     (dict(o=None), INVALID), (dict(o=OFF), INVALID), (dict(state=None), INVALID), (dict(state=OFF), INVALID),
-    (dict(n_seq=1 << 23), UNSUPPORTED),
+    (dict(n_seq=1 << 23), UNSUPPORTED), (dict(o=GOOD), INVALID),
 ])
 def test_delta_rule_step_refusals(bad, want):
     assert step(**bad) == want
@@ -92,6 +94,7 @@ def test_delta_rule_step_refusals(bad, want):
     (dict(dv=None), INVALID), (dict(dg=None), INVALID), (dict(dbeta=ODD), INVALID), (dict(state=OFF), INVALID),
     (dict(dstate=OFF), INVALID), (dict(dstart=OFF), INVALID), (dict(ld_dq=120), INVALID), (dict(ld_dk=132), INVALID),
     (dict(ld_dv=248), INVALID), (dict(ld_dv=(1 << 24) + 8), INVALID), (dict(ws=None), WORKSPACE),
+    (dict(dq=GOOD), INVALID), (dict(dv=GOOD), INVALID), (dict(dk=OUT[0]), INVALID), (dict(do=OUT[2]), INVALID),
 ])
 def test_delta_rule_backward_refusals(bad, want):
     assert backward(**bad) == want
