@@ -6,7 +6,6 @@ If the library is missing, every call raises ZmError; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -552,12 +551,17 @@ def _same_gpu(first, *others):
             raise ZmError(f"tensors must all be on {first.device}, got one on {t.device}")
 
 
-_AS_IT_IS = contextlib.nullcontext()
-
-
-def _on_device(device):
-    """Makes a tensor's device the current one for a call, if it is not."""
-    return _AS_IT_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _run(name, device, *args):
+    """Calls an entry point on the device's current stream, with the device made the
+    current one for the call if it is not."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    if st != OK:
+        _check(st, name)
 
 
 def _row_stride(x, width):
@@ -593,7 +597,7 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-6, out=None, stats=None):
     layer_norm_backward.  out=x normalises in place."""
     _norm_rows("x", x)
     n, width = x.shape
-    y = torch.empty((n, width), dtype=x.dtype, device=x.device) if out is None else out
+    y = x.new_empty((n, width)) if out is None else out
     if out is not None:
         _norm_rows("out", out, x)
     _vector(gamma, width, "gamma")
@@ -602,11 +606,8 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-6, out=None, stats=None):
         _norm_stats(stats, n)
     ld_x, ld_y = _row_stride(x, width), _row_stride(y, width)
     _same_gpu(x, gamma, beta, y, stats)
-    with _on_device(x.device):
-        st = load_library().zm_layer_norm(
-            ctypes.byref(NormDesc(width, _IO[x.dtype], float(eps), 0)), n, _ptr(x), ld_x,
-            _ptr(gamma), _ptr(beta), _ptr(y), ld_y, _ptr(stats), _stream(x.device))
-    _check(st, "zm_layer_norm")
+    _run("zm_layer_norm", x.device, ctypes.byref(NormDesc(width, _IO[x.dtype], float(eps), 0)),
+         n, _ptr(x), ld_x, _ptr(gamma), _ptr(beta), _ptr(y), ld_y, _ptr(stats))
     return y
 
 
@@ -625,7 +626,7 @@ def layer_norm_backward(dy, x, stats, gamma=None, out=None, dgamma=None, dbeta=N
     _norm_rows("x", x)
     _norm_rows("dy", dy, x)
     n, width = x.shape
-    dx = torch.empty((n, width), dtype=x.dtype, device=x.device) if out is None else out
+    dx = x.new_empty((n, width)) if out is None else out
     if out is not None:
         _norm_rows("out", out, x)
     _vector(gamma, width, "gamma")
@@ -640,12 +641,10 @@ def layer_norm_backward(dy, x, stats, gamma=None, out=None, dgamma=None, dbeta=N
     need = layer_norm_backward_workspace_size(n, width, x.dtype)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device) if workspace is None \
         else workspace
-    with _on_device(x.device):
-        st = load_library().zm_layer_norm_backward(
-            ctypes.byref(NormDesc(width, _IO[x.dtype], 1e-6, 0)), n, _ptr(dy), lds[0], _ptr(x),
-            lds[1], _ptr(gamma), _ptr(stats), _ptr(dx), lds[2], _ptr(dgamma), _ptr(dbeta),
-            _ptr(ws), _ws_bytes(ws), _stream(x.device))
-    _check(st, "zm_layer_norm_backward")
+    desc = NormDesc(width, _IO[x.dtype], 1e-6, 0)
+    _run("zm_layer_norm_backward", x.device, ctypes.byref(desc), n, _ptr(dy), lds[0], _ptr(x),
+         lds[1], _ptr(gamma), _ptr(stats), _ptr(dx), lds[2], _ptr(dgamma), _ptr(dbeta),
+         _ptr(ws), _ws_bytes(ws))
     return dx, dgamma, dbeta
 
 
@@ -683,10 +682,10 @@ def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_ou
             or not pos.is_contiguous():
         raise ZmError(f"pos must be contiguous int32 or fp32 [{n}, {len(sec)}]")
     _vector(freqs, sum(sec), "freqs")
-    qo = torch.empty((n, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    qo = q.new_empty((n, hq, d)) if q_out is None else q_out
     ko = k_out
     if k is not None and ko is None:
-        ko = torch.empty((n, hk, d), dtype=k.dtype, device=k.device)
+        ko = k.new_empty((n, hk, d))
     ldq, ldqo = _heads_rows("q", q, n, hq, d, q.dtype), _heads_rows("q_out", qo, n, hq, d, q.dtype)
     ldk = ldko = 0
     if k is not None:
@@ -696,10 +695,8 @@ def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_ou
     desc = RotaryDesc(hq, hk, d, _IO[q.dtype], int(layout), 1 if inverse else 0,
                       1 if pos.dtype == torch.float32 else 0, len(sec),
                       (ctypes.c_int32 * 4)(*sec), ldq, ldk, ldqo, ldko)
-    with _on_device(q.device):
-        st = load_library().zm_rotary(ctypes.byref(desc), n, _ptr(pos), _ptr(freqs), _ptr(q),
-                                      _ptr(k), _ptr(qo), _ptr(ko), _stream(q.device))
-    _check(st, "zm_rotary")
+    _run("zm_rotary", q.device, ctypes.byref(desc), n, _ptr(pos), _ptr(freqs), _ptr(q),
+         _ptr(k), _ptr(qo), _ptr(ko))
     return qo, ko
 
 
@@ -760,20 +757,18 @@ def delta_rule(q, k, v, g, beta, state=None, offsets=None, scale=None, out=None,
     _delta_state("state", state, desc)
     _delta_state("state_out", state_out, desc)
     shape = (desc.n_seq, desc.heads, desc.d_head, desc.d_head)
-    o = torch.empty((n, desc.heads, desc.d_head), dtype=q.dtype, device=q.device) if out is None \
-        else out
+    o = q.new_empty((n, desc.heads, desc.d_head)) if out is None else out
     desc.ld_o = _heads_rows("out", o, n, desc.heads, desc.d_head, q.dtype)
     end = torch.empty(shape, dtype=torch.float32, device=q.device) if state_out is None \
         else state_out
     _same_gpu(q, k, v, g, beta, state, offsets, o, end, workspace)
-    need = delta_rule_workspace_size(desc, n)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None \
-        else workspace
-    with _on_device(q.device):
-        st = load_library().zm_delta_rule(
-            ctypes.byref(desc), n, _ptr(offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-            _ptr(state), _ptr(end), _ptr(o), _ptr(ws), _ws_bytes(ws), _stream(q.device))
-    _check(st, "zm_delta_rule")
+    ws = workspace
+    if ws is None:
+        need = delta_rule_workspace_size(desc, n)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _run("zm_delta_rule", q.device, ctypes.byref(desc), n, _ptr(offsets), _ptr(q), _ptr(k),
+         _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(end), _ptr(o), _ptr(ws),
+         0 if ws is None else _ws_bytes(ws))
     return o, end
 
 
@@ -785,15 +780,11 @@ def delta_rule_step(q, k, v, g, beta, state, scale=None, out=None):
     if state is None:
         raise ZmError("delta_rule_step needs a state")
     _delta_state("state", state, desc)
-    o = torch.empty((n, desc.heads, desc.d_head), dtype=q.dtype, device=q.device) if out is None \
-        else out
+    o = q.new_empty((n, desc.heads, desc.d_head)) if out is None else out
     desc.ld_o = _heads_rows("out", o, n, desc.heads, desc.d_head, q.dtype)
     _same_gpu(q, k, v, g, beta, state, o)
-    with _on_device(q.device):
-        st = load_library().zm_delta_rule_step(
-            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
-            _ptr(o), _stream(q.device))
-    _check(st, "zm_delta_rule_step")
+    _run("zm_delta_rule_step", q.device, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v),
+         _ptr(g), _ptr(beta), _ptr(state), _ptr(o))
     return o
 
 
@@ -835,13 +826,10 @@ def delta_rule_backward(do, q, k, v, g, beta, state=None, dstate=None, offsets=N
     need = delta_rule_backward_workspace_size(desc, n)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None \
         else workspace
-    with _on_device(q.device):
-        st = load_library().zm_delta_rule_backward(
-            ctypes.byref(desc), n, _ptr(offsets), _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-            _ptr(beta), _ptr(state), _ptr(dstate), _ptr(dq), lds[0], _ptr(dk), lds[1], _ptr(dv),
-            lds[2], _ptr(dg), _ptr(dbeta), _ptr(dstart), _ptr(ws), _ws_bytes(ws),
-            _stream(q.device))
-    _check(st, "zm_delta_rule_backward")
+    _run("zm_delta_rule_backward", q.device, ctypes.byref(desc), n, _ptr(offsets), _ptr(do),
+         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(dstate), _ptr(dq),
+         lds[0], _ptr(dk), lds[1], _ptr(dv), lds[2], _ptr(dg), _ptr(dbeta), _ptr(dstart),
+         _ptr(ws), _ws_bytes(ws))
     return out
 
 
