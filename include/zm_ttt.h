@@ -275,7 +275,7 @@ typedef struct zm_norm_desc {
 } zm_norm_desc;
 
 /* x, y: [n][width] rows of strides ld_x, ld_y (>= width, multiples of 8), bases
- * 16-byte aligned.  gamma, beta: fp32 [width], either may be NULL (1, 0).
+ * 16-byte aligned.  gamma, beta: fp32 [width], 16-byte aligned, either may be NULL (1, 0).
  * stats: NULL, or fp32 [2][n] that receives mu, then r, for the backward.  y
  * may be x (same stride); otherwise they must not overlap.  n = 0 is valid. */
 ZM_API int zm_layer_norm(const zm_norm_desc* desc, int64_t n, const void* x, int64_t ld_x,
@@ -330,7 +330,8 @@ typedef struct zm_rotary_desc {
 
 /* pos: [n][axes] contiguous; freqs: fp32 [P] (radians per unit of position).
  * q_out may be q and k_out may be k (same stride: in place, what is unrotated
- * is then not touched); otherwise no two of the arrays may overlap.  q and k
+ * is then not touched); otherwise an output must not overlap another array (k's
+ * pointer for q_out, q's for k_out or one for both is refused).  q and k
  * may be slices of one projection's rows.  n = 0 is valid. */
 ZM_API int zm_rotary(const zm_rotary_desc* desc, int64_t n, const void* pos, const float* freqs,
               const void* q, const void* k, void* q_out, void* k_out, void* stream);

@@ -114,6 +114,7 @@ int zm_rotary(const zm_rotary_desc* desc, int64_t n, const void* pos, const floa
     ZM_TRY(check_rows(k, d->ld_k, (int64_t)d->heads_k * d->d_head));
     ZM_TRY(check_rows(k_out, d->ld_k_out, (int64_t)d->heads_k * d->d_head));
     if (k == k_out && d->ld_k != d->ld_k_out) return ZM_ERR_INVALID_ARG;
+    if (q_out == k_out || q_out == k || k_out == q) return ZM_ERR_INVALID_ARG;
   }
   a.q = RotaryTensor{q, q_out, d->ld_q, d->ld_q_out, d->heads_q};
   a.k = RotaryTensor{k, k_out, d->ld_k, d->ld_k_out, d->heads_k};

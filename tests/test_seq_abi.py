@@ -86,6 +86,12 @@ def test_rotary_refusals(bad, want):
     assert rot(**bad) == want
 
 
+@pytest.mark.parametrize("q,k,qo,ko", [(1, 2, 2, 3), (1, 2, 3, 1), (1, 2, 3, 3)])
+def test_rotary_outputs_in_place_of_the_other_input_or_of_each_other(q, k, qo, ko):
+    p = [ctypes.c_void_p(i << 20) for i in (q, k, qo, ko)]
+    assert rot(q=p[0], k=p[1], qo=p[2], ko=p[3]) == INVALID
+
+
 def test_rotary_without_tokens_is_fine():
     assert rot(n=0, pos=None, freqs=None, q=None, k=None, qo=None, ko=None) == zm.OK
 
