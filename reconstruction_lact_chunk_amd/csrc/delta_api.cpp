@@ -43,13 +43,14 @@ DeltaPlan delta_plan(const zm_delta_desc* d, int64_t n) {
   // One workgroup goes through a whole sequence of one head while these are enough
   // for half the compute units, or while the sequences are short; else a workgroup to
   // each segment of at least kMinSegChunks chunks, about kTargetWgs of them.
-  // Measured with 8 heads of 128, us whole / in segments: bf16 512 tokens 54 / 62,
-  // 640 65 / 65, 1560 151 / 83 (segments of 8 chunks: 138); fp32 384 tokens 96 / 88,
-  // 512 121 / 92; backward bf16 512 tokens 139 / 145, 1560 347 / 194.
-  constexpr int kMinSegChunks = 2, kSplitChunks = 8;
+  // Measured with 8 heads of 128, us whole / in segments: bf16 384 tokens 43 / 50, 512
+  // 54 / 52, 1560 150 / 71 (1374 in segments of 8 chunks 128, of 2 72); fp32 256 tokens
+  // 70 / 71, 384 96 / 74; backward bf16 384 tokens 113 / 120, 1560 346 / 169.
+  constexpr int kMinSegChunks = 2;
+  const int64_t split_chunks = d->io_dtype == ZM_F32 ? 5 : 8;
   const int64_t units = (int64_t)d->n_seq * d->heads;
   int64_t seg = p.n_chunks > 0 ? p.n_chunks : 1;
-  if (units < kTargetWgs / 2 && p.n_chunks >= (int64_t)kSplitChunks * d->n_seq) {
+  if (units < kTargetWgs / 2 && p.n_chunks >= split_chunks * d->n_seq) {
     seg = ceil_div((int64_t)p.n_chunks * d->heads, kTargetWgs);
     if (seg < kMinSegChunks) seg = kMinSegChunks;
   }
