@@ -126,8 +126,8 @@ __global__ __launch_bounds__(1024) void k_delta_table(DeltaSeqs s) {
 template <bool F32>
 __device__ __forceinline__ Parts<Tok<F32>::NT> row_parts(const typename Tok<F32>::T* base, int64_t ld,
                                                          int tok, int count, int col) {
-  if (tok < count) return load8(base + (int64_t)tok * ld + col);
-  return zero_parts<Tok<F32>::NT>();
+  const auto p = load8(base + (tok < count ? tok : count - 1) * ld + col);
+  return tok < count ? p : zero_parts<Tok<F32>::NT>();
 }
 
 // Operand tiles of a 64 x 64 matrix in LDS: item i of 6 x 64 is tile i / 64, lane
@@ -177,33 +177,16 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
   const int4 ch = delta_chunk(a.sq, ci);
   const int count = ch.y;
   if (count == 0) return;
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int hk = h / (a.heads / a.heads_k);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, hk = h / (a.heads / a.heads_k);
   const T* const kp = (const T*)a.k.p + (int64_t)ch.x * a.k.ld + hk * D;
   const T* const qp = (const T*)a.q.p + (int64_t)ch.x * a.q.ld + hk * D;
   const int64_t slot = (int64_t)ci * a.heads + h;
 
-  if (w == 0) {
-    float gl = 0.f, b = 0.f;
-    if (lane < count) {
-      gl = a.g[((int64_t)ch.x + lane) * a.heads + h];
-      b = a.beta[((int64_t)ch.x + lane) * a.heads + h];
-      if (gl < kMinLogDecay) gl = kMinLogDecay;
-    }
-    // sums in 64 bits: a strong decay among weak ones must not blur their differences
-    double s = gl;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-      const double o = __shfl_up(s, m, 64);
-      if (lane >= m) s += o;
-    }
-    cs[lane] = s;
-    be[lane] = b;
-    const double last = __shfl(s, 63, 64);
-    float* const r = a.rows + slot * 3 * kChunk;
-    r[lane] = expf((float)s);
-    r[kChunk + lane] = expf((float)(last - s));
-    r[2 * kChunk + lane] = b;
+  float gl = 0.f, b = 0.f;
+  if (w == 0 && lane < count) {
+    gl = a.g[((int64_t)ch.x + lane) * a.heads + h];
+    b = a.beta[((int64_t)ch.x + lane) * a.heads + h];
   }
   f32x4 kk[4], qk[4];
 #pragma unroll
@@ -220,6 +203,23 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
       mma<LIM>(kk[j], ka, kb);
       mma<LIM>(qk[j], qa, kb);
     }
+  }
+  if (w == 0) {  // the wave with fewest products
+    if (gl < kMinLogDecay) gl = kMinLogDecay;
+    // sums in 64 bits: a strong decay among weak ones must not blur their differences
+    double s = gl;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+      const double o = __shfl_up(s, m, 64);
+      if (lane >= m) s += o;
+    }
+    cs[lane] = s;
+    be[lane] = b;
+    const double last = __shfl(s, 63, 64);
+    float* const r = a.rows + slot * 3 * kChunk;
+    r[lane] = expf((float)s);
+    r[kChunk + lane] = expf((float)(last - s));
+    r[2 * kChunk + lane] = b;
   }
   __syncthreads();
 #pragma unroll
