@@ -350,10 +350,10 @@ ZM_API int zm_rotary(const zm_rotary_desc* desc, int64_t n, const void* pos, con
  * offsets[b + 1] - 1 (device int32 [n_seq + 1], nondecreasing in 0..n; values
  * outside are clamped to that), which may be none.  offsets may be NULL for a
  * single sequence of all n tokens.  Rows of the outputs outside every sequence
- * are left as they were.  A token that is not finite can make the outputs and
- * gradients of the 64 tokens that it is taken with (counted from its sequence's
- * first) and of later ones NaN in its heads, but not earlier chunks' outputs
- * and no other sequence's.
+ * are left as they were.  A token that is not finite can make NaN, in its heads, of
+ * the outputs of the 64 tokens that it is taken with (counted from its sequence's
+ * first) and of later ones and of its sequence's gradients; earlier chunks'
+ * outputs and other sequences stay as they are.
  * Values of tokens and states stay below 2^60 in size (they are scaled by up to that).
  * States: fp32 [n_seq, heads, d_head (rows: v), d_head (k)], 16-byte aligned. */
 typedef struct zm_delta_desc {

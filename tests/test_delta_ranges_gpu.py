@@ -118,3 +118,55 @@ def test_one_tensor_for_several_arguments():
     out = [torch.empty_like(y) for y in g1[:5]] + [d]
     zm.delta_rule_backward(t, t, t, t, x["g"], x["beta"], state=x["state"], dstate=d, out=out)
     assert all(torch.equal(a, b) for a, b in zip(out, g1))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,offsets,heads,heads_k", [(1000, None, 2, 1), (700, [3, 3, 90, 650, 650], 4, 4),
+                                                     (1500, [0, 1100, 1110, 1490], 3, 1)])
+def test_workspaces_hold_anything(n, offsets, heads, heads_k, dtype):
+    # every byte 255 is NaN as fp32 and bf16: nothing is read that the call has not written
+    n_seq = len(offsets) - 1 if offsets else 1
+    print(f"case delta workspace n={n} {dtype}", flush=True)
+    x = inputs(n, heads, heads_k, 64, dtype, n, n_seq=n_seq)
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    args, kw = [x[k] for k in NAMES], dict(state=x["state"], offsets=off)
+    do = torch.randn_like(x["v"], dtype=torch.float32).to(dtype)
+    dstate = torch.randn_like(x["state"])
+    desc = zm.DeltaDesc(heads, heads_k, 64, zm.BF16 if dtype == torch.bfloat16 else zm.F32, n_seq, 1.0, 64 * heads_k,
+                        64 * heads_k, 64 * heads, 64 * heads)
+
+    def full(size):
+        return torch.full((max(size, 256),), 255, dtype=torch.uint8, device="cuda")
+
+    live = slice(offsets[0], offsets[-1]) if offsets else slice(0, n)
+    o, end = zm.delta_rule(*args, **kw, workspace=full(zm.delta_rule_workspace_size(desc, n)))
+    o2, end2 = zm.delta_rule(*args, **kw)
+    assert torch.equal(o[live], o2[live]) and torch.equal(end, end2) and not end.isnan().any()
+    a = zm.delta_rule_backward(do, *args, **kw, dstate=dstate,
+                               workspace=full(zm.delta_rule_backward_workspace_size(desc, n)))
+    b = zm.delta_rule_backward(do, *args, **kw, dstate=dstate)
+    assert all(torch.equal(s[live], t[live]) and not s[live].isnan().any() for s, t in zip(a[:5], b[:5]))
+    assert torch.equal(a[5], b[5]) and not a[5].isnan().any()
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_token_that_is_not_finite(name, dtype):
+    # token 200 of the first sequence (its chunk begins at 192), long enough for segments
+    offsets = [0, 700, 800]
+    x = inputs(800, 4, 2, 64, dtype, 95, n_seq=2)
+    good = run(x, offsets)
+    do = torch.randn_like(x["v"], dtype=torch.float32).to(dtype)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    good_g = zm.delta_rule_backward(do, *(x[k] for k in NAMES), state=x["state"], offsets=off)
+    x[name][200, 0] = float("nan") if name != "q" else float("inf")
+    heads = slice(0, 2) if name in ("q", "k") else slice(0, 1)   # value heads that read it
+    rest = slice(heads.stop, 4)
+    o, end = run(x, offsets)
+    assert not o[200, heads].isfinite().any()
+    assert torch.equal(o[:192], good[0][:192]) and torch.equal(o[700:], good[0][700:])
+    assert torch.equal(o[:, rest], good[0][:, rest])
+    assert torch.equal(end[1], good[1][1]) and torch.equal(end[:, rest], good[1][:, rest])
+    g = zm.delta_rule_backward(do, *(x[k] for k in NAMES), state=x["state"], offsets=off)
+    assert all(torch.equal(a[700:], b[700:]) for a, b in zip(g[:5], good_g[:5])) and torch.equal(g[5][1], good_g[5][1])
+    assert all(torch.equal(a[:, rest], b[:, rest]) for a, b in zip(g[2:5], good_g[2:5]))
