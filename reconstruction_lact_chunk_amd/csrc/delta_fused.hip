@@ -18,8 +18,8 @@
 // 2^s M^) and U^ = U / 2^(s + c_i), c in powers of two,
 //   U^ = T^ (V / 2^(s + c_i) - K M^),  T^ = (I + strictly_lower(b_i k_i.k_j))^-1 diag(b),
 //   O = scale 2^(s + c_i) (Q M^ + lower(Q K^T) U^),  M^ <- M^ + K^T U^,  s <- s + c_C:
-// the same numbers up to powers of two, so nothing is lost while |s + c_i| stays
-// under kMaxShift.  A chunk that would leave that range takes 2^s into M^ first; one
+// the same numbers up to powers of two, whose factors come from 64-bit exponents
+// (exp2_wide), so nothing is lost while |s + c_i| stays under kMaxShift.  A chunk that would leave that range takes 2^s into M^ first; one
 // whose own decay is over it (a reset) is formed with the decays in place.
 #include "delta_rule.h"
 
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
         const uint16_t* const kt = k_tile(j);
         const float be = bn;
         double s = gn < kMinLogDecay ? kMinLogDecay : gn;
-        s *= 1.4426950408889634;  // exponents of two from here
+        s *= kLog2E;  // exponents of two from here
         if (j + 1 < n) load_gates(j + 1);
         Parts<1> ki[KS];
         tile(kt, PW, ki);
@@ -237,20 +237,20 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
         if (move) shift = 0.0;
         if (PW == 0) {
           float* const r = row_factors(j);
-          const float at = (float)(shift + s);
-          const float up = __builtin_amdgcn_exp2f(at);
-          r[kRowV + lane] = gated ? 1.f : __builtin_amdgcn_exp2f(-at);
+          const double at = shift + s;
+          const float up = exp2_wide(at);
+          r[kRowV + lane] = gated ? 1.f : exp2_wide(-at);
           r[kRowO + lane] = gated ? 1.f : C::Q ? a.scale * up : up;
           if (gated) {
             r[kRowGam + lane] = up;
-            r[kRowDec + lane] = __builtin_amdgcn_exp2f((float)(end - s));
+            r[kRowDec + lane] = exp2_wide(end - s);
           }
           if (lane == 0) {
             ((unsigned*)r)[kFlags] = (gated ? kGated : 0) | (move ? kShift : 0);
-            r[kPre] = __builtin_amdgcn_exp2f((float)from);
-            r[kLast] = __builtin_amdgcn_exp2f((float)end);
-            r[kScale0] = __builtin_amdgcn_exp2f((float)shift);
-            r[kScale1] = gated ? 1.f : __builtin_amdgcn_exp2f((float)(shift + end));
+            r[kPre] = exp2_wide(from);
+            r[kLast] = exp2_wide(end);
+            r[kScale0] = exp2_wide(shift);
+            r[kScale1] = gated ? 1.f : exp2_wide(shift + end);
           }
         }
         if (gated) cs[lane] = s;
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               // above the diagonal the exponent may be positive: not taken
-              const float e = __builtin_amdgcn_exp2f((float)(cs[16 * PW + 4 * g + r] - cj));
+              const float e = exp2_wide(cs[16 * PW + 4 * g + r] - cj);
               if (J < PW || 4 * g + r > c) av[r] *= e;
             }
           }
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
             const double cp = cs[16 * PI + c];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float e = __builtin_amdgcn_exp2f((float)(cp - cs[16 * J + 4 * g + r]));
+              const float e = exp2_wide(cp - cs[16 * J + 4 * g + r]);
               if (J < PI || 4 * g + r <= c) pt[J][r] *= a.scale * e;
             }
           }

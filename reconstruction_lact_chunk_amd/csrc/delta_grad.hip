@@ -399,7 +399,7 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
     if (sl == 0) {  // out of the way of the first slice
       if (threadIdx.x < 3 * kChunk) rows[threadIdx.x] = rv;
       if (w == SUMS) {
-        double sum = gl < kMinLogDecay ? kMinLogDecay : gl;
+        double sum = (gl < kMinLogDecay ? kMinLogDecay : gl) * kLog2E;  // exponents of two
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
           const double o = __shfl_up(sum, m, 64);
@@ -482,7 +482,7 @@ __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGrad
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int j = 16 * jt + 4 * g + r;
-      const float gd = expf(j <= i ? (float)(sum_i - cs[j]) : 0.f), x = j < i ? gd * xt[n][r] : 0.f;
+      const float gd = exp2_wide(j <= i ? sum_i - cs[j] : 0.0), x = j < i ? gd * xt[n][r] : 0.f;
       wv[r] = j <= i ? a.scale * gd * pt[n][r] : 0.f;
       ev[r] = -beta * x;
       sx += j < i ? x * kk[n][r] : 0.f;

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
   if (w == 0) {  // the wave with fewest products
     if (gl < kMinLogDecay) gl = kMinLogDecay;
     // sums in 64 bits: a strong decay among weak ones must not blur their differences
-    double s = gl;
+    double s = gl * kLog2E;  // exponents of two
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
       const double o = __shfl_up(s, m, 64);
@@ -217,8 +217,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
     be[lane] = b;
     const double last = __shfl(s, 63, 64);
     float* const r = a.rows + slot * 3 * kChunk;
-    r[lane] = expf((float)s);
-    r[kChunk + lane] = expf((float)(last - s));
+    r[lane] = exp2_wide(s);
+    r[kChunk + lane] = exp2_wide(last - s);
     r[2 * kChunk + lane] = b;
   }
   __syncthreads();
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * w + 4 * g + r;
-      const float gd = row >= col ? expf((float)(cs[row] - cs[col])) : 0.f;
+      const float gd = row >= col ? exp2_wide(cs[row] - cs[col]) : 0.f;
       const float av = row > col ? be[row] * gd * kk[j][r] : 0.f;
       ma[row * kPitch + col] = av;
       mp[row * kPitch + col] = row >= col ? a.scale * gd * qk[j][r] : 0.f;

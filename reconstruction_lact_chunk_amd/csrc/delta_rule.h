@@ -35,6 +35,7 @@ constexpr int kTriFrags = 6;           // 16 x 32 operand tiles of a 64 x 64 tri
 constexpr int kFragElems = 64 * 8;     // bf16 elements of one such tile
 constexpr int kTableLds = 1024;        // sequences that the table's kernel keeps in LDS
 constexpr float kMinLogDecay = -128.f; // exp of less is 0 in fp32
+constexpr double kLog2E = 1.4426950408889634;
 
 // Where the sequences lie.  Without a table (one sequence) a chunk follows from
 // its index; offsets are clamped to 0 <= ... <= n and made nondecreasing, so that
@@ -85,6 +86,15 @@ struct DeltaScanArgs {
   float* m_out;             // [n_chunks][heads][d][d]: M at each chunk's start (backward), as below
   float* u_out;             // U (backward), as below
 };
+
+// 2^x to 32 bits for an x of any size.  Of a sum of decays near 60 rounded to 32 bits as a
+// whole up to 2^-19 is lost, 1.3e-6 of the factor, and between two tokens that does not
+// cancel: so the whole part goes into the exponent and only the rest is rounded.
+__device__ __forceinline__ float exp2_wide(double x) {
+  const double whole = rint(x);
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(x - whole)),
+                                 (int)fmin(fmax(whole, -4096.0), 4096.0));
+}
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
