@@ -29,8 +29,8 @@ namespace {
 
 enum { kOutputs = 0, kKeep = 1, kTransition = 2 };
 
-constexpr int kAtPitch = 68;   // floats of a row of A^T in LDS
-constexpr int kDPitch = 20;    // floats of a row of a diagonal block's inverse
+constexpr int kDPitch = 20;         // floats of a row of a 16 x 16 block in LDS
+constexpr int kBlock = 16 * kDPitch;  // A^T's blocks (J, i), J <= i, and the diagonal ones' inverses
 // K tiles in LDS: this chunk's, the next one's, the one in flight; Q's third takes the
 // place of the first, whose last reader is done before its load starts.
 constexpr int kRingK = 3, kRingQ = 2;
@@ -60,18 +60,23 @@ struct FusedCfg {
   static constexpr int kOffQ = kRingK * TILE * 2;
   static constexpr int kOffT = kOffQ + (Q ? kRingQ * TILE * 2 : 0);
   static constexpr int kOffP = kOffT + 3 * TRI * 2;
-  static constexpr int kOffV = kOffP + (Q ? 2 * TRI * 2 : 0);
+  static constexpr int kOffV = kOffP + (Q ? 3 * TRI * 2 : 0);
   static constexpr int kOffRows = kOffV + TILE * 2;                    // two chunks' factors
   static constexpr int kOffAt = kOffRows + 2 * kRowFloats * 4;
-  static constexpr int kOffD = kOffAt + kChunk * kAtPitch * 4;
-  static constexpr int kOffDt = kOffD + 4 * 16 * kDPitch * 4;
-  static constexpr int kOffCs = kOffDt + 4 * 16 * kDPitch * 4;
+  static constexpr int kOffD = kOffAt + 10 * kBlock * 4;
+  static constexpr int kOffDt = kOffD + 4 * kBlock * 4;
+  static constexpr int kOffCs = kOffDt + 4 * kBlock * 4;
   static constexpr int kOffBe = kOffCs + TW * kChunk * 8;
   static constexpr int BYTES = kOffBe + TW * kChunk * 4;
   static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
+
+// Row `row` of block (J, i) of A^T: columns J of A, rows i.
+__device__ __forceinline__ constexpr int at_row(int J, int i, int row) {
+  return (i * (i + 1) / 2 + J) * kBlock + row * kDPitch;
+}
 
 // Tiles hold row r's granule p at place p ^ swizzle(r): row reads (16 rows of tile
 // order, two granules) and transposing reads spread over the banks.
@@ -270,18 +275,18 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
               if (J < PW || 4 * g + r > c) av[r] *= e;
             }
           }
-          *(f32x4*)(at + (16 * J + c) * kAtPitch + 16 * PW + 4 * g) = av;
+          *(f32x4*)(at + at_row(J, PW, c) + 4 * g) = av;
         }
         // row c of the inverse, from its end: a forward substitution, which (unlike a
         // product of powers of A) stays exact where keys repeat
         float x[16];
-        const float* const blk = at + 16 * PW * kAtPitch + 16 * PW;
+        const float* const blk = at + at_row(PW, PW, 0);
 #pragma unroll
         for (int i = 15; i >= 0; --i) {
           f32x4 row[4];
 #pragma unroll
           for (int q = 3; q >= 0; --q)
-            if (4 * q + 3 > i) row[q] = *(const f32x4*)(blk + i * kAtPitch + 4 * q);
+            if (4 * q + 3 > i) row[q] = *(const f32x4*)(blk + i * kDPitch + 4 * q);
           // two chains: the newest entry last
           float v = i == c ? 1.f : 0.f, y = 0.f;
 #pragma unroll
@@ -309,7 +314,7 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
           y[w] = tt[w] = f32x4{0.f, 0.f, 0.f, 0.f};
           dv[w] = *(const f32x4*)(dt + (16 * w + c) * kDPitch + 4 * g);
 #pragma unroll
-          for (int j = w + 1; j <= PW; ++j) av[w][j] = *(const f32x4*)(at + (16 * w + c) * kAtPitch + 16 * j + 4 * g);
+          for (int j = w + 1; j <= PW; ++j) av[w][j] = *(const f32x4*)(at + at_row(w, j, c) + 4 * g);
         }
         tt[PW] = *(const f32x4*)(dm + (16 * PW + c) * kDPitch + 4 * g);
 #pragma unroll
@@ -351,7 +356,7 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
       auto store_p = [&]() {
         if (!C::Q) return;
 #pragma unroll
-        for (int J = 0; J <= PI; ++J) store_tile(pf, PI, J, pt[J], 2);
+        for (int J = 0; J <= PI; ++J) store_tile(pf, PI, J, pt[J], 3);
       };
       // lower(Q K^T), or P with its decays
       auto scores = [&](int j) {
@@ -509,14 +514,14 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
         }
         if (with_q) {
 #pragma unroll
-          for (int p = 1; p >= 0; --p)
+          for (int p = 2; p >= 0; --p)
 #pragma unroll
             for (int it = 0; it < 4; ++it) qm[it] = mfma_bf16(qf[it], b.p[p], qm[it]);
         }
         if (with_q) weave_reads<4>();
         weave<12, 2>();
         if (more) weave_reads<4>();
-        if (with_q) weave<8, 3>();
+        if (with_q) weave<12, 2>();
         __builtin_amdgcn_sched_barrier(0);
         b = next;
       }
@@ -597,31 +602,33 @@ __global__ __launch_bounds__(64 * (D / 16 + 4)) void k_delta_fused(DeltaArgs a, 
       }
     };
     // the parts of half ts of U that go into M, and those for O
-    Parts<3> ub;
-    Parts<2> ob;
+    Parts<3> ub, ob;
     auto split_u = [&](int ts) {
       if (flags & kGated) {
-        if (C::Q) ob = split_tiles<2>(u[2 * ts], u[2 * ts + 1]);
+        if (C::Q) ob = split_tiles<3>(u[2 * ts], u[2 * ts + 1]);
 #pragma unroll
         for (int it = 2 * ts; it < 2 * ts + 2; ++it) u[it] *= *(const f32x4*)(rows + kRowDec + token_row(it, 4 * g));
       }
       ub = split_tiles<3>(u[2 * ts], u[2 * ts + 1]);
-      if (C::Q && !(flags & kGated)) ob = Parts<2>{{ub.p[0], ub.p[1]}};
+      if (C::Q && !(flags & kGated)) ob = ub;
     };
     // Q M + P U
     auto outputs = [&](int ts) {
       bf16x8 f[2][4];
-#pragma unroll
-      for (int k = 1; k >= 0; --k)
+      auto part = [&](int k) {
 #pragma unroll
         for (int it = 2 * ts; it < 4; ++it)
-          f[k][it] = *(const bf16x8*)(smem + C::kOffP + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
+          f[k & 1][it] = *(const bf16x8*)(smem + C::kOffP + lo + (k * C::TRI + low_frag(it, ts) * kFragElems) * 2);
+      };
+      part(2);
 #pragma unroll
-      for (int o = 1; o >= 0; --o)
+      for (int k = 2; k >= 0; --k) {
+        if (k > 0) part(k - 1);
 #pragma unroll
-        for (int p = o; p >= 0; --p)
+        for (int p = 2 - k; p >= 0; --p)
 #pragma unroll
-          for (int it = 2 * ts; it < 4; ++it) qm[it] = mfma_bf16(f[p][it], ob.p[o - p], qm[it]);
+          for (int it = 2 * ts; it < 4; ++it) qm[it] = mfma_bf16(f[k & 1][it], ob.p[p], qm[it]);
+      }
     };
     // M += K^T U, a half of the chunk's tokens at a time
     auto advance = [&](f32x4* mm, int ts) {

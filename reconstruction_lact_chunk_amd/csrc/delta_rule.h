@@ -17,8 +17,8 @@
 // (M, U, T, P, fp32 tokens) enters as a sum of bf16 parts: three parts carry 24
 // bits, and of the products of parts those below 2^-24 are left out, so the
 // state is as exact as fp32 products would leave it at 3 (bf16 tokens) or 6
-// matrix instructions instead of the 16 that fp32 ones cost.  What is rounded to
-// bf16 in the end (O with bf16 io) takes two parts, 2^-17 each.
+// matrix instructions instead of the 16 that fp32 ones cost.  O takes as many parts
+// where it ends as bf16: it can be what is left of terms much larger than itself.
 //
 // The matrix cores return rows 4 g + r (r < 4) of column c in lane 16 g + c, and
 // take rows in slots 8 g + e (e < 8) of a 32-row step in the same lane.  With
