@@ -300,7 +300,7 @@ __device__ __forceinline__ bf16x8 read_tr8(const uint16_t* at) {
 template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGradArgs s) {
   using T = typename Tok<F32>::T;
-  constexpr int NT = Tok<F32>::NT, KS = D / 32, MT = D / 16, NW = NT == 1 ? 2 : 3, THR = 4 * D;
+  constexpr int NT = Tok<F32>::NT, KS = D / 32, MT = D / 16, NW = 3, THR = 4 * D;
   constexpr int SETS = 512 / THR, TPW = (12 + MT - 1) / MT;
   // a buffer: dX and U of 3 parts, dO, and for fp32 K and Q; bf16 K and Q stay whole
   constexpr int BUF = (6 + NT + (F32 ? 2 * NT : 0)) * kSlice;
