@@ -367,7 +367,8 @@ typedef struct zm_delta_desc {
                                       d_head), multiples of 8, at most 2^24 */
 } zm_delta_desc;
 
-/* Bytes of workspace of zm_delta_rule for n tokens in desc->n_seq sequences. */
+/* Bytes of workspace of zm_delta_rule for n tokens in desc->n_seq sequences (never less for
+ * more tokens). */
 ZM_API int zm_delta_rule_workspace_size(const zm_delta_desc* desc, int64_t n, size_t* bytes);
 
 /* The rule over whole sequences, 64 tokens at a time (fp32 states, products of

@@ -33,7 +33,8 @@ int check_ptr(const void* p, size_t align) { return p && aligned(p, align) ? ZM_
 
 struct DeltaPlan {
   int n_chunks, n_segs, seg_chunks;
-  bool split;  // sequences in several segments
+  int seg_room;  // segments the workspace has place for: at least n_segs, never fewer for more tokens
+  bool split;    // sequences in several segments
 };
 
 // Upper bounds over every way n tokens can fall into n_seq sequences.
@@ -58,6 +59,10 @@ DeltaPlan delta_plan(const zm_delta_desc* d, int64_t n) {
   p.n_segs = (int)(p.n_chunks / seg) + d->n_seq;
   p.split = p.n_chunks > seg;
   if (!p.split) p.n_segs = d->n_seq;
+  // n_segs falls where seg steps up; of chunks / seg neither chunks / kMinSegChunks nor
+  // kTargetWgs / heads is ever passed
+  const int64_t most = kTargetWgs / d->heads, room = p.n_chunks / kMinSegChunks;
+  p.seg_room = p.split ? (int)(room < most ? room : most) + d->n_seq : d->n_seq;
   return p;
 }
 
@@ -87,7 +92,7 @@ DeltaSeqs seqs(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, const int*
                     (int64_t)d->n_seq * d->heads > kTargetWgs;
   if (d->n_seq > 1) {
     s.chunks = c.take<int4>(p.n_chunks);
-    s.segs = c.take<int4>(p.n_segs);
+    s.segs = c.take<int4>(p.seg_room);
     s.first_chunk = c.take<int>(d->n_seq + 1);
     s.begin = c.take<int>(d->n_seq + 1);
   }
@@ -112,7 +117,7 @@ ForwardWs forward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, cons
     f.a.rows = c.take<float>(slots * 3 * kChunk);
   }
   if (p.split) {
-    const size_t states = (size_t)p.n_segs * d->heads * d->d_head * d->d_head;
+    const size_t states = (size_t)p.seg_room * d->heads * d->d_head * d->d_head;
     f.trans = c.take<float>(2 * states);
     f.starts = c.take<float>(states);
   }
@@ -143,7 +148,7 @@ BackwardWs backward_ws(const zm_delta_desc* d, const DeltaPlan& p, int64_t n, co
   f.a.pt_frags = c.take<uint16_t>(slots * 3 * tile);
   f.a.rows = c.take<float>(slots * 3 * kChunk);
   if (p.split) {
-    const size_t states = (size_t)p.n_segs * d->heads * dd;
+    const size_t states = (size_t)p.seg_room * d->heads * dd;
     f.trans = c.take<float>(3 * states);
     f.starts = c.take<float>(states);
     f.ends = c.take<float>(states);
