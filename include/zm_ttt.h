@@ -374,8 +374,8 @@ ZM_API int zm_delta_rule_workspace_size(const zm_delta_desc* desc, int64_t n, si
 /* The rule over whole sequences, 64 tokens at a time (fp32 states, products of
  * 24 bits where they reach a state).  state_in: the states before the first tokens or NULL
  * (zeros); state_out: receives the states after the last ones, or NULL; it may
- * be state_in.  o must not overlap the inputs (the same pointer is refused).  Bitwise reproducible; sequences
- * longer than some hundred tokens are cut into segments that run side by side
+ * be state_in.  o and state_out must not overlap other arrays (the same pointer is refused).  Bitwise
+ * reproducible; sequences longer than some hundred tokens are cut into segments that run side by side
  * where few (sequence, head) pairs would leave the GPU idle, by a rule on n,
  * n_seq and heads alone. */
 ZM_API int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* offsets,
@@ -384,7 +384,7 @@ ZM_API int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* of
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* One token of each of n_seq sequences (row b: sequence b), states updated in
- * place.  No workspace. */
+ * place.  o must not overlap another array (the same pointer is refused).  No workspace. */
 ZM_API int zm_delta_rule_step(const zm_delta_desc* desc, const void* q, const void* k, const void* v,
                        const float* g, const float* beta, float* state, void* o, void* stream);
 

@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <initializer_list>
+
 #include "api_util.h"
 #include "delta_rule.h"
 
@@ -192,10 +194,14 @@ int check_inputs(const zm_delta_desc* d, int64_t n, const int* offsets, const vo
   return check_ptr(beta, 4);
 }
 
-// An output in an input's place would be read after it is written: by other heads'
-// workgroups, or by the second pass over segments.
-int check_apart(int64_t n, const void* out, const void* q, const void* k, const void* v, const void* d_o = nullptr) {
-  return n > 0 && (out == q || out == k || out == v || out == d_o) ? ZM_ERR_INVALID_ARG : ZM_OK;
+// An output in an input's place would be read after it is written (by other heads'
+// workgroups, or by the second pass over segments), and of two outputs in one place one
+// would be lost.  Null pointers are not arrays.
+int check_apart(const void* out, std::initializer_list<const void*> others) {
+  if (out)
+    for (const void* p : others)
+      if (p == out) return ZM_ERR_INVALID_ARG;
+  return ZM_OK;
 }
 
 void set_inputs(DeltaArgs& a, const zm_delta_desc* d, const void* q, const void* k, const void* v,
@@ -234,11 +240,12 @@ int zm_delta_rule(const zm_delta_desc* desc, int64_t n, const int32_t* offsets, 
   ZM_TRY(check_counts(desc, n));
   ZM_TRY(check_inputs(desc, n, offsets, q, k, v, g, beta));
   if (n > 0) ZM_TRY(check_ptr(o, 16));
-  ZM_TRY(check_apart(n, o, q, k, v));
+  if (n > 0) ZM_TRY(check_apart(o, {q, k, v, g, beta, offsets, state_in, state_out}));
   if (!aligned(state_in, 16) || !aligned(state_out, 16)) return ZM_ERR_INVALID_ARG;
   const DeltaPlan p = delta_plan(desc, n);
   ForwardWs f = forward_ws(desc, p, n, offsets, workspace);
   ZM_TRY(check_workspace(workspace, workspace_bytes, f.bytes));
+  if (n > 0) ZM_TRY(check_apart(state_out, {q, k, v, g, beta, offsets}));  // it may be state_in
   if (desc->n_seq == 0) return ZM_OK;
   set_inputs(f.a, desc, q, k, v, g, beta);
   const hipStream_t st = (hipStream_t)stream;
@@ -269,7 +276,7 @@ int zm_delta_rule_step(const zm_delta_desc* desc, const void* q, const void* k, 
   ZM_TRY(check_inputs(desc, desc->n_seq, (const int*)256, q, k, v, g, beta));
   ZM_TRY(check_ptr(state, 16));
   ZM_TRY(check_ptr(o, 16));
-  ZM_TRY(check_apart(desc->n_seq, o, q, k, v));
+  ZM_TRY(check_apart(o, {q, k, v, g, beta, state}));
   DeltaStepArgs a{};
   a.q = DeltaTokens{q, desc->ld_q};
   a.k = DeltaTokens{k, desc->ld_k};
@@ -315,15 +322,26 @@ int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* 
     ZM_TRY(check_ptr(dv, 16));
     ZM_TRY(check_ptr(dg, 4));
     ZM_TRY(check_ptr(dbeta, 4));
-    ZM_TRY(check_apart(n, dq, q, k, v, d_o));
-    ZM_TRY(check_apart(n, dk, q, k, v, d_o));
-    ZM_TRY(check_apart(n, dv, q, k, v, d_o));
-    if (dq == dk || dq == dv || dk == dv) return ZM_ERR_INVALID_ARG;
+    ZM_TRY(check_apart(dq, {q, k, v, d_o, dk, dv}));
+    ZM_TRY(check_apart(dk, {q, k, v, d_o, dv}));
+    ZM_TRY(check_apart(dv, {q, k, v, d_o}));
   }
   if (!aligned(state_in, 16) || !aligned(dstate_out, 16) || !aligned(dstate_in, 16)) return ZM_ERR_INVALID_ARG;
   const DeltaPlan p = delta_plan(desc, n);
   BackwardWs f = backward_ws(desc, p, n, offsets, workspace);
   ZM_TRY(check_workspace(workspace, workspace_bytes, f.bytes));
+  ZM_TRY(check_apart(dstate_in, {state_in}));  // dstate_in may be dstate_out
+  if (n > 0) {
+    const auto apart = [&](const void* out, std::initializer_list<const void*> others) {
+      ZM_TRY(check_apart(out, {q, k, v, d_o, g, beta, offsets}));
+      return check_apart(out, others);
+    };
+    for (const void* out : {(const void*)dq, (const void*)dk, (const void*)dv})
+      ZM_TRY(apart(out, {dg, dbeta, dstate_in, dstate_out, state_in}));
+    ZM_TRY(apart(dg, {dbeta, dstate_in, dstate_out, state_in}));
+    ZM_TRY(apart(dbeta, {dstate_in, dstate_out, state_in}));
+    ZM_TRY(apart(dstate_in, {}));
+  }
   if (desc->n_seq == 0) return ZM_OK;
   set_inputs(f.a, desc, q, k, v, g, beta);
   const hipStream_t st = (hipStream_t)stream;
