@@ -287,7 +287,8 @@ ZM_API int zm_layer_norm_backward_workspace_size(const zm_norm_desc* desc, int64
 
 /* The gradient: with xh = (x - mu) r from stats and a = dy gamma,
  *   dx = r (a - mean(a) - xh mean(a xh)), dgamma = sum_rows dy xh, dbeta = sum_rows dy.
- * dgamma, dbeta: fp32 [width], overwritten (n = 0: zeros); either may be NULL.
+ * dgamma, dbeta: fp32 [width], overwritten (n = 0: zeros); either may be NULL, and they
+ * must not be one array (refused).
  * dx may be dy or x (same stride).  Sums in fixed order: bitwise reproducible.
  * The workspace is 256-byte aligned; with both dgamma and dbeta NULL it is not
  * read and may be NULL. */

@@ -67,6 +67,7 @@ int zm_layer_norm_backward(const zm_norm_desc* desc, int64_t n, const void* dy, 
                            size_t workspace_bytes, void* stream) {
   ZM_TRY(check_norm(desc, n));
   if (!aligned(gamma, 16) || !aligned(dgamma, 4) || !aligned(dbeta, 4)) return ZM_ERR_INVALID_ARG;
+  if (dgamma && dgamma == dbeta) return ZM_ERR_INVALID_ARG;  // one would be lost
   if (n > 0) {
     ZM_TRY(check_rows(dy, ld_dy, desc->width));
     ZM_TRY(check_rows(x, ld_x, desc->width));

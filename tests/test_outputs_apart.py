@@ -68,3 +68,12 @@ def test_the_state_s_gradient_may_be_replaced_and_apart_is_fine():
     assert backward(("dstart", "dstate"), size=0) == zm.ERR_WORKSPACE
     assert backward(None, size=0) == zm.ERR_WORKSPACE
     assert delta(("state_out", "state"), size=0) == zm.ERR_WORKSPACE
+
+
+def test_layer_norm_backward():
+    p = pointers(("dy", "x", "gamma", "stats", "dx", "params", "ws"), None)
+    d = zm.NormDesc(64, zm.BF16, 1e-6, 0)
+    for n in (0, 4):
+        assert zm.load_library().zm_layer_norm_backward(
+            ctypes.byref(d), n, p["dy"], 64, p["x"], 64, p["gamma"], p["stats"], p["dx"], 64, p["params"], p["params"],
+            p["ws"], 1 << 20, None) == zm.ERR_INVALID_ARG
