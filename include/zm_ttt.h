@@ -306,8 +306,8 @@ ZM_API int zm_layer_norm_backward(const zm_norm_desc* desc, int64_t n, const voi
  *   ZM_ROTARY_PAIRS        2 p and 2 p + 1
  *   ZM_ROTARY_AXIS_HALVES  the halves of the axis's own block: with f the pairs
  *                          of earlier axes and s its own, p + f and p + f + s
- * Dims from 2 P on pass unrotated.  The angle is formed in 64 bits and reduced
- * before it is rounded, so far positions lose no precision; position 0 (as of
+ * Dims from 2 P on pass unrotated.  Cosine and sine are those of the angle in 64
+ * bits, so far positions lose no precision; position 0 (as of
  * a frame's special tokens) leaves finite values unchanged.  A position that is
  * infinite or NaN gives NaN in the pairs of its axis. */
 typedef enum zm_rotary_layout {
