@@ -202,9 +202,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
-    """Handle of the device's current stream, without a torch.cuda.Stream around it (2 us)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """Handle of the device's current stream, where torch gives it as a number without a
+    torch.cuda.Stream around it (2 us less)."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _check_weights(w1, w2, w3, device=True):
