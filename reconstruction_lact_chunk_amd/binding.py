@@ -618,6 +618,8 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-6, out=None, stats=None):
 
 
 def layer_norm_backward_workspace_size(n: int, width: int, dtype=torch.bfloat16) -> int:
+    if dtype not in _IO:
+        raise ZmError(f"dtype {dtype}: rows are bf16 or fp32")
     out = ctypes.c_size_t(0)
     _check(load_library().zm_layer_norm_backward_workspace_size(
         ctypes.byref(NormDesc(int(width), _IO[dtype], 1e-6, 0)), int(n), ctypes.byref(out)),
@@ -713,6 +715,8 @@ def _delta_inputs(q, k, v, g, beta, scale):
         raise ZmError("q, k must be [n, heads_k, d] and v [n, heads, d]")
     n, hk, d = q.shape
     h = v.shape[1]
+    if d < 1:
+        raise ZmError("q has heads of no elements")
     if hk < 1 or h < 1 or h % hk:
         raise ZmError(f"{h} value heads are no multiple of {hk} key heads")
     lds = [_heads_rows("q", q, n, hk, d, q.dtype), _heads_rows("k", k, n, hk, d, q.dtype),
