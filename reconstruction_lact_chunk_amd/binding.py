@@ -3,6 +3,8 @@
 Argument marshalling only: every step of the TTT layer runs in the HIP
 library.  torch is used for device memory and for the current HIP stream.
 If the library is missing, every call raises ZmError; there is no fallback.
+Calls are not recorded by autograd: results do not require a gradient whatever the
+inputs do, and a training step calls the *_backward functions itself.
 """
 from __future__ import annotations
 

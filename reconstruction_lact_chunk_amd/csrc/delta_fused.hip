@@ -9,8 +9,10 @@
 // Nothing of a chunk but q, k, v, o moves through memory.  The state waves are bound
 // by their own issue (matrix instructions and the splitting of fp32 operands into
 // bf16 parts); the triangle waves run in the gaps.  Measured, 137400 tokens, 8 heads of
-// 128 in segments of 68 chunks: outputs 507 us, 7.5 us a chunk; transitions (two runs of
-// a state) 626 us, 9.2 us a chunk.  State waves of 32 columns, or on 32 x 32
+// 128 in segments of 68 chunks: outputs 551 us, 8.1 us a chunk; transitions (two runs of
+// a state) 623 us, 9.2 us a chunk.  A sixth of the outputs' matrix instructions are the
+// third parts of M, P and U in O (507 us without them): O is a difference of large terms
+// where a token replaces a large value.  State waves of 32 columns, or on 32 x 32
 // instructions, came within 5% of it; triangles formed by a kernel of their own and read
 // back took 4 times as long.
 //
@@ -19,8 +21,9 @@
 //   U^ = T^ (V / 2^(s + c_i) - K M^),  T^ = (I + strictly_lower(b_i k_i.k_j))^-1 diag(b),
 //   O = scale 2^(s + c_i) (Q M^ + lower(Q K^T) U^),  M^ <- M^ + K^T U^,  s <- s + c_C:
 // the same numbers up to powers of two, whose factors come from 64-bit exponents
-// (exp2_wide), so nothing is lost while |s + c_i| stays under kMaxShift.  A chunk that would leave that range takes 2^s into M^ first; one
-// whose own decay is over it (a reset) is formed with the decays in place.
+// (exp2_wide), so nothing is lost while |s + c_i| stays under kMaxShift.  A chunk that
+// would leave that range takes 2^s into M^ first; one whose own decay is over it (a
+// reset) is formed with the decays in place.
 #include "delta_rule.h"
 
 namespace zm {

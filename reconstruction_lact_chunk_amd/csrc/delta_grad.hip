@@ -291,12 +291,13 @@ __device__ __forceinline__ bf16x8 read_tr8(const uint16_t* at) {
 // One workgroup per (chunk, head), a wave to 16 dims: M and dM' rows, loaded and
 // taken apart by the one wave that needs them, times the chunk's dO, dX and U,
 // which all waves share through LDS, 32 dims at a time and read ahead by one such
-// slice.  The 16 x 16 tiles of the triangles go round the waves on the way; W and E
+// slice.  W and E take three parts as all else: where a token replaced a large value W K takes
+// it off M^T dO again.  The 16 x 16 tiles of the triangles go round the waves on the way; W and E
 // are then shared through LDS for the products with K and Q.  8 sequences of 1374 bf16
-// tokens, 8 heads of 128: 146 us, 3.2 TB/s; half of a workgroup's 25 us are the slices
+// tokens, 8 heads of 128: 148 us, 3.1 TB/s; half of a workgroup's 25 us are the slices
 // (M, dM', U and dX of fp32), half the start, the triangles and the sums, and its 99 KB
 // of LDS let one run on a compute unit.  With every wave splitting all of M and dM' it
-// took 505 us; workgroups that go on to the next chunk, or two slices read ahead, 152.
+// took 505 us; workgroups that go on to the next chunk, or two slices read ahead, 152 of 146.
 template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, 2) void k_delta_grads(DeltaArgs a, DeltaGradArgs s) {
   using T = typename Tok<F32>::T;

@@ -3,7 +3,8 @@
 // Bound by the states' traffic: a row is read once and written once, both dots
 // with k and q are taken on the way in.  16 lanes hold a row (D / 16 columns a
 // lane), so a wave covers 4 rows at a time and the dots end in 4 exchanges.  256
-// sequences, 8 heads of 128 (272 MB): 41 us, 6.6 TB/s; one sequence 4.5 us, a launch.
+// sequences, 8 heads of 128 (272 MB): 54 us a call over changing states, 5 TB/s, and 41 us where
+// the same ones come again, part of them from cache; one sequence 4.5 us, a launch.
 #include "delta_rule.h"
 
 namespace zm {

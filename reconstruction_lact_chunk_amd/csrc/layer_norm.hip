@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kNormWaves = 4;  // waves of a workgroup
 // Workgroups of the forward pass: 4 to a compute unit go over the rows, gamma and beta
-// in registers and the next row read ahead.  40001 fp32 rows of 2048 (655 MB): 122 us,
+// in registers and the next row read ahead.  40001 fp32 rows of 2048 (655 MB): 121 us,
 // 5.4 TB/s; 127 with gamma and beta by single loads, and so 128 with 8 workgroups, 133
 // with 6, 192 with one to every two rows, 220 with that and both read for every row.
 // 1374 bf16 rows of 1024: 4.3 us, about what an empty launch takes.
@@ -170,7 +170,9 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm(
 // its lanes' columns of dgamma and dbeta in registers over all of them; at the
 // end its waves add theirs in order through LDS and the sums go to the
 // workgroup's slot, which k_norm_param_sum adds in order (no atomics).  137400 bf16 rows
-// of 1024 (844 MB): 153 us, 5.5 TB/s, and 5 us for the sum of the slots.
+// of 1024 (844 MB): 153 us, 5.5 TB/s, and 5 us for the sum of the slots; 40001 fp32 rows of 2048
+// (983 MB) 209 us, 4.7 TB/s.  A row has a wave at least, so narrow ones are far from the memory's
+// rate: 1200000 bf16 rows of 64 take 408 us (forward 330), 1.1 TB/s, 300000 of 256 132 us (89).
 template <typename T, int WPR, int NP>
 __global__ __launch_bounds__(64 * kNormWaves) void k_layer_norm_backward(
     const T* dy, int64_t lddy, const T* x, int64_t ldx, const float* __restrict__ gamma,
