@@ -407,8 +407,9 @@ ZM_API int zm_delta_rule_backward_workspace_size(const zm_delta_desc* desc, int6
  * dv [n, heads, d_head] in the io type, dg, dbeta fp32 [n, heads] and
  * dstate_in (NULL: not wanted).  Token strides as in the descriptor.  Rows
  * outside every sequence are left as they were.  The outputs must not overlap the inputs
- * or each other (the same pointer is refused; dstate_in may be dstate_out).  Where g is below -128 (a reset) its gradient is
- * zero up to rounding.  Bitwise reproducible. */
+ * or each other (the same pointer is refused; dstate_in may be dstate_out).  dg is a difference of
+ * sums, good to some 2^-24 of the state times its gradient: where a strong decay makes it far
+ * smaller than those, and below g = -128 (a reset), it is zero up to that rounding.  Bitwise reproducible. */
 ZM_API int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const int32_t* offsets,
                   const void* d_o, const void* q, const void* k, const void* v, const float* g,
                   const float* beta, const float* state_in, const float* dstate_out,
