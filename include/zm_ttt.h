@@ -417,6 +417,70 @@ ZM_API int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const in
                   float* dg, float* dbeta, float* dstate_in,
                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* Linear attention with decays: the linear fast weight f_S(x) = S x written by adding
+ * v_t k_t^T (the delta rule above without taking S k_t off), with a decay to each head:
+ *   S_t = a_t S_{t-1} + v_t k_t^T,  a_t = exp(g_t),  o_t = scale S_t q_t.
+ * Tokens, heads, offsets and states as for zm_delta_rule.  g (log decay, any value below 60;
+ * -inf resets the state) is fp32, token t's of value head h at g[t ld_g + h]: ld_g >= heads, or
+ * ld_g = 0 for one decay to each head, the same for every token; NULL: no decay, a = 1.
+ * A token that is not finite can make NaN, in its heads, of the outputs of the 64 tokens
+ * (fp32: 32) that it is taken with (counted from its sequence's first) and of later ones and of its
+ * sequence's gradients; earlier chunks' outputs and other sequences stay as they are.
+ * Values of tokens and states stay below 2^60 in size. */
+typedef struct zm_linear_desc {
+  int32_t heads;      /* value heads, 1..64, a multiple of heads_k */
+  int32_t heads_k;    /* query/key heads */
+  int32_t d_head;     /* 64 or 128 */
+  int32_t io_dtype;   /* zm_dtype of q, k, v, o and their gradients */
+  int32_t n_seq;      /* sequences, >= 0 */
+  float scale;        /* of the outputs */
+  int64_t ld_q, ld_k, ld_v, ld_o;  /* token strides: >= heads * d_head (q, k: heads_k *
+                                      d_head), multiples of 8, at most 2^24 */
+  int64_t ld_g;       /* 0, or heads .. 2^24 */
+} zm_linear_desc;
+
+/* Bytes of workspace of zm_linear_attention for n tokens in desc->n_seq sequences (never less
+ * for more tokens): at most 1024 / heads + 1 states to a head. */
+ZM_API int zm_linear_attention_workspace_size(const zm_linear_desc* desc, int64_t n, size_t* bytes);
+
+/* Whole sequences, a chunk of tokens at a time (fp32 states, products of 24 bits up to a
+ * state and up to an output's own rounding).  state_in: the states before the first tokens or
+ * NULL (zeros); state_out: receives the states after the last ones, or NULL; it may be state_in.
+ * o and state_out must not overlap other arrays (the same pointer is refused).  Rows of o
+ * outside every sequence are left as they were.  Bitwise reproducible.  A sequence is cut into
+ * segments of a length that follows from n, n_seq, heads and io_dtype alone, which run side by
+ * side. */
+ZM_API int zm_linear_attention(const zm_linear_desc* desc, int64_t n, const int32_t* offsets,
+                  const void* q, const void* k, const void* v, const float* g,
+                  const float* state_in, float* state_out, void* o,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of each of n_seq sequences (row b: sequence b), states updated in place.
+ * o must not overlap another array (the same pointer is refused).  No workspace. */
+ZM_API int zm_linear_attention_step(const zm_linear_desc* desc, const void* q, const void* k, const void* v,
+                       const float* g, float* state, void* o, void* stream);
+
+/* Bytes of workspace of zm_linear_attention_backward (never less for more tokens): to each 64
+ * tokens (fp32: 32; or begun ones of a sequence) of a value head a state, the forward's twice, and
+ * with shared key heads two fp32 copies of the value heads' tokens. */
+ZM_API int zm_linear_attention_backward_workspace_size(const zm_linear_desc* desc, int64_t n, size_t* bytes);
+
+/* The gradient of zm_linear_attention from its inputs alone: d_o [n, heads, d_head] (stride
+ * desc->ld_o) and dstate_out (gradient of the last states, NULL: zeros) give dq, dk [n, heads_k,
+ * d_head] (summed over the value heads of a key head), dv [n, heads, d_head] in the io type, dg
+ * (NULL: not wanted, as it has to be without g) and dstate_in (NULL: not wanted).  dg is fp32
+ * [n, heads] contiguous, or, with ld_g = 0, [heads]: summed over all tokens.  Rows outside every
+ * sequence are left as they were.  The outputs must not overlap the inputs or each other (the
+ * same pointer is refused; dstate_in may be dstate_out).  dg_t is formed of terms that each hold
+ * the factor a_t, so it is as good as fp32 products where decays are strong too; below
+ * g = -128 it is zero.  Bitwise reproducible. */
+ZM_API int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const int32_t* offsets,
+                  const void* d_o, const void* q, const void* k, const void* v, const float* g,
+                  const float* state_in, const float* dstate_out,
+                  void* dq, int64_t ld_dq, void* dk, int64_t ld_dk, void* dv, int64_t ld_dv,
+                  float* dg, float* dstate_in,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 ZM_API const char* zm_status_string(int status);
 

@@ -33,6 +33,8 @@ EXPORTED = (
     "zm_layer_norm", "zm_layer_norm_backward_workspace_size", "zm_layer_norm_backward",
     "zm_rotary", "zm_delta_rule_workspace_size", "zm_delta_rule", "zm_delta_rule_step",
     "zm_delta_rule_backward_workspace_size", "zm_delta_rule_backward",
+    "zm_linear_attention_workspace_size", "zm_linear_attention", "zm_linear_attention_step",
+    "zm_linear_attention_backward_workspace_size", "zm_linear_attention_backward",
 )
 
 
@@ -108,6 +110,22 @@ class DeltaDesc(ctypes.Structure):
     ]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [
+        ("heads", ctypes.c_int32),
+        ("heads_k", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("n_seq", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("ld_q", ctypes.c_int64),
+        ("ld_k", ctypes.c_int64),
+        ("ld_v", ctypes.c_int64),
+        ("ld_o", ctypes.c_int64),
+        ("ld_g", ctypes.c_int64),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -161,10 +179,19 @@ def load_library(path: str | None = None):
     lib.zm_delta_rule_backward.argtypes = [_DD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
                                            _P, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]
     lib.zm_delta_rule_step.argtypes = [_DD, _P, _P, _P, _P, _P, _P, _P, _P]
+    _AD = ctypes.POINTER(LinearDesc)
+    lib.zm_linear_attention_workspace_size.argtypes = [_AD, _I64, ctypes.POINTER(_SZ)]
+    lib.zm_linear_attention.argtypes = [_AD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+    lib.zm_linear_attention_step.argtypes = [_AD, _P, _P, _P, _P, _P, _P, _P]
+    lib.zm_linear_attention_backward_workspace_size.argtypes = [_AD, _I64, ctypes.POINTER(_SZ)]
+    lib.zm_linear_attention_backward.argtypes = [_AD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                 _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]
     for name in ("zm_layer_norm", "zm_layer_norm_backward_workspace_size",
                  "zm_layer_norm_backward", "zm_rotary", "zm_delta_rule_workspace_size",
                  "zm_delta_rule", "zm_delta_rule_step", "zm_delta_rule_backward_workspace_size",
-                 "zm_delta_rule_backward"):
+                 "zm_delta_rule_backward", "zm_linear_attention_workspace_size",
+                 "zm_linear_attention", "zm_linear_attention_step",
+                 "zm_linear_attention_backward_workspace_size", "zm_linear_attention_backward"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("zm_ttt_workspace_size", "zm_ttt_update", "zm_ttt_update_loss", "zm_ttt_apply",
                  "zm_ttt_update_apply", "zm_ttt_update_apply_scratch",
@@ -842,6 +869,134 @@ def delta_rule_backward(do, q, k, v, g, beta, state=None, dstate=None, offsets=N
          _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(dstate), _ptr(dq),
          lds[0], _ptr(dk), lds[1], _ptr(dv), lds[2], _ptr(dg), _ptr(dbeta), _ptr(dstart),
          _ptr(ws), _ws_bytes(ws))
+    return out
+
+
+def _linear_inputs(q, k, v, g, scale):
+    """Shape and type checks of a linear-attention call; returns its descriptor (one
+    sequence, ld_o of a contiguous output) and n."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ZmError("q, k must be [n, heads_k, d] and v [n, heads, d]")
+    n, hk, d = q.shape
+    h = v.shape[1]
+    if d < 1:
+        raise ZmError("q has heads of no elements")
+    if hk < 1 or h < 1 or h % hk:
+        raise ZmError(f"{h} value heads are no multiple of {hk} key heads")
+    lds = [_heads_rows("q", q, n, hk, d, q.dtype), _heads_rows("k", k, n, hk, d, q.dtype),
+           _heads_rows("v", v, n, h, d, q.dtype)]
+    ld_g = 0
+    if g is not None:
+        if g.dtype != torch.float32 or (g.shape != (n, h) and g.shape != (h,)) \
+                or (g.numel() > 0 and g.stride(-1) != 1 and h > 1):
+            raise ZmError(f"g must be fp32 [{n}, {h}] or [{h}] with unit stride on the heads")
+        if g.dim() == 2:
+            ld_g = g.stride(0) if n > 1 else h
+            if ld_g < h:
+                raise ZmError("g's rows overlap: pass [heads] for one decay to each head")
+    return LinearDesc(h, hk, d, _IO[q.dtype], 1, float(d ** -0.5 if scale is None else scale), *lds,
+                      h * d, ld_g), n
+
+
+def linear_attention_workspace_size(desc: LinearDesc, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().zm_linear_attention_workspace_size(ctypes.byref(desc), int(n),
+                                                             ctypes.byref(out)),
+           "zm_linear_attention_workspace_size")
+    return int(out.value)
+
+
+def linear_attention(q, k, v, g=None, state=None, offsets=None, scale=None, out=None,
+                     state_out=None, workspace=None):
+    """Linear attention with decays over packed sequences: S <- exp(g) S + v k^T token by
+    token, o = scale S q.  q, k [n, Hk, d], v [n, H, d] (bf16 or fp32, d 64 or 128); g
+    fp32 [n, H], or [H] for one log decay to each head, or None for no decay; offsets
+    int32 [n_seq + 1] on the GPU (None: one sequence); state fp32 [n_seq, H, d, d] or
+    None (zeros); scale None: d ** -0.5.  Returns (o, the states after the last tokens);
+    pass state_out=state to carry the state in place, as from frame to frame.  Rows of
+    o outside every sequence are not written."""
+    desc, n = _linear_inputs(q, k, v, g, scale)
+    desc.n_seq = _delta_offsets(offsets)
+    _delta_state("state", state, desc)
+    _delta_state("state_out", state_out, desc)
+    shape = (desc.n_seq, desc.heads, desc.d_head, desc.d_head)
+    o = q.new_empty((n, desc.heads, desc.d_head)) if out is None else out
+    desc.ld_o = _heads_rows("out", o, n, desc.heads, desc.d_head, q.dtype)
+    end = torch.empty(shape, dtype=torch.float32, device=q.device) if state_out is None \
+        else state_out
+    _same_gpu(q, k, v, g, state, offsets, o, end, workspace)
+    ws = workspace
+    if ws is None:
+        need = linear_attention_workspace_size(desc, n)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _run("zm_linear_attention", q.device, ctypes.byref(desc), n, _ptr(offsets), _ptr(q), _ptr(k),
+         _ptr(v), _ptr(g), _ptr(state), _ptr(end), _ptr(o), _ptr(ws),
+         0 if ws is None else _ws_bytes(ws))
+    return o, end
+
+
+def linear_attention_step(q, k, v, g, state, scale=None, out=None):
+    """One token of each of n sequences (row b: sequence b) through linear attention;
+    g fp32 [n, H], [H] or None; state fp32 [n, H, d, d] is updated in place.  Returns o."""
+    desc, n = _linear_inputs(q, k, v, g, scale)
+    desc.n_seq = n
+    if state is None:
+        raise ZmError("linear_attention_step needs a state")
+    _delta_state("state", state, desc)
+    o = q.new_empty((n, desc.heads, desc.d_head)) if out is None else out
+    desc.ld_o = _heads_rows("out", o, n, desc.heads, desc.d_head, q.dtype)
+    _same_gpu(q, k, v, g, state, o)
+    _run("zm_linear_attention_step", q.device, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v),
+         _ptr(g), _ptr(state), _ptr(o))
+    return o
+
+
+def linear_attention_backward_workspace_size(desc: LinearDesc, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().zm_linear_attention_backward_workspace_size(
+        ctypes.byref(desc), int(n), ctypes.byref(out)),
+        "zm_linear_attention_backward_workspace_size")
+    return int(out.value)
+
+
+def linear_attention_backward(do, q, k, v, g=None, state=None, dstate=None, offsets=None,
+                              scale=None, out=None, workspace=None):
+    """Gradients of linear_attention from its inputs, do (the gradient of o) and dstate
+    (the gradient of the last states, None: zeros): (dq, dk, dv, dg, the gradient of the
+    first states), dg contiguous of g's shape or None without g.  out: those five tensors
+    to write to (dg's place None without g)."""
+    desc, n = _linear_inputs(q, k, v, g, scale)
+    desc.n_seq = _delta_offsets(offsets)
+    h, hk, d = desc.heads, desc.heads_k, desc.d_head
+    _delta_state("state", state, desc)
+    _delta_state("dstate", dstate, desc)
+    if out is None:
+        like = dict(dtype=q.dtype, device=q.device)
+        f32 = dict(dtype=torch.float32, device=q.device)
+        out = (torch.empty((n, hk, d), **like), torch.empty((n, hk, d), **like),
+               torch.empty((n, h, d), **like),
+               None if g is None else torch.empty(g.shape, **f32),
+               torch.empty((desc.n_seq, h, d, d), **f32))
+    if len(out) != 5:
+        raise ZmError("out: the five tensors dq, dk, dv, dg, dstate")
+    dq, dk, dv, dg, dstart = out
+    desc.ld_o = _heads_rows("do", do, n, h, d, q.dtype)
+    lds = [_heads_rows("dq", dq, n, hk, d, q.dtype), _heads_rows("dk", dk, n, hk, d, q.dtype),
+           _heads_rows("dv", dv, n, h, d, q.dtype)]
+    if g is None and dg is not None:
+        raise ZmError("there is no dg without g")
+    if dg is not None and (dg.dtype != torch.float32 or dg.shape != g.shape
+                           or not dg.is_contiguous()):
+        raise ZmError(f"dg must be contiguous fp32 {list(g.shape)}")
+    _delta_state("the first states' gradient", dstart, desc)
+    _same_gpu(q, do, k, v, g, state, dstate, offsets, *out, workspace)
+    need = linear_attention_backward_workspace_size(desc, n)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None \
+        else workspace
+    _run("zm_linear_attention_backward", q.device, ctypes.byref(desc), n, _ptr(offsets),
+         _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(dstate), _ptr(dq),
+         lds[0], _ptr(dk), lds[1], _ptr(dv), lds[2], _ptr(dg), _ptr(dstart), _ptr(ws),
+         _ws_bytes(ws))
     return out
 
 

@@ -1,0 +1,307 @@
+// Linear attention with decays (linear_attn.h): the table of segments, what segments add
+// to the state, their join, and the outputs.
+#include "linear_attn.h"
+
+namespace zm {
+
+namespace {
+
+// ---- table --------------------------------------------------------------------
+// One workgroup: the clamped, nondecreasing offsets, the prefix sums of chunks, segments
+// and slots, and every segment's entry.
+__global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
+  __shared__ int part[4][16], total;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, per = (s.n_seq + 1023) / 1024;
+  const int b0 = t * per < s.n_seq ? t * per : s.n_seq, b1 = b0 + per < s.n_seq ? b0 + per : s.n_seq;
+  // running maximum of the clamped ends
+  const int start = clampi(s.offsets[0], 0, s.n);
+  int top = start;
+  for (int b = b0; b < b1; ++b) {
+    const int e = clampi(s.offsets[b + 1], 0, s.n);
+    if (e > top) top = e;
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const int o = __shfl_up(top, m, 64);
+    if (lane >= m && o > top) top = o;
+  }
+  if (lane == 63) part[0][w] = top;
+  int run = __shfl_up(top, 1, 64);
+  if (lane == 0) run = start;
+  __syncthreads();
+  for (int i = 0; i < w; ++i)
+    if (part[0][i] > run) run = part[0][i];
+  const int run0 = run;
+  // chunks, segments and slots before this thread's sequences
+  int v[3] = {0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    int e = clampi(s.offsets[b + 1], 0, s.n);
+    if (e < run) e = run;
+    const int k = lin_segs(s, e - run);
+    v[0] += lin_chunks(s, e - run);
+    v[1] += k;
+    v[2] += k > 1 ? k : 0;
+    run = e;
+  }
+  int at[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    int x = v[j];
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+      const int o = __shfl_up(x, m, 64);
+      if (lane >= m) x += o;
+    }
+    if (lane == 63) part[1 + j][w] = x;
+    at[j] = x - v[j];
+  }
+  __syncthreads();
+  for (int i = 0; i < w; ++i)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) at[j] += part[1 + j][i];
+  run = run0;
+  for (int b = b0; b < b1; ++b) {
+    int e = clampi(s.offsets[b + 1], 0, s.n);
+    if (e < run) e = run;
+    const int len = e - run;
+    const int k = lin_segs(s, len);
+    s.of_seq[b] = int2{at[2], k};
+    for (int i = 0; i < k; ++i) {
+      const int64_t from = (int64_t)i * s.seg_tokens;
+      LinSeg g;
+      g.tok = run + (int)from;
+      g.count = len - from < s.seg_tokens ? (int)(len - from) : s.seg_tokens;
+      g.seq = b;
+      g.flags = (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0);
+      g.chunk0 = at[0] + (int)(from / s.chunk);
+      g.slot = at[2] + i;
+      g.pad[0] = g.pad[1] = 0;
+      s.segs[at[1] + i] = g;
+    }
+    at[0] += lin_chunks(s, len);
+    at[1] += k;
+    at[2] += k > 1 ? k : 0;
+    run = e;
+  }
+  if (t == 1023) {  // behind the last sequence, whosever that is
+    total = at[1];
+    s.of_seq[s.n_seq] = int2{start, run};
+    s.of_seq[s.n_seq + 1] = int2{at[0], 0};
+  }
+  __syncthreads();
+  for (int i = total + t; i < s.n_segs; i += 1024) s.segs[i].count = -1;
+}
+
+// ---- what a segment adds ----------------------------------------------------------
+// One workgroup to a (segment, head): the states' half of the pass, blockIdx.y 1 for the
+// gradients' (last to first).
+template <int D, bool F32, bool REV>
+__device__ __forceinline__ void segment_state(const LinArgs& a, const LinSeg& sg, int h, uint16_t* lds,
+                                              LinFactors* fac) {
+  using C = LinCfg<D, F32>;
+  using T = typename Tok<F32>::T;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int hk = h / (a.heads / a.heads_k);
+  const LinTokens bt = REV ? a.q : a.k, ct = REV ? a.d_o : a.v;
+  const T* const bp = (const T*)bt.p + (int64_t)sg.tok * bt.ld + hk * D;
+  const T* const cp = (const T*)ct.p + (int64_t)sg.tok * ct.ld + h * D;
+  const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
+  uint16_t* const b = lds;
+  uint16_t* const cc = lds + C::TILE;
+  const int n = (sg.count + C::CH - 1) / C::CH;
+  LinState<D, F32> st;
+  st.zero();
+  double sum = 0.0;
+  LinFetch<D, F32, 256> fb, fc;
+  float gl = 0.f;
+  auto fetch = [&](int j) {
+    const int ci = REV ? n - 1 - j : j, t0 = ci * C::CH;
+    const int count = sg.count - t0 < C::CH ? sg.count - t0 : C::CH;
+    fb.load(bp + (int64_t)t0 * bt.ld, bt.ld, count);
+    fc.load(cp + (int64_t)t0 * ct.ld, ct.ld, count);
+    gl = gp && lane < count ? gp[(int64_t)(t0 + lane) * a.ld_g] : 0.f;
+    return count;
+  };
+  int count = fetch(0);
+  for (int j = 0; j < n; ++j) {
+    if (w == 3) lin_factors<REV>(fac, gl, REV ? a.scale : 1.f);
+    fb.store(b, count);
+    fc.store(cc, count);
+    __syncthreads();
+    if (j + 1 < n) count = fetch(j + 1);
+    st.scale(fac->last);
+    sum += fac->cs[63];
+    lin_tokens<D, F32, REV, false>(nullptr, st, nullptr, b, cc, fac, w, lane, g, c);
+    __syncthreads();
+  }
+  st.store(a.part[REV] + ((int64_t)(sg.slot + (REV ? -1 : 1)) * a.heads + h) * D * D, w, g, c);
+  if (threadIdx.x == 0) a.decay[REV][(int64_t)sg.slot * a.heads + h] = exp2_wide(sum);
+}
+
+template <int D, bool F32>
+__global__ __launch_bounds__(256, 2) void k_linear_states(LinArgs a) {
+  using C = LinCfg<D, F32>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * C::TILE];
+  __shared__ LinFactors fac;
+  const int h = blockIdx.x % a.heads;
+  const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
+  if (sg.count <= 0) return;
+  if (blockIdx.y == 0) {
+    if (!(sg.flags & 2)) segment_state<D, F32, false>(a, sg, h, lds, &fac);
+  } else {
+    if (!(sg.flags & 1)) segment_state<D, F32, true>(a, sg, h, lds, &fac);
+  }
+}
+
+// ---- join ------------------------------------------------------------------------
+// Four elements of a state a thread, a sequence's segments in order: each one's slot takes
+// the state at its start.  Loads of eight segments are in flight.
+__global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways, int64_t work) {
+  const int blocks = dd / 1024;  // of a state
+  for (int64_t x = blockIdx.x; x < work; x += gridDim.x) {
+    const int el = 4 * ((int)(x % blocks) * 256 + threadIdx.x);
+    const int64_t y = x / blocks, z = y / a.heads;
+    const int h = (int)(y % a.heads), rev = (int)(z % ways);
+    const int64_t b = z / ways;
+    int2 s = {0, 0};  // first slot, segments
+    if (a.sq.segs) {
+      s = a.sq.of_seq[b];
+    } else {
+      const int2 r = lin_range(a.sq);
+      s.y = lin_segs(a.sq, r.y - r.x);
+    }
+    if (s.y < 2) continue;
+    const float* const init = rev ? a.dstate_out : a.state_in;
+    f32x4 m = {0.f, 0.f, 0.f, 0.f};
+    if (init) m = *(const f32x4*)(init + (b * a.heads + h) * dd + el);
+    const int64_t first = ((int64_t)(rev ? s.x + s.y - 1 : s.x) * a.heads + h), step = rev ? -a.heads : a.heads;
+    float* const part = a.part[rev] + el;
+    const float* const decay = a.decay[rev];
+    *(f32x4*)(part + first * dd) = m;
+    constexpr int U = 8;
+    for (int i0 = 1; i0 < s.y; i0 += U) {
+      f32x4 add[U];
+      float f[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = first + (i0 + u < s.y ? i0 + u : s.y - 1) * step;
+        add[u] = *(const f32x4*)(part + at * dd);
+        f[u] = decay[at - step];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u >= s.y) break;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = fmaf(m[r], f[u], add[u][r]);
+        *(f32x4*)(part + (first + (i0 + u) * step) * dd) = m;
+      }
+    }
+  }
+}
+
+// ---- outputs -----------------------------------------------------------------------
+template <int D, bool F32>
+__global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void k_linear_out(LinArgs a) {
+  using C = LinCfg<D, F32>;
+  using T = typename Tok<F32>::T;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[3 * C::TILE + C::TRI];
+  __shared__ LinFactors fac;
+  const int h = blockIdx.x % a.heads;
+  const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
+  if (sg.count < 0) return;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int hk = h / (a.heads / a.heads_k);
+  uint16_t* const q = lds;
+  uint16_t* const k = q + C::TILE;
+  uint16_t* const v = k + C::TILE;
+  uint16_t* const tri = v + C::TILE;
+  LinState<D, F32> st;
+  const int64_t own = ((int64_t)sg.seq * a.heads + h) * D * D;
+  if (sg.flags != 3) st.template load<false>(a.part[0] + ((int64_t)sg.slot * a.heads + h) * D * D, w, g, c);
+  else if (a.state_in) st.template load<false>(a.state_in + own, w, g, c);
+  else st.zero();
+  const int n = (sg.count + C::CH - 1) / C::CH;
+  if (n > 0) {
+    const T* const qp = (const T*)a.q.p + (int64_t)sg.tok * a.q.ld + hk * D;
+    const T* const kp = (const T*)a.k.p + (int64_t)sg.tok * a.k.ld + hk * D;
+    const T* const vp = (const T*)a.v.p + (int64_t)sg.tok * a.v.ld + h * D;
+    T* const op = (T*)a.o + (int64_t)sg.tok * a.ld_o + h * D;
+    const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
+    LinFetch<D, F32, 256> fq, fk, fv;
+    float gl = 0.f;
+    auto fetch = [&](int j) {
+      const int t0 = j * C::CH, count = sg.count - t0 < C::CH ? sg.count - t0 : C::CH;
+      fq.load(qp + (int64_t)t0 * a.q.ld, a.q.ld, count);
+      fk.load(kp + (int64_t)t0 * a.k.ld, a.k.ld, count);
+      fv.load(vp + (int64_t)t0 * a.v.ld, a.v.ld, count);
+      gl = gp && lane < count ? gp[(int64_t)(t0 + lane) * a.ld_g] : 0.f;
+      return count;
+    };
+    int next = fetch(0);
+    for (int j = 0; j < n; ++j) {
+      const int count = next;
+      if (w == 3) lin_factors<false>(&fac, gl, a.scale);
+      fq.store(q, count);
+      fk.store(k, count);
+      fv.store(v, count);
+      __syncthreads();
+      if (j + 1 < n) next = fetch(j + 1);
+      for (int t = w; t < 2 * C::FRAGS; t += kLinWaves) {
+        const int f = t >> 1;
+        const int it = C::CH == 32 || f < 2 ? f : 2 + (f - 2) / 2, ts = C::CH == 32 || f < 2 ? 0 : (f - 2) & 1;
+        const int jt = 2 * ts + (t & 1);
+        const f32x4 x = lin_gate<false>(lin_tri<D, F32>(q, k, it, jt, g, c), &fac, a.scale, it, jt, g, c);
+        lin_put(tri, C::FRAGS, f, jt, lane, x);
+      }
+      LinOut<D, F32> out;
+      out.read(st, q, &fac, g, c);
+      st.scale(fac.last);
+      __syncthreads();
+      lin_tokens<D, F32, false, true>(&out, st, tri, k, v, &fac, w, lane, g, c);
+      out.store(op + (int64_t)j * C::CH * a.ld_o, a.ld_o, count, w, g, c);
+      __syncthreads();
+    }
+  }
+  if ((sg.flags & 2) && a.state_out) st.store(a.state_out + own, w, g, c);
+}
+
+template <int D>
+hipError_t states_any(const LinArgs& a, bool f32, bool both, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads), both ? 2 : 1), blk(256);
+  if (f32) hipLaunchKernelGGL((k_linear_states<D, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((k_linear_states<D, false>), grid, blk, 0, st, a);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t out_any(const LinArgs& a, bool f32, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(256);
+  if (f32) hipLaunchKernelGGL((k_linear_out<D, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((k_linear_out<D, false>), grid, blk, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linear_table(const LinSeqs& s, hipStream_t st) {
+  hipLaunchKernelGGL(k_linear_table, dim3(1), dim3(1024), 0, st, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, bool both, hipStream_t st) {
+  return d == 128 ? states_any<128>(a, f32, both, st) : states_any<64>(a, f32, both, st);
+}
+
+hipError_t launch_linear_join(const LinArgs& a, int d, bool both, hipStream_t st) {
+  const int ways = both ? 2 : 1;
+  const int64_t work = (int64_t)a.sq.n_seq * ways * a.heads * (d * d / 1024);
+  const int64_t blocks = work < 64 * kTargetWgs ? work : 64 * kTargetWgs;
+  hipLaunchKernelGGL(k_linear_join, dim3((unsigned)blocks), dim3(256), 0, st, a, d * d, ways, work);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_out(const LinArgs& a, int d, bool f32, hipStream_t st) {
+  return d == 128 ? out_any<128>(a, f32, st) : out_any<64>(a, f32, st);
+}
+
+}  // namespace zm
