@@ -337,6 +337,39 @@ typedef struct zm_rotary_desc {
 ZM_API int zm_rotary(const zm_rotary_desc* desc, int64_t n, const void* pos, const float* freqs,
               const void* q, const void* k, void* q_out, void* k_out, void* stream);
 
+/* The heads of q and k normalised and rotated in one pass: per head x of d_head elements
+ *   y = rotate((x - mu) / sqrt(mean((x - mu)^2) + eps) gamma + beta),
+ * mu = mean(x) (ZM_NORM_LAYER) or 0 (ZM_NORM_RMS), statistics in fp32 (elements below 2^60 in
+ * size), one rounding at the end, the rotation as zm_rotary's (rotary.inverse must be 0). */
+typedef enum zm_norm_kind { ZM_NORM_RMS = 0, ZM_NORM_LAYER = 1 } zm_norm_kind;
+
+typedef struct zm_norm_rotary_desc {
+  zm_rotary_desc rotary;
+  int32_t norm;         /* zm_norm_kind */
+  float eps;            /* > 0 */
+} zm_norm_rotary_desc;
+
+/* Arrays as for zm_rotary; gammas and betas: fp32 [d_head], 16-byte aligned, or NULL (ones,
+ * zeros), the same for every head of their tensor. */
+ZM_API int zm_norm_rotary(const zm_norm_rotary_desc* desc, int64_t n, const void* pos, const float* freqs,
+              const void* q, const void* k, const float* q_gamma, const float* q_beta,
+              const float* k_gamma, const float* k_beta, void* q_out, void* k_out, void* stream);
+
+/* Bytes of workspace of zm_norm_rotary_backward (16 KB a head dim at most; never less for more tokens). */
+ZM_API int zm_norm_rotary_backward_workspace_size(const zm_norm_rotary_desc* desc, int64_t n, size_t* bytes);
+
+/* The gradient from the inputs: dq_out, dk_out, the gradients of q_out, k_out (strides
+ * rotary.ld_q_out, ld_k_out), give dq, dk (the io type) and, fp32 [d_head], summed over tokens
+ * and heads, the parameters' gradients (each NULL: not wanted; without k's heads zeros).
+ * dq may be dq_out or q (same stride), dk dk_out or k; otherwise the outputs must not overlap
+ * other arrays.  Bitwise reproducible.  The workspace is needed with a parameter's gradient and n > 0. */
+ZM_API int zm_norm_rotary_backward(const zm_norm_rotary_desc* desc, int64_t n, const void* pos, const float* freqs,
+              const void* dq_out, const void* dk_out, const void* q, const void* k,
+              const float* q_gamma, const float* k_gamma,
+              void* dq, int64_t ld_dq, void* dk, int64_t ld_dk,
+              float* dq_gamma, float* dq_beta, float* dk_gamma, float* dk_beta,
+              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Gated delta rule: the linear fast weight f_S(x) = S x, S [d_head][d_head] fp32
  * per value head, trained token by token on |S k - v|^2 / 2 with a decay
  * (the notes' linear case of the fast weight, with one gradient step of rate
@@ -481,6 +514,31 @@ ZM_API int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, c
                   float* dg, float* dstate_in,
                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gradients' global norm and clipping: N = sqrt(sum of x^2 over all elements of all
+ * tensors), y = x min(1, max_norm / (N + 1e-6)).  Sums are in 64 bits, so N is finite
+ * for finite fp32 elements up to its own range.  An N that is infinite makes y 0 (NaN where x is
+ * infinite), one that is NaN makes every y NaN. */
+typedef struct zm_tensor {
+  const void* x;      /* n elements one after the other, aligned to one */
+  void* y;            /* where the clipped ones go: x itself, or an array of its own */
+  int64_t n;          /* 0..2^36; of none the pointers are not looked at */
+  int32_t dtype;      /* zm_dtype of x and y */
+  int32_t reserved;   /* must be 0 */
+} zm_tensor;
+
+/* Bytes of workspace of the two calls below for `count` tensors (at most 8192). */
+ZM_API int zm_grad_norm_workspace_size(int32_t count, size_t* bytes);
+
+/* norm (device, fp32): N.  tensors is host memory that is read during the call alone; the ys
+ * are not looked at.  Bitwise reproducible, as the next. */
+ZM_API int zm_grad_norm(const zm_tensor* tensors, int32_t count, float* norm,
+              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Writes every y, and N (before clipping) to norm.  max_norm: finite, >= 0.  No array may
+ * overlap another one (x may be its own y). */
+ZM_API int zm_clip_grads(const zm_tensor* tensors, int32_t count, float max_norm, float* norm,
+              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 ZM_API const char* zm_status_string(int status);
 
@@ -528,7 +586,8 @@ ZM_API int zm_ttt_layer(const zm_ttt_desc* desc, const zm_layer_weights* lw, int
 ZM_API const char* zm_ttt_last_error(void);
 
 /* Library version as major*10000 + minor*100 + patch.  Entry points that came
- * beside the others, none of which changed (zm_layer_norm, zm_rotary, zm_delta_rule and theirs),
+ * beside the others, none of which changed (zm_layer_norm, zm_rotary, zm_delta_rule, zm_linear_attention,
+ * zm_norm_rotary, zm_grad_norm, zm_clip_grads and theirs),
  * left the number as it was: a program that loads the library at run time looks for
  * their symbols. */
 ZM_API int zm_ttt_version(void);

@@ -24,6 +24,7 @@ STREAM_EMIT_BF16, STREAM_REUSE_BF16 = 0x100, 0x200
 SCRATCH_BYTES = 64 << 20  # ZM_TTT_SCRATCH_BYTES
 STEP_GRADIENT, STEP_NEWTON_SCHULZ = 0, 1
 ROTARY_HALVES, ROTARY_PAIRS, ROTARY_AXIS_HALVES = 0, 1, 2
+NORM_RMS, NORM_LAYER = 0, 1
 
 EXPORTED = (
     "zm_ttt_workspace_size", "zm_ttt_update", "zm_ttt_update_loss", "zm_ttt_apply",
@@ -35,6 +36,8 @@ EXPORTED = (
     "zm_delta_rule_backward_workspace_size", "zm_delta_rule_backward",
     "zm_linear_attention_workspace_size", "zm_linear_attention", "zm_linear_attention_step",
     "zm_linear_attention_backward_workspace_size", "zm_linear_attention_backward",
+    "zm_norm_rotary", "zm_norm_rotary_backward_workspace_size", "zm_norm_rotary_backward",
+    "zm_grad_norm_workspace_size", "zm_grad_norm", "zm_clip_grads",
 )
 
 
@@ -126,6 +129,24 @@ class LinearDesc(ctypes.Structure):
     ]
 
 
+class NormRotaryDesc(ctypes.Structure):
+    _fields_ = [
+        ("rotary", RotaryDesc),
+        ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -186,12 +207,24 @@ def load_library(path: str | None = None):
     lib.zm_linear_attention_backward_workspace_size.argtypes = [_AD, _I64, ctypes.POINTER(_SZ)]
     lib.zm_linear_attention_backward.argtypes = [_AD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                                  _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]
+    _RN = ctypes.POINTER(NormRotaryDesc)
+    lib.zm_norm_rotary.argtypes = [_RN, _I64] + [_P] * 11
+    lib.zm_norm_rotary_backward_workspace_size.argtypes = [_RN, _I64, ctypes.POINTER(_SZ)]
+    lib.zm_norm_rotary_backward.argtypes = [_RN, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P,
+                                            _I64, _P, _P, _P, _P, _P, _SZ, _P]
+    _TL = ctypes.POINTER(Tensor)
+    lib.zm_grad_norm_workspace_size.argtypes = [ctypes.c_int32, ctypes.POINTER(_SZ)]
+    lib.zm_grad_norm.argtypes = [_TL, ctypes.c_int32, _P, _P, _SZ, _P]
+    lib.zm_clip_grads.argtypes = [_TL, ctypes.c_int32, ctypes.c_float, _P, _P, _SZ, _P]
     for name in ("zm_layer_norm", "zm_layer_norm_backward_workspace_size",
                  "zm_layer_norm_backward", "zm_rotary", "zm_delta_rule_workspace_size",
                  "zm_delta_rule", "zm_delta_rule_step", "zm_delta_rule_backward_workspace_size",
                  "zm_delta_rule_backward", "zm_linear_attention_workspace_size",
                  "zm_linear_attention", "zm_linear_attention_step",
-                 "zm_linear_attention_backward_workspace_size", "zm_linear_attention_backward"):
+                 "zm_linear_attention_backward_workspace_size", "zm_linear_attention_backward",
+                 "zm_norm_rotary", "zm_norm_rotary_backward_workspace_size",
+                 "zm_norm_rotary_backward", "zm_grad_norm_workspace_size", "zm_grad_norm",
+                 "zm_clip_grads"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("zm_ttt_workspace_size", "zm_ttt_update", "zm_ttt_update_loss", "zm_ttt_apply",
                  "zm_ttt_update_apply", "zm_ttt_update_apply_scratch",
@@ -696,14 +729,8 @@ def _heads_rows(name, t, n, heads, d, dtype):
     return t.stride(0) if n > 1 else heads * d
 
 
-def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_out=None,
-           k_out=None):
-    """Rotates q [n, Hq, d] and k [n, Hk, d] (or None) by their positions: pos
-    [n, axes] int32 or fp32, freqs fp32 [P], sections the pairs of each axis
-    (sum P <= d / 2; dims from 2 P on pass unrotated), layout how the dims pair
-    (ROTARY_HALVES, ROTARY_PAIRS, ROTARY_AXIS_HALVES).  inverse=True turns
-    back, which is the gradient.  q_out=q, k_out=k rotate in place.  Returns
-    (q_out, k_out)."""
+def _rotary_inputs(q, k, pos, freqs, sections):
+    """Shape and type checks of a rotation's inputs: (n, heads of q, of k, d, the sections)."""
     if q.dim() != 3:
         raise ZmError("q must be [n, heads, d]")
     n, hq, d = q.shape
@@ -719,6 +746,18 @@ def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_ou
             or not pos.is_contiguous():
         raise ZmError(f"pos must be contiguous int32 or fp32 [{n}, {len(sec)}]")
     _vector(freqs, sum(sec), "freqs")
+    return n, hq, hk, d, sec
+
+
+def rotary(q, k, pos, freqs, sections, layout=ROTARY_HALVES, inverse=False, q_out=None,
+           k_out=None):
+    """Rotates q [n, Hq, d] and k [n, Hk, d] (or None) by their positions: pos
+    [n, axes] int32 or fp32, freqs fp32 [P], sections the pairs of each axis
+    (sum P <= d / 2; dims from 2 P on pass unrotated), layout how the dims pair
+    (ROTARY_HALVES, ROTARY_PAIRS, ROTARY_AXIS_HALVES).  inverse=True turns
+    back, which is the gradient.  q_out=q, k_out=k rotate in place.  Returns
+    (q_out, k_out)."""
+    n, hq, hk, d, sec = _rotary_inputs(q, k, pos, freqs, sections)
     qo = q.new_empty((n, hq, d)) if q_out is None else q_out
     ko = k_out
     if k is not None and ko is None:
@@ -998,6 +1037,162 @@ def linear_attention_backward(do, q, k, v, g=None, state=None, dstate=None, offs
          lds[0], _ptr(dk), lds[1], _ptr(dv), lds[2], _ptr(dg), _ptr(dstart), _ptr(ws),
          _ws_bytes(ws))
     return out
+
+
+def _norm_params(d, **params):
+    for name, p in params.items():
+        _vector(p, d, name)
+
+
+def norm_rotary(q, k, pos, freqs, sections, q_gamma=None, k_gamma=None, q_beta=None, k_beta=None,
+                eps=1e-6, norm=NORM_RMS, layout=ROTARY_HALVES, q_out=None, k_out=None):
+    """Every head of q [n, Hq, d] and k [n, Hk, d] (or None) normalised (NORM_RMS: by the root
+    of its mean square; NORM_LAYER: also less its mean), times gamma plus beta (fp32 [d] or
+    None) and rotated by its token's positions as `rotary` does, in one pass.  q_out=q,
+    k_out=k work in place.  Returns (q_out, k_out)."""
+    n, hq, hk, d, sec = _rotary_inputs(q, k, pos, freqs, sections)
+    _norm_params(d, q_gamma=q_gamma, k_gamma=k_gamma, q_beta=q_beta, k_beta=k_beta)
+    qo = q.new_empty((n, hq, d)) if q_out is None else q_out
+    ko = k_out
+    if k is not None and ko is None:
+        ko = k.new_empty((n, hk, d))
+    ldq, ldqo = _heads_rows("q", q, n, hq, d, q.dtype), _heads_rows("q_out", qo, n, hq, d, q.dtype)
+    ldk = ldko = 0
+    if k is not None:
+        ldk = _heads_rows("k", k, n, hk, d, q.dtype)
+        ldko = _heads_rows("k_out", ko, n, hk, d, q.dtype)
+    _same_gpu(q, k, pos, freqs, q_gamma, k_gamma, q_beta, k_beta, qo, ko)
+    desc = NormRotaryDesc(RotaryDesc(hq, hk, d, _IO[q.dtype], int(layout), 0,
+                                     1 if pos.dtype == torch.float32 else 0, len(sec),
+                                     (ctypes.c_int32 * 4)(*sec), ldq, ldk, ldqo, ldko),
+                          int(norm), float(eps))
+    _run("zm_norm_rotary", q.device, ctypes.byref(desc), n, _ptr(pos), _ptr(freqs), _ptr(q),
+         _ptr(k), _ptr(q_gamma), _ptr(q_beta), _ptr(k_gamma), _ptr(k_beta), _ptr(qo), _ptr(ko))
+    return qo, ko
+
+
+def norm_rotary_backward_workspace_size(desc: NormRotaryDesc, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().zm_norm_rotary_backward_workspace_size(ctypes.byref(desc), int(n),
+                                                                 ctypes.byref(out)),
+           "zm_norm_rotary_backward_workspace_size")
+    return int(out.value)
+
+
+def norm_rotary_backward(dq_out, dk_out, q, k, pos, freqs, sections, q_gamma=None, k_gamma=None,
+                         eps=1e-6, norm=NORM_RMS, layout=ROTARY_HALVES, out=None, workspace=None):
+    """Gradients of norm_rotary from its inputs and those of its outputs: (dq, dk, dq_gamma,
+    dk_gamma, dq_beta, dk_beta), the parameters' fp32 [d] whether gammas are given or not
+    (dk, dk_gamma and dk_beta None without k).  out: those six tensors to write to, the
+    parameters' None where not wanted; dq may be dq_out or q, dk dk_out or k."""
+    n, hq, hk, d, sec = _rotary_inputs(q, k, pos, freqs, sections)
+    _norm_params(d, q_gamma=q_gamma, k_gamma=k_gamma)
+    if (k is None) != (dk_out is None):
+        raise ZmError("dk_out is needed with k, and only with it")
+    if out is None:
+        both = torch.empty((4, d), dtype=torch.float32, device=q.device)
+        out = (q.new_empty((n, hq, d)), None if k is None else k.new_empty((n, hk, d)), both[0],
+               None if k is None else both[1], both[2], None if k is None else both[3])
+    if len(out) != 6:
+        raise ZmError("out: the six tensors dq, dk, dq_gamma, dk_gamma, dq_beta, dk_beta")
+    dq, dk, dqg, dkg, dqb, dkb = out
+    _norm_params(d, dq_gamma=dqg, dk_gamma=dkg, dq_beta=dqb, dk_beta=dkb)
+    lds = [_heads_rows(name, t, n, hq, d, q.dtype)
+           for name, t in (("q", q), ("dq_out", dq_out), ("dq", dq))]
+    ldks = [0, 0, 0]
+    if k is not None:
+        if dk is None:
+            raise ZmError("out: dk is needed with k")
+        ldks = [_heads_rows(name, t, n, hk, d, q.dtype)
+                for name, t in (("k", k), ("dk_out", dk_out), ("dk", dk))]
+    _same_gpu(q, k, dq_out, dk_out, pos, freqs, q_gamma, k_gamma, *out, workspace)
+    desc = NormRotaryDesc(RotaryDesc(hq, hk, d, _IO[q.dtype], int(layout), 0,
+                                     1 if pos.dtype == torch.float32 else 0, len(sec),
+                                     (ctypes.c_int32 * 4)(*sec), lds[0], ldks[0], lds[1],
+                                     ldks[1]), int(norm), float(eps))
+    ws = workspace
+    if ws is None:
+        need = norm_rotary_backward_workspace_size(desc, n)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _run("zm_norm_rotary_backward", q.device, ctypes.byref(desc), n, _ptr(pos), _ptr(freqs),
+         _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_gamma), _ptr(k_gamma), _ptr(dq),
+         lds[2], _ptr(dk), ldks[2], _ptr(dqg), _ptr(dqb), _ptr(dkg), _ptr(dkb), _ptr(ws),
+         _ws_bytes(ws))
+    return out
+
+
+class TensorList:
+    """Gradients (contiguous bf16 or fp32 tensors of one GPU) laid out once for grad_norm and
+    clip_grads; out: where the clipped ones go (None: in place).  It keeps the tensors alive, and
+    they keep their memory: one whose storage is exchanged needs a new list."""
+
+    def __init__(self, tensors, out=None):
+        self.tensors = list(tensors)
+        self.out = self.tensors if out is None else list(out)
+        if len(self.out) != len(self.tensors):
+            raise ZmError(f"{len(self.out)} outputs for {len(self.tensors)} tensors")
+        self.array = (Tensor * max(len(self.tensors), 1))()
+        self.device = self.tensors[0].device if self.tensors else None
+        for i, (x, y) in enumerate(zip(self.tensors, self.out)):
+            if x.dtype not in _IO or not x.is_contiguous():
+                raise ZmError(f"tensor {i} must be contiguous bf16 or fp32")
+            if y is not x and (y.dtype != x.dtype or y.shape != x.shape or not y.is_contiguous()):
+                raise ZmError(f"output {i} must be contiguous {x.dtype} {tuple(x.shape)}")
+            self.array[i] = Tensor(x.data_ptr(), y.data_ptr(), x.numel(), _IO[x.dtype], 0)
+        if self.tensors:
+            _same_gpu(*self.tensors, *(() if out is None else self.out))
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def grad_norm_workspace_size(count: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().zm_grad_norm_workspace_size(int(count), ctypes.byref(out)),
+           "zm_grad_norm_workspace_size")
+    return int(out.value)
+
+
+def _norm_call(tensors, norm, workspace):
+    if not len(tensors) and norm is None:
+        raise ZmError("no tensors: pass norm, an fp32 tensor of one element on the GPU")
+    device = tensors.device if len(tensors) else norm.device
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=device)
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ZmError("norm must be an fp32 tensor of one element")
+    if not norm.is_cuda or norm.device != device or \
+            (workspace is not None and workspace.device != device):
+        raise ZmError("tensors, norm and workspace must be on one GPU")
+    if workspace is None:
+        workspace = torch.empty(grad_norm_workspace_size(len(tensors)), dtype=torch.uint8,
+                                device=device)
+    return norm, workspace
+
+
+def grad_norm(tensors, norm=None, workspace=None):
+    """The root of the sum of all squares of a list of tensors (or a TensorList), summed in
+    64 bits; returns norm, fp32 of one element."""
+    tensors = tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+    norm, ws = _norm_call(tensors, norm, workspace)
+    _run("zm_grad_norm", norm.device, tensors.array, len(tensors), _ptr(norm), _ptr(ws),
+         _ws_bytes(ws))
+    return norm
+
+
+def clip_grads(tensors, max_norm, out=None, norm=None, workspace=None):
+    """Scales a list of tensors (or a TensorList, which then has the outputs) by
+    min(1, max_norm / (N + 1e-6)), N their global norm: in place, or into out.  Returns N
+    (before clipping), fp32 of one element."""
+    if isinstance(tensors, TensorList):
+        if out is not None:
+            raise ZmError("a TensorList has its outputs: pass out to it")
+    else:
+        tensors = TensorList(tensors, out)
+    norm, ws = _norm_call(tensors, norm, workspace)
+    _run("zm_clip_grads", norm.device, tensors.array, len(tensors), float(max_norm), _ptr(norm),
+         _ptr(ws), _ws_bytes(ws))
+    return norm
 
 
 def set_profile_events(events):

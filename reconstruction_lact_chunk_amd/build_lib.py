@@ -22,7 +22,8 @@ ARCH = "gfx950"
 
 SOURCES = ["weights.hip", "update_bf16.hip", "apply_bf16.hip", "frame_bf16.hip", "fp32_path.hip",
            "newton_schulz.hip", "wide_kernels.hip", "wide_gemm.hip", "wide_path.cpp", "gemm_lt.cpp",
-           "layer_kernels.hip", "wide_ns.hip", "layer_norm.hip", "rotary.hip", "seq_api.cpp",
+           "layer_kernels.hip", "wide_ns.hip", "layer_norm.hip", "rotary.hip", "norm_rotary.hip",
+           "seq_api.cpp", "grad_clip.hip", "grad_api.cpp",
            "delta_prep.hip", "delta_scan.hip", "delta_fused.hip",
            "delta_step.hip", "delta_grad.hip", "delta_api.cpp", "linear_attn.hip", "linear_grad.hip",
            "linear_step.hip", "linear_api.cpp", "api.cpp"]

@@ -1,5 +1,6 @@
 // Launchers of the operators around a streamed token sequence: layer norm
-// (layer_norm.hip) and multi-axis rotary positions (rotary.hip).
+// (layer_norm.hip), multi-axis rotary positions (rotary.hip) and both on the heads
+// of q and k (norm_rotary.hip).
 #pragma once
 
 #include "zm_internal.h"
@@ -41,5 +42,29 @@ struct RotaryArgs {
   bool f32, pos_f32, inverse;
 };
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t st);
+
+// ---- heads normalised and rotated -------------------------------------------------
+struct NormRotaryArgs {
+  RotaryArgs r;             // forward: x to y; backward: x and the gradient's rows, below
+  const float* gamma[2];    // of q, k: [d] or null (ones)
+  const float* beta[2];     // or null (zeros)
+  float eps;
+  bool layer;               // layer norm, else RMS norm
+  // backward
+  const void* dy[2];        // gradients of the rotated rows, strides r.q.ldy, r.k.ldy
+  void* dx[2];
+  int64_t lddx[2];
+  float* part;              // norm_rotary_slots(..) x 4 x d: sums for gamma q, beta q, gamma k, beta k
+  bool params;              // some of dparam is wanted
+  float* dparam[4];         // those sums, each may be null
+};
+// Workgroups of the backward at most, each with a partial sum of the parameter gradients.
+constexpr int kNormRotarySlots = 4 * kTargetWgs;
+inline int64_t norm_rotary_slots(int64_t n, int heads) {
+  const int64_t s = n * heads;
+  return s < kNormRotarySlots ? s : kNormRotarySlots;
+}
+hipError_t launch_norm_rotary(const NormRotaryArgs& a, hipStream_t st);
+hipError_t launch_norm_rotary_backward(const NormRotaryArgs& a, hipStream_t st);
 
 }  // namespace zm
