@@ -121,6 +121,7 @@ size_t backward_ws(LinArgs& a, const zm_linear_desc* d, const LinPlan& p, int64_
   const size_t dd = (size_t)d->d_head * d->d_head, rows = (size_t)n * d->heads * d->d_head;
   a.flow = c.take<float>((size_t)n * d->heads);
   a.d_dump = c.take<float>((size_t)p.n_chunks * d->heads * dd);
+  a.d_exp = c.take<double>((size_t)p.n_chunks * d->heads);
   *sums = d->ld_g == 0 ? c.take<float>((size_t)p.n_chunks * d->heads) : nullptr;
   if (d->heads != d->heads_k) {
     a.o_part = c.take<float>(rows);

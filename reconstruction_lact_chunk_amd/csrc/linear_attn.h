@@ -14,6 +14,12 @@
 //   dk            V    dO   Q    D^T            exp(c_C - c)   scale exp(c)        last to first
 //   out = f o (A state) + T C,  T = scale G o (A B^T) (G^T, last to first),
 //   state <- exp(c_C) state + B^T (w o C).
+// Decays are taken out where they can be.  With the state held as 2^s M^ and e_i = s plus the
+// decay from the chunk's first (last) edge up to token i, all in powers of two,
+//   out = 2^e_i (A M^ + lower(A B^T) (C_j / 2^e_j)),  M^ <- M^ + B^T (C / 2^e),  s <- s + c_C
+// (scale with one of the two powers): the same numbers up to the powers, which come from 64-bit exponents
+// (exp2_wide), while |e| stays under kLinSpan.  A chunk that would leave that range
+// takes 2^s into M^ first; one whose own decays do (a reset) is formed with them in place.
 // So the gradients need no state of any chunk in memory.  Few long sequences are cut into
 // segments: a first pass leaves what each adds to the state, a join makes the states at
 // their starts (or ends) of these.
@@ -28,29 +34,28 @@
 // fp32 tokens) as a sum of three bf16 parts (delta_rule.h): 24 bits, so the state and the
 // outputs up to their own rounding are as exact as fp32 products would leave them.
 //
-// A wave holds CT * 16 columns of the state and all its rows; its accumulators are operands
-// of the next product as they are, column mt = CT w + ct, c at dim_row(mt, c), and an
-// output's rows (columns of the state) are consecutive in a lane.
+// A wave holds 16 columns of the state and all its rows; its accumulators are operands of
+// the next product as they are.  Outputs are formed transposed, so that a lane has four
+// consecutive dims of a token.
 #pragma once
 
 #include "delta_rule.h"
 
 namespace zm {
 
-constexpr int kLinWaves = 4;  // waves to a state
-
 template <int D, bool F32>
 struct LinCfg {
   static constexpr int CH = F32 ? 32 : 64;       // tokens of a chunk
   static constexpr int NT = F32 ? 3 : 1;         // parts of a token element
   static constexpr int LIM = F32 ? 2 : 0;        // order of the parts' products of two tokens
-  static constexpr int CT = D / (16 * kLinWaves);  // 16-column tiles of a wave
+  static constexpr int WAVES = D / 16;           // to a state
+  static constexpr int THREADS = 64 * WAVES;
   static constexpr int KS = D / 32;              // steps over the head dims
   static constexpr int MT = D / 16;              // row tiles of the state
   static constexpr int IT = CH / 16;             // token tiles
   static constexpr int TS = CH / 32;             // steps over the tokens
   static constexpr int FRAGS = CH == 64 ? 6 : 2; // operand tiles of a triangle
-  static constexpr int PITCH = D + 16;           // elements of a row in LDS
+  static constexpr int PITCH = F32 ? D + 16 : D; // elements of a row in LDS
   static constexpr int PART = CH * PITCH;        // elements of one part of a tile
   static constexpr int TILE = NT * PART;
   static constexpr int TRI = 3 * FRAGS * kFragElems;
@@ -58,16 +63,20 @@ struct LinCfg {
 
 // What a chunk's tokens are multiplied with; computed by one wave.
 struct LinFactors {
-  float f[64];     // of A's rows
-  float w[64];     // of C's rows in the state
-  float ti[64];    // T = ti[out] tj[source], unless `gated`
-  float tj[64];
-  double cs[64];   // sums of decays, powers of two
-  float last;      // of the state
-  int gated;       // they span too much for ti tj: every element from its own difference
-  float pad[2];
+  float up[64];    // of outputs; kLinGated: of A M^ alone
+  float dn[64];    // of C in the state and, unless kLinGated, of T's columns
+  double cs[64];   // sums of the chunk's decays, powers of two
+  double s;        // exponent of the state
+  double after;    // of the state behind the chunk
+  double sum;      // of all decays up to the chunk's
+  int count;       // tokens; dn is zero past them
+  float pre;       // kLinScale: of the state before the chunk
+  float last;      // kLinGated: of the state after the outputs' read
+  float end;       // 2^exponent of the state behind the chunk
+  int flags;
 };
-constexpr double kLinSpan = 60.0;  // ti and tj stay in 2^-60 .. 2^60
+enum { kLinGated = 1, kLinScale = 2 };
+constexpr double kLinSpan = 60.0;
 
 struct LinSeg {
   int tok, count;   // first token, tokens (-1: unused)
@@ -117,7 +126,8 @@ struct LinArgs {
   float* o_part;       // dq and dk to each value head [n][heads][d], where these share key heads
   float* dk_part;
   float* flow;         // [n][heads]: the part of dg that the reverse pass forms, or null without g
-  float* d_dump;       // D^T at every chunk's end
+  float* d_dump;       // D^T at every chunk's end, less a power of two
+  double* d_exp;       // [chunks][heads] that power
   float* dg;           // [n][heads], or, with ld_g = 0, the chunks' sums [chunks][heads]
 };
 
@@ -158,94 +168,215 @@ __device__ __forceinline__ LinSeg lin_seg(const LinSeqs& s, int si) {
   return g;
 }
 
-// Rows of a token tensor on their way from memory to LDS: THREADS threads, E-element
-// granules.  Rows past `count` are zero in LDS.
-template <int D, bool F32, int THREADS>
+// x as three bf16 parts, each what 8 bits hold of what the ones before leave, cut off: the sum
+// is x to its last bit, and a part of two elements is one instruction.
+__device__ __forceinline__ Parts<3> cut8(const float* x) {
+  Parts<3> out;
+  unsigned r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(x[i]);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(r[2 * i + 1], r[2 * i], 0x07060302u);
+    out.p[p] = as_bf16x8(w);
+    if (p < 2)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        r[i] = __float_as_uint(__uint_as_float(r[i]) - __uint_as_float(r[i] & 0xffff0000u));
+  }
+  return out;
+}
+__device__ __forceinline__ Parts<3> cut_tiles(const f32x4& a, const f32x4& b) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return cut8(x);
+}
+
+// Tiles of token rows in LDS.  bf16: the row's granules (8 elements) in the order p ^
+// lin_swizzle(row), so that the 16 lanes that a read serves at once, of 4 + 4 rows and two
+// granules, spread over the banks, and a wave's direct load can write 64 granules one after the other.
+// fp32: three parts, rows of PITCH elements.
+template <int D>
+__device__ __forceinline__ constexpr int lin_swizzle(int r) {
+  return D == 128 ? ((r & 3) << 2) | (((r >> 3) & 1) << 1) : (((r >> 1) & 1) << 2) | (((r >> 3) & 1) << 1);
+}
+template <int D, bool F32>
+__device__ __forceinline__ int lin_at(int row, int granule) {
+  return row * LinCfg<D, F32>::PITCH + 8 * (F32 ? granule : granule ^ lin_swizzle<D>(row));
+}
+
+// A lane's number that the compiler does not know to be the same every time: what follows from
+// it (addresses) is formed again where it is used, and not kept in registers over the loop.
+struct LinLane {
+  int lane, g, c;
+  __device__ __forceinline__ explicit LinLane(int l) {
+    asm volatile("" : "+v"(l));
+    lane = l;
+    g = l >> 4;
+    c = l & 15;
+  }
+};
+
+__device__ __forceinline__ void lin_wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
+// A chunk's rows of a token tensor on their way from memory to a tile.  Rows past `count` are
+// the last token's: finite where that is, and their dn of zero leaves them out.  A lane's
+// place is a 32-bit offset from the chunk's first row (63 rows of 2^24 fp32 elements stay
+// under 2^32).
+//
+// By way of registers (fp32 elements are cut into their parts there):
+template <int D, bool F32>
 struct LinFetch {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
-  static constexpr int GPR = D / 8, N = C::CH * GPR / THREADS;
-  static_assert(C::CH * GPR % THREADS == 0, "granules");
+  static constexpr int GPR = D / 8, N = C::CH * GPR / C::THREADS, STEP = C::THREADS / GPR;
+  static_assert(C::CH * GPR % C::THREADS == 0 && C::THREADS % GPR == 0, "granules");
   u32x4 raw[N][F32 ? 2 : 1];
-
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int count) {
+  __device__ __forceinline__ void load(const T* base, unsigned ld, int count) {
+    const int row = threadIdx.x % C::THREADS / GPR, col = 8 * (threadIdx.x % GPR);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int gr = threadIdx.x % THREADS + THREADS * i, row = gr / GPR, col = 8 * (gr % GPR);
-      const T* const p = base + (int64_t)(row < count ? row : count - 1) * ld + col;
+      const unsigned r = row + STEP * i, from = (int)r < count ? r : count - 1;
+      const char* const p = (const char*)base + (from * ld + col) * (unsigned)sizeof(T);
       raw[i][0] = *(const u32x4*)p;
-      if constexpr (F32) raw[i][1] = *(const u32x4*)(p + 4);
+      if constexpr (F32) raw[i][1] = *(const u32x4*)(p + 16);
     }
   }
-  __device__ __forceinline__ void store(uint16_t* tile, int count) const {
+  __device__ __forceinline__ void store(uint16_t* tile) {
+    const int row = threadIdx.x % C::THREADS / GPR, gr = threadIdx.x % GPR;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int gr = threadIdx.x % THREADS + THREADS * i, row = gr / GPR, col = 8 * (gr % GPR);
-      uint16_t* const at = tile + row * C::PITCH + col;
-      const bool in = row < count;
+      uint16_t* const at = tile + lin_at<D, F32>(row + STEP * i, gr);
       if constexpr (F32) {
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = in ? __uint_as_float(raw[i][e >> 2][e & 3]) : 0.f;
-        const Parts<3> p = split8<3>(x);
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(raw[i][e >> 2][e & 3]);
+        const Parts<3> p = cut8(x);
 #pragma unroll
         for (int k = 0; k < 3; ++k) *(bf16x8*)(at + k * C::PART) = p.p[k];
       } else {
-        u32x4 x = raw[i][0];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = in ? x[e] : 0u;
-        *(u32x4*)at = x;
+        *(u32x4*)at = raw[i][0];
       }
     }
   }
 };
-
-// Parts of 8 elements of a row, and of 8 tokens (order dtau) of column dim_row(mt, c).
-template <int D, bool F32>
-__device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_row(const uint16_t* t, int row, int col) {
-  using C = LinCfg<D, F32>;
-  Parts<C::NT> p;
+// bf16 straight into LDS by the D / 16 waves of a state: the tile has to be free when the load
+// starts, and is there after lin_wait_loads and a barrier.  LDS reads in between would
+// wait for the load.
+template <int D>
+__device__ __forceinline__ void lin_load(uint16_t* tile, const uint16_t* base, unsigned ld, int count, int w, int lane) {
+  using C = LinCfg<D, false>;
+  constexpr int GPR = D / 8, RPL = 64 / GPR, N = C::CH / RPL / C::WAVES;  // rows of a load, loads of a wave
 #pragma unroll
-  for (int k = 0; k < C::NT; ++k) p.p[k] = *(const bf16x8*)(t + k * C::PART + row * C::PITCH + col);
-  return p;
-}
-template <int D, bool F32>
-__device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_col(const uint16_t* t, int mt, int ts, int g, int c) {
-  using C = LinCfg<D, F32>;
-  Parts<C::NT> p;
-  const int row = 32 * ts + dtau(g, c >> 2), col = 32 * (mt >> 1) + 8 * (c & 3) + 4 * (mt & 1);
-#pragma unroll
-  for (int k = 0; k < C::NT; ++k) {
-    const uint16_t* const at = t + k * C::PART + row * C::PITCH + col;
-    p.p[k] = __builtin_shufflevector(delta_read_tr(at), delta_read_tr(at + 8 * C::PITCH), 0, 1, 2, 3, 4, 5, 6, 7);
+  for (int i = 0; i < N; ++i) {
+    const int r0 = (N * w + i) * RPL, r = r0 + lane / GPR;
+    const unsigned from = r < count ? r : count - 1;
+    const unsigned off = (from * ld + 8 * ((lane % GPR) ^ lin_swizzle<D>(r))) * 2u;
+    __builtin_amdgcn_global_load_lds((const void*)((const char*)base + off),
+                                     (__attribute__((address_space(3))) void*)(tile + r0 * D), 16, 0, 0);
   }
-  return p;
 }
 
-// The factors of a chunk from its lanes' log decays (zero past the tokens); one wave.
+// Parts of granule `gr` of a row, and of 8 tokens (order dtau) of column dim_row(mt, c), or of
+// column 16 w + c.
+template <int D, bool F32>
+__device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_row(const uint16_t* t, int row, int gr) {
+  using C = LinCfg<D, F32>;
+  Parts<C::NT> p;
+#pragma unroll
+  for (int k = 0; k < C::NT; ++k) p.p[k] = *(const bf16x8*)(t + k * C::PART + lin_at<D, F32>(row, gr));
+  return p;
+}
+template <int D, bool F32>
+__device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_read_tr(const uint16_t* t, int ts, int granule, int half, int g,
+                                                                 int c) {
+  using C = LinCfg<D, F32>;
+  Parts<C::NT> p;
+  const int row = 32 * ts + dtau(g, c >> 2);
+#pragma unroll
+  for (int k = 0; k < C::NT; ++k)
+    p.p[k] = __builtin_shufflevector(delta_read_tr(t + k * C::PART + lin_at<D, F32>(row, granule) + half),
+                                     delta_read_tr(t + k * C::PART + lin_at<D, F32>(row + 8, granule) + half), 0, 1, 2, 3,
+                                     4, 5, 6, 7);
+  return p;
+}
+template <int D, bool F32>
+__device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_row_dims(const uint16_t* t, int mt, int ts, int g, int c) {
+  return lin_read_tr<D, F32>(t, ts, 4 * (mt >> 1) + (c & 3), 4 * (mt & 1), g, c);
+}
+template <int D, bool F32>
+__device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_columns(const uint16_t* t, int w, int ts, int g, int c) {
+  return lin_read_tr<D, F32>(t, ts, 2 * w + ((c & 3) >> 1), 4 * (c & 1), g, c);
+}
+
+// Sums over the lanes up to each one: shifts within 16 lanes, then the rows' last lanes to
+// the next row and to the upper half.  No addresses, as exchanges through LDS take them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lin_add_from(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)b, CTRL, ROWS, 0xf, false);
+  const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), CTRL, ROWS, 0xf, false);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lin_prefix(double x) {
+  x = lin_add_from<0x111, 0xf>(x);  // one lane on
+  x = lin_add_from<0x112, 0xf>(x);
+  x = lin_add_from<0x114, 0xf>(x);
+  x = lin_add_from<0x118, 0xf>(x);
+  x = lin_add_from<0x142, 0xa>(x);  // lane 15 to row 1, 47 to row 3
+  return lin_add_from<0x143, 0xc>(x);  // lane 31 to rows 2 and 3
+}
+__device__ __forceinline__ double lin_lane63(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const unsigned lo = __builtin_amdgcn_readlane((unsigned)b, 63), hi = __builtin_amdgcn_readlane((unsigned)(b >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The factors of a chunk from its lanes' log decays; one wave.  before: those of the chunk
+// before it in the pass, null for the first.
 template <bool REV>
-__device__ __forceinline__ void lin_factors(LinFactors* f, float gl, float scale) {
+__device__ __forceinline__ void lin_factors(LinFactors* f, const LinFactors* before, float gl, int count, float scale) {
   const int lane = threadIdx.x & 63;
+  if (lane >= count) gl = 0.f;
   if (gl < kMinLogDecay) gl = kMinLogDecay;
+  double s = before ? before->after : 0.0;
   // in 64 bits: a strong decay among weak ones must not blur their differences
-  double s = gl * kLog2E;
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) {
-    const double o = __shfl_up(s, m, 64);
-    if (lane >= m) s += o;
+  const double c = lin_prefix(gl * kLog2E);
+  const double last = lin_lane63(c), e0 = REV ? last - c : c;
+  auto leaves = [&](double e) { return __any(!(fabs(e) <= kLinSpan)) || !(fabs(s + last) <= kLinSpan); };
+  int flags = 0;
+  float pre = 1.f;
+  if (leaves(s + e0)) {
+    flags = kLinScale;
+    pre = exp2_wide(s);
+    s = 0.0;
+    if (leaves(e0)) flags |= kLinGated;
   }
-  const double last = __shfl(s, 63, 64), ref = 0.5 * (last + __shfl(s, 0, 64));
-  const float in = scale * exp2_wide(s), out = exp2_wide(last - s);
-  f->f[lane] = REV ? out : in;
-  f->w[lane] = REV ? in : out;
-  const float up = scale * exp2_wide(s - ref), down = exp2_wide(ref - s);
-  f->ti[lane] = REV ? down : up;
-  f->tj[lane] = REV ? up : down;
-  f->cs[lane] = s;
-  const bool wide = __any(!(fabs(s - ref) <= kLinSpan));
+  float up, dn;
+  if (flags & kLinGated) {
+    const float in = scale * exp2_wide(c), out = exp2_wide(last - c);
+    up = REV ? out : in;
+    dn = REV ? in : out;
+  } else {
+    up = exp2_wide(s + e0);
+    dn = exp2_wide(-(s + e0));
+    if (REV) dn *= scale;
+    else up *= scale;
+  }
+  f->up[lane] = up;
+  f->dn[lane] = lane < count ? dn : 0.f;
+  f->cs[lane] = c;
   if (lane == 0) {
+    const double after = flags & kLinGated ? 0.0 : s + last;
+    f->s = s;
+    f->after = after;
+    f->sum = (before ? before->sum : 0.0) + last;
+    f->count = count;
+    f->pre = pre;
     f->last = exp2_wide(last);
-    f->gated = wide;
+    f->end = exp2_wide(after);
+    f->flags = flags;
   }
 }
 
@@ -266,162 +397,126 @@ __device__ __forceinline__ f32x4 lin_tri(const uint16_t* a, const uint16_t* b, i
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < C::KS; ++s) {
-    const auto bb = lin_row<D, F32>(b, token_row(jt, c), 32 * s + 8 * g);
-    const auto aa = lin_row<D, F32>(a, 16 * it + c, 32 * s + 8 * g);
+    const auto bb = lin_row<D, F32>(b, token_row(jt, c), 4 * s + g);
+    const auto aa = lin_row<D, F32>(a, 16 * it + c, 4 * s + g);
     mma<C::LIM>(acc, bb, aa);
   }
   return acc;
 }
 
-// The same with the decays and the mask.
+// The same with the decays (kLinGated: all of them) and the mask.
 template <bool REV>
 __device__ __forceinline__ f32x4 lin_gate(const f32x4& x, const LinFactors* f, float scale, int it, int jt, int g,
                                           int c) {
   const int out = 16 * it + c, src = token_row(jt, 4 * g);
   f32x4 t;
-  if (f->gated) {
+  if (f->flags & kLinGated) {
     const double co = f->cs[out];
+    const int count = f->count;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const double dif = REV ? f->cs[src + r] - co : co - f->cs[src + r];
-      const bool in = REV ? src + r >= out : src + r <= out;
+      const bool in = src + r < count && (REV ? src + r >= out : src + r <= out);
       t[r] = in ? x[r] * scale * exp2_wide(in ? dif : 0.0) : 0.f;
     }
   } else {
-    const f32x4 w = *(const f32x4*)(f->tj + src);
-    const float to = f->ti[out];
+    const f32x4 w = *(const f32x4*)(f->dn + src);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const bool in = REV ? src + r >= out : src + r <= out;
-      t[r] = in ? x[r] * (to * w[r]) : 0.f;
-    }
+    for (int r = 0; r < 4; ++r) t[r] = (REV ? src + r >= out : src + r <= out) ? x[r] * w[r] : 0.f;
   }
   return t;
 }
 
 // Four sources of a triangle's tile into its operand tiles: element 4 (jt & 1) + r of lane.
 __device__ __forceinline__ void lin_put(uint16_t* frags, int frags_each, int fi, int jt, int lane, const f32x4& t) {
-  float r[4] = {t[0], t[1], t[2], t[3]};
+  unsigned r[4] = {__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3])};
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     u32x2 w;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w[i] = pack_bf16x2(r[2 * i], r[2 * i + 1]);
-      r[2 * i] -= bf16lo(w[i]);
-      r[2 * i + 1] -= bf16hi(w[i]);
-    }
+    for (int i = 0; i < 2; ++i) w[i] = __builtin_amdgcn_perm(r[2 * i + 1], r[2 * i], 0x07060302u);
     *(u32x2*)(frags + (p * frags_each + fi) * kFragElems + lane * 8 + 4 * (jt & 1)) = w;
+    if (p < 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = __float_as_uint(__uint_as_float(r[i]) - __uint_as_float(r[i] & 0xffff0000u));
   }
 }
 
 template <int D, bool F32>
 struct LinState {
   using C = LinCfg<D, F32>;
-  f32x4 m[C::MT][C::CT];
+  f32x4 m[C::MT];  // rows dim_row(mt, 4 g + r), column 16 w + c
 
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct) m[mt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int mt = 0; mt < C::MT; ++mt) m[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   // S [d (columns of the state)][d (rows)] in memory; TR: the other way round.
   template <bool TR>
   __device__ __forceinline__ void load(const float* s, int w, int g, int c) {
+    const int col = 16 * w + c;
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt)
+    for (int mt = 0; mt < C::MT; ++mt) {
+      const int row = dim_row(mt, 4 * g);
+      if constexpr (TR) {
 #pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct) {
-        const int col = dim_row(C::CT * w + ct, c), row = dim_row(mt, 4 * g);
-        if constexpr (TR) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) m[mt][ct][r] = s[(row + r) * D + col];
-        } else {
-          m[mt][ct] = *(const f32x4*)(s + col * D + row);
-        }
+        for (int r = 0; r < 4; ++r) m[mt][r] = s[(row + r) * D + col];
+      } else {
+        m[mt] = *(const f32x4*)(s + col * D + row);
       }
+    }
   }
   __device__ __forceinline__ void store(float* s, int w, int g, int c) const {
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct)
-        *(f32x4*)(s + dim_row(C::CT * w + ct, c) * D + dim_row(mt, 4 * g)) = m[mt][ct];
+    for (int mt = 0; mt < C::MT; ++mt) *(f32x4*)(s + (16 * w + c) * D + dim_row(mt, 4 * g)) = m[mt];
   }
   __device__ __forceinline__ void scale(float x) {
 #pragma unroll
     for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[mt][ct][r] *= x;
+      for (int r = 0; r < 4; ++r) m[mt][r] *= x;
   }
 };
-
-// Output columns of a wave: rows 4 g + r of tile ct are CT * 4 consecutive dims from here.
-template <int D>
-__device__ __forceinline__ constexpr int lin_col0(int w, int g) {
-  return D == 128 ? 32 * w + 8 * g : dim_row(w, 4 * g);
-}
 
 template <int D, bool F32>
 struct LinOut {
   using C = LinCfg<D, F32>;
-  f32x4 o[C::IT][C::CT];
+  f32x4 o[C::IT];  // dims 16 w + 4 g + r of token 16 it + c
 
-  // f o (A state), transposed: columns are tokens
-  __device__ __forceinline__ void read(const LinState<D, F32>& st, const uint16_t* a, const LinFactors* f, int g, int c) {
+  // A M^
+  __device__ __forceinline__ void read(const LinState<D, F32>& st, const uint16_t* a, int g, int c) {
 #pragma unroll
-    for (int it = 0; it < C::IT; ++it)
-#pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct) o[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int it = 0; it < C::IT; ++it) o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < C::KS; ++s) {
-      Parts<3> mp[C::CT];
+      const Parts<3> mp = cut_tiles(st.m[2 * s], st.m[2 * s + 1]);
 #pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct) mp[ct] = split_tiles<3>(st.m[2 * s][ct], st.m[2 * s + 1][ct]);
-#pragma unroll
-      for (int it = 0; it < C::IT; ++it) {
-        const auto aa = lin_row<D, F32>(a, 16 * it + c, 32 * s + 8 * g);
-#pragma unroll
-        for (int ct = 0; ct < C::CT; ++ct) mma<2>(o[it][ct], mp[ct], aa);
-      }
+      for (int it = 0; it < C::IT; ++it) mma<2>(o[it], mp, lin_row<D, F32>(a, 16 * it + c, 4 * s + g));
     }
+  }
+  __device__ __forceinline__ void scale(const LinFactors* f, int c) {
 #pragma unroll
     for (int it = 0; it < C::IT; ++it) {
-      const float x = f->f[16 * it + c];
+      const float x = f->up[16 * it + c];
 #pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[it][ct][r] *= x;
+      for (int r = 0; r < 4; ++r) o[it][r] *= x;
     }
   }
   // rows of the chunk's tokens, T elements (or fp32) of stride ld
   template <typename T>
-  __device__ __forceinline__ void store(T* base, int64_t ld, int count, int w, int g, int c) const {
+  __device__ __forceinline__ void store(T* base, unsigned ld, int count, int w, int g, int c) const {
 #pragma unroll
     for (int it = 0; it < C::IT; ++it) {
-      const int tok = 16 * it + c;
-      if (tok >= count) continue;
-      T* const p = base + (int64_t)tok * ld + lin_col0<D>(w, g);
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int ct = 0; ct < C::CT; ++ct) *(f32x4*)((float*)p + 4 * ct) = o[it][ct];
-      } else {
-        unsigned x[2 * C::CT];
-#pragma unroll
-        for (int ct = 0; ct < C::CT; ++ct)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) x[2 * ct + i] = pack_bf16x2(o[it][ct][2 * i], o[it][ct][2 * i + 1]);
-        if constexpr (C::CT == 2) *(u32x4*)p = u32x4{x[0], x[1], x[2], x[3]};
-        else *(u32x2*)p = u32x2{x[0], x[1]};
-      }
+      if (count < C::CH && 16 * it + c >= count) continue;
+      T* const p = (T*)((char*)base + ((16 * it + c) * ld + 16 * w + 4 * g) * (unsigned)sizeof(T));
+      if constexpr (sizeof(T) == 4) *(f32x4*)p = o[it];
+      else *(u32x2*)p = u32x2{pack_bf16x2(o[it][0], o[it][1]), pack_bf16x2(o[it][2], o[it][3])};
     }
   }
 };
 
-// out += T C and state <- state + B^T (w o C) (the state has its factor already).
+// out += T C and M^ <- M^ + B^T (dn o C).
 template <int D, bool F32, bool REV, bool OUT>
 __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>& st, const uint16_t* frags,
                                            const uint16_t* b, const uint16_t* cc, const LinFactors* f, int w, int lane,
@@ -429,51 +524,43 @@ __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>
   using C = LinCfg<D, F32>;
 #pragma unroll
   for (int ts = 0; ts < C::TS; ++ts) {
-    Parts<3> cw[C::CT];
+    const auto cf = lin_columns<D, F32>(cc, w, ts, g, c);
+    if constexpr (OUT) {
 #pragma unroll
-    for (int ct = 0; ct < C::CT; ++ct) {
-      const auto cf = lin_col<D, F32>(cc, C::CT * w + ct, ts, g, c);
-      if constexpr (OUT) {
+      for (int it = 0; it < C::IT; ++it) {
+        if (!lin_in<D, F32, REV>(it, ts)) continue;
+        Parts<3> t;
 #pragma unroll
-        for (int it = 0; it < C::IT; ++it) {
-          if (!lin_in<D, F32, REV>(it, ts)) continue;
-          Parts<3> t;
-#pragma unroll
-          for (int p = 0; p < 3; ++p)
-            t.p[p] = *(const bf16x8*)(frags + (p * C::FRAGS + lin_frag<D, F32, REV>(it, ts)) * kFragElems + lane * 8);
-          mma<2>(out->o[it][ct], cf, t);
-        }
+        for (int p = 0; p < 3; ++p)
+          t.p[p] = *(const bf16x8*)(frags + (p * C::FRAGS + lin_frag<D, F32, REV>(it, ts)) * kFragElems + lane * 8);
+        mma<2>(out->o[it], cf, t);
       }
-      float x[8];
+    }
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 p0 = __builtin_bit_cast(u32x4, cf.p[0]);
+      x[2 * i] = bf16lo(p0[i]);
+      x[2 * i + 1] = bf16hi(p0[i]);
+    }
+    if constexpr (F32) {
+      // the smaller parts first: their sum is exact, and so is the whole
+      const u32x4 p1 = __builtin_bit_cast(u32x4, cf.p[1]), p2 = __builtin_bit_cast(u32x4, cf.p[2]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const u32x4 p0 = __builtin_bit_cast(u32x4, cf.p[0]);
-        x[2 * i] = bf16lo(p0[i]);
-        x[2 * i + 1] = bf16hi(p0[i]);
+        x[2 * i] += bf16lo(p1[i]) + bf16lo(p2[i]);
+        x[2 * i + 1] += bf16hi(p1[i]) + bf16hi(p2[i]);
       }
-      if constexpr (F32) {
-        // the smaller parts first: their sum is exact, and so is the whole
-        const u32x4 p1 = __builtin_bit_cast(u32x4, cf.p[1]), p2 = __builtin_bit_cast(u32x4, cf.p[2]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[2 * i] += bf16lo(p1[i]) + bf16lo(p2[i]);
-          x[2 * i + 1] += bf16hi(p1[i]) + bf16hi(p2[i]);
-        }
-      }
-      const f32x4 w0 = *(const f32x4*)(f->w + 32 * ts + dtau(g, 0)), w1 = *(const f32x4*)(f->w + 32 * ts + dtau(g, 4));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] *= w0[e];
-        x[4 + e] *= w1[e];
-      }
-      cw[ct] = split8<3>(x);
     }
+    const f32x4 w0 = *(const f32x4*)(f->dn + 32 * ts + dtau(g, 0)), w1 = *(const f32x4*)(f->dn + 32 * ts + dtau(g, 4));
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt) {
-      const auto bf = lin_col<D, F32>(b, mt, ts, g, c);
-#pragma unroll
-      for (int ct = 0; ct < C::CT; ++ct) mma<2>(st.m[mt][ct], bf, cw[ct]);
+    for (int e = 0; e < 4; ++e) {
+      x[e] *= w0[e];
+      x[4 + e] *= w1[e];
     }
+    const Parts<3> cw = cut8(x);
+#pragma unroll
+    for (int mt = 0; mt < C::MT; ++mt) mma<2>(st.m[mt], lin_row_dims<D, F32>(b, mt, ts, g, c), cw);
   }
 }
 

@@ -100,56 +100,67 @@ __device__ __forceinline__ void segment_state(const LinArgs& a, const LinSeg& sg
                                               LinFactors* fac) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int hk = h / (a.heads / a.heads_k);
   const LinTokens bt = REV ? a.q : a.k, ct = REV ? a.d_o : a.v;
   const T* const bp = (const T*)bt.p + (int64_t)sg.tok * bt.ld + hk * D;
   const T* const cp = (const T*)ct.p + (int64_t)sg.tok * ct.ld + h * D;
   const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
-  uint16_t* const b = lds;
-  uint16_t* const cc = lds + C::TILE;
   const int n = (sg.count + C::CH - 1) / C::CH;
   LinState<D, F32> st;
   st.zero();
-  double sum = 0.0;
-  LinFetch<D, F32, 256> fb, fc;
-  float gl = 0.f;
-  auto fetch = [&](int j) {
-    const int ci = REV ? n - 1 - j : j, t0 = ci * C::CH;
-    const int count = sg.count - t0 < C::CH ? sg.count - t0 : C::CH;
-    fb.load(bp + (int64_t)t0 * bt.ld, bt.ld, count);
-    fc.load(cp + (int64_t)t0 * ct.ld, ct.ld, count);
-    gl = gp && lane < count ? gp[(int64_t)(t0 + lane) * a.ld_g] : 0.f;
-    return count;
+  LinFetch<D, F32> fb, fc;
+  // chunk j of the pass: its first token, tokens and decays
+  auto first = [&](int j) { return (REV ? n - 1 - j : j) * C::CH; };
+  auto tokens = [&](int j) { return sg.count - first(j) < C::CH ? sg.count - first(j) : C::CH; };
+  auto decay = [&](int j) {
+    return gp && lane < tokens(j) ? gp[(int64_t)(first(j) + lane) * a.ld_g] : 0.f;
   };
-  int count = fetch(0);
+  auto fetch = [&](int j) {
+    fb.load(bp + (int64_t)first(j) * bt.ld, (unsigned)bt.ld, tokens(j));
+    fc.load(cp + (int64_t)first(j) * ct.ld, (unsigned)ct.ld, tokens(j));
+  };
+  const bool mine = w == C::WAVES - 1;  // the factors are this wave's, a chunk ahead
+  const float scale = REV ? a.scale : 1.f;
+  float gl = 0.f;
+  fetch(0);
+  if (mine) {
+    lin_factors<REV>(fac, nullptr, decay(0), tokens(0), scale);
+    if (n > 1) gl = decay(1);
+  }
   for (int j = 0; j < n; ++j) {
-    if (w == 3) lin_factors<REV>(fac, gl, REV ? a.scale : 1.f);
-    fb.store(b, count);
-    fc.store(cc, count);
+    fb.store(lds);
+    fc.store(lds + C::TILE);
     __syncthreads();
-    if (j + 1 < n) count = fetch(j + 1);
-    st.scale(fac->last);
-    sum += fac->cs[63];
-    lin_tokens<D, F32, REV, false>(nullptr, st, nullptr, b, cc, fac, w, lane, g, c);
+    const LinFactors* const f = fac + (j & 1);
+    if (j + 1 < n) fetch(j + 1);
+    if (mine && j + 1 < n) {
+      lin_factors<REV>(fac + (~j & 1), f, gl, tokens(j + 1), scale);
+      if (j + 2 < n) gl = decay(j + 2);
+    }
+    if (f->flags & kLinScale) st.scale(f->pre);
+    if (f->flags & kLinGated) st.scale(f->last);
+    lin_tokens<D, F32, REV, false>(nullptr, st, nullptr, lds, lds + C::TILE, f, w, lane, g, c);
     __syncthreads();
   }
+  st.scale(fac[(n - 1) & 1].end);
   st.store(a.part[REV] + ((int64_t)(sg.slot + (REV ? -1 : 1)) * a.heads + h) * D * D, w, g, c);
-  if (threadIdx.x == 0) a.decay[REV][(int64_t)sg.slot * a.heads + h] = exp2_wide(sum);
+  if (mine && lane == 0) a.decay[REV][(int64_t)sg.slot * a.heads + h] = exp2_wide(fac[(n - 1) & 1].sum);
 }
 
 template <int D, bool F32>
-__global__ __launch_bounds__(256, 2) void k_linear_states(LinArgs a) {
+__global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
   using C = LinCfg<D, F32>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * C::TILE];
-  __shared__ LinFactors fac;
+  __shared__ LinFactors fac[2];
   const int h = blockIdx.x % a.heads;
   const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
   if (sg.count <= 0) return;
   if (blockIdx.y == 0) {
-    if (!(sg.flags & 2)) segment_state<D, F32, false>(a, sg, h, lds, &fac);
+    if (!(sg.flags & 2)) segment_state<D, F32, false>(a, sg, h, lds, fac);
   } else {
-    if (!(sg.flags & 1)) segment_state<D, F32, true>(a, sg, h, lds, &fac);
+    if (!(sg.flags & 1)) segment_state<D, F32, true>(a, sg, h, lds, fac);
   }
 }
 
@@ -201,15 +212,17 @@ __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways
 
 // ---- outputs -----------------------------------------------------------------------
 template <int D, bool F32>
-__global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void k_linear_out(LinArgs a) {
+__global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_out(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
   __shared__ __attribute__((aligned(16))) uint16_t lds[3 * C::TILE + C::TRI];
-  __shared__ LinFactors fac;
+  __shared__ LinFactors fac[2];
+  __shared__ float next_decays[64];
   const int h = blockIdx.x % a.heads;
   const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
   if (sg.count < 0) return;
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int hk = h / (a.heads / a.heads_k);
   uint16_t* const q = lds;
   uint16_t* const k = q + C::TILE;
@@ -227,47 +240,83 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void k_linear_out(Lin
     const T* const vp = (const T*)a.v.p + (int64_t)sg.tok * a.v.ld + h * D;
     T* const op = (T*)a.o + (int64_t)sg.tok * a.ld_o + h * D;
     const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
-    LinFetch<D, F32, 256> fq, fk, fv;
-    float gl = 0.f;
-    auto fetch = [&](int j) {
-      const int t0 = j * C::CH, count = sg.count - t0 < C::CH ? sg.count - t0 : C::CH;
-      fq.load(qp + (int64_t)t0 * a.q.ld, a.q.ld, count);
-      fk.load(kp + (int64_t)t0 * a.k.ld, a.k.ld, count);
-      fv.load(vp + (int64_t)t0 * a.v.ld, a.v.ld, count);
-      gl = gp && lane < count ? gp[(int64_t)(t0 + lane) * a.ld_g] : 0.f;
-      return count;
+    LinFetch<D, F32> fq, fk, fv;
+    auto tokens = [&](int j) { return sg.count - j * C::CH < C::CH ? sg.count - j * C::CH : C::CH; };
+    auto decay = [&](int j) {
+      return gp && lane < tokens(j) ? gp[(int64_t)(j * C::CH + lane) * a.ld_g] : 0.f;
     };
-    int next = fetch(0);
-    for (int j = 0; j < n; ++j) {
-      const int count = next;
-      if (w == 3) lin_factors<false>(&fac, gl, a.scale);
-      fq.store(q, count);
-      fk.store(k, count);
-      fv.store(v, count);
-      __syncthreads();
-      if (j + 1 < n) next = fetch(j + 1);
-      for (int t = w; t < 2 * C::FRAGS; t += kLinWaves) {
-        const int f = t >> 1;
-        const int it = C::CH == 32 || f < 2 ? f : 2 + (f - 2) / 2, ts = C::CH == 32 || f < 2 ? 0 : (f - 2) & 1;
-        const int jt = 2 * ts + (t & 1);
-        const f32x4 x = lin_gate<false>(lin_tri<D, F32>(q, k, it, jt, g, c), &fac, a.scale, it, jt, g, c);
-        lin_put(tri, C::FRAGS, f, jt, lane, x);
+    // bf16: straight into the tiles when all waves are done with a chunk; the other workgroup of
+    // the compute unit works meanwhile
+    auto fetch = [&](int j) {
+      const int64_t t0 = (int64_t)j * C::CH;
+      const LinLane l(lane);
+      if constexpr (F32) {
+        fq.load(qp + t0 * a.q.ld, (unsigned)a.q.ld, tokens(j));
+        fk.load(kp + t0 * a.k.ld, (unsigned)a.k.ld, tokens(j));
+        fv.load(vp + t0 * a.v.ld, (unsigned)a.v.ld, tokens(j));
+      } else {
+        lin_load<D>(q, qp + t0 * a.q.ld, (unsigned)a.q.ld, tokens(j), w, l.lane);
+        lin_load<D>(k, kp + t0 * a.k.ld, (unsigned)a.k.ld, tokens(j), w, l.lane);
+        lin_load<D>(v, vp + t0 * a.v.ld, (unsigned)a.v.ld, tokens(j), w, l.lane);
       }
-      LinOut<D, F32> out;
-      out.read(st, q, &fac, g, c);
-      st.scale(fac.last);
-      __syncthreads();
-      lin_tokens<D, F32, false, true>(&out, st, tri, k, v, &fac, w, lane, g, c);
-      out.store(op + (int64_t)j * C::CH * a.ld_o, a.ld_o, count, w, g, c);
-      __syncthreads();
+    };
+    const bool mine = w == C::WAVES - 1;  // the factors are this wave's, a chunk ahead
+    float gl = 0.f;
+    fetch(0);
+    if (mine) {
+      lin_factors<false>(fac, nullptr, decay(0), tokens(0), a.scale);
+      if (n > 1) gl = decay(1);
     }
+    for (int j = 0; j < n; ++j) {
+      if (mine) next_decays[lane] = gl;
+      if constexpr (F32) {
+        fq.store(q);
+        fk.store(k);
+        fv.store(v);
+      } else {
+        lin_wait_loads();
+      }
+      __syncthreads();
+      const LinFactors* const f = fac + (j & 1);
+      const int flags = f->flags;
+      if (mine && j + 1 < n) {
+        lin_factors<false>(fac + (~j & 1), f, next_decays[lane], tokens(j + 1), a.scale);
+      }
+      if (F32 && j + 1 < n) fetch(j + 1);
+      for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
+        const LinLane l(lane);
+        const int fr = t >> 1;
+        const int it = C::CH == 32 || fr < 2 ? fr : 2 + (fr - 2) / 2, ts = C::CH == 32 || fr < 2 ? 0 : (fr - 2) & 1;
+        const int jt = 2 * ts + (t & 1);
+        const f32x4 x = lin_gate<false>(lin_tri<D, F32>(q, k, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
+        lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
+      }
+      if (flags & kLinScale) st.scale(f->pre);
+      LinOut<D, F32> out;
+      const LinLane lr(lane);
+      out.read(st, q, lr.g, lr.c);
+      if (flags & kLinGated) {
+        out.scale(f, c);
+        st.scale(f->last);
+      }
+      __syncthreads();
+      const LinLane lt(lane);
+      lin_tokens<D, F32, false, true>(&out, st, tri, k, v, f, w, lt.lane, lt.g, lt.c);
+      const LinLane lo(lane);
+      if (!(flags & kLinGated)) out.scale(f, lo.c);
+      out.store(op + (int64_t)j * C::CH * a.ld_o, (unsigned)a.ld_o, tokens(j), w, lo.g, lo.c);
+      __syncthreads();
+      if (!F32 && j + 1 < n) fetch(j + 1);
+      gl = mine && j + 2 < n ? decay(j + 2) : 0.f;
+    }
+    st.scale(fac[(n - 1) & 1].end);
   }
   if ((sg.flags & 2) && a.state_out) st.store(a.state_out + own, w, g, c);
 }
 
 template <int D>
 hipError_t states_any(const LinArgs& a, bool f32, bool both, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads), both ? 2 : 1), blk(256);
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads), both ? 2 : 1), blk(4 * D);
   if (f32) hipLaunchKernelGGL((k_linear_states<D, true>), grid, blk, 0, st, a);
   else hipLaunchKernelGGL((k_linear_states<D, false>), grid, blk, 0, st, a);
   return hipGetLastError();
@@ -275,7 +324,7 @@ hipError_t states_any(const LinArgs& a, bool f32, bool both, hipStream_t st) {
 
 template <int D>
 hipError_t out_any(const LinArgs& a, bool f32, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(256);
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(4 * D);
   if (f32) hipLaunchKernelGGL((k_linear_out<D, true>), grid, blk, 0, st, a);
   else hipLaunchKernelGGL((k_linear_out<D, false>), grid, blk, 0, st, a);
   return hipGetLastError();

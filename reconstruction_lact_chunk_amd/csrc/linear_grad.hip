@@ -22,46 +22,31 @@ __device__ __forceinline__ float prefix16(float x, int c) {
   return x;
 }
 
-// An output element with its factor times the same element of a token tensor's row in
-// memory or LDS, summed over the wave's columns.
-template <int D, bool F32>
-__device__ __forceinline__ float dot_row(const f32x4* o, const typename Tok<F32>::T* row) {
-  constexpr int CT = LinCfg<D, F32>::CT;
-  float s = 0.f;
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    float x[4];
-    if constexpr (F32) {
-      const f32x4 v = *(const f32x4*)(row + 4 * ct);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = v[r];
-    } else {
-      const u32x2 v = *(const u32x2*)(row + 4 * ct);
-      x[0] = bf16lo(v[0]);
-      x[1] = bf16hi(v[0]);
-      x[2] = bf16lo(v[1]);
-      x[3] = bf16hi(v[1]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) s = fmaf(o[ct][r], x[r], s);
-  }
-  return s;
+// A lane's four outputs of a token times the same elements of a token tensor's row.
+__device__ __forceinline__ float dot4(const f32x4& o, const float* p) {
+  const f32x4 v = *(const f32x4*)p;
+  return o[0] * v[0] + o[1] * v[1] + o[2] * v[2] + o[3] * v[3];
+}
+__device__ __forceinline__ float dot4(const f32x4& o, const uint16_t* p) {
+  const u32x2 v = *(const u32x2*)p;
+  return o[0] * bf16lo(v[0]) + o[1] * bf16hi(v[0]) + o[2] * bf16lo(v[1]) + o[3] * bf16hi(v[1]);
 }
 
 // ---- dk, dv --------------------------------------------------------------------
-// One workgroup to a (segment, head), four waves each for dv (state D) and dk (D^T).
+// One workgroup to a (segment, head), D / 16 waves each for dv (state D) and dk (D^T).
 // The dk waves leave D^T at the chunk's end for the other pass.
 template <int D, bool F32>
-__global__ __launch_bounds__(512) void k_linear_dkdv(LinArgs a) {
+__global__ __launch_bounds__(8 * D) void k_linear_dkdv(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
   __shared__ __attribute__((aligned(16))) uint16_t lds[4 * C::TILE + 2 * C::TRI];
-  __shared__ LinFactors fac;
-  __shared__ float crossing[kLinWaves][64], going[kLinWaves][64];
+  __shared__ LinFactors fac[2];
+  __shared__ float next_decays[64];
+  __shared__ float crossing[4][64], going[C::WAVES][64];
   const int h = blockIdx.x % a.heads;
   const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
   if (sg.count < 0) return;
-  const int wave = threadIdx.x >> 6, side = wave >> 2, w = wave & 3;  // side 1: dk
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), side = wave / C::WAVES, w = wave % C::WAVES;  // side 1: dk
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int hk = h / (a.heads / a.heads_k);
   uint16_t* const q = lds;
@@ -90,89 +75,113 @@ __global__ __launch_bounds__(512) void k_linear_dkdv(LinArgs a) {
     const LinTokens t0 = side ? a.v : a.q, t1 = side ? a.d_o : a.k;
     const T* const p0 = side ? vp : qp;
     const T* const p1 = side ? dp : kp;
-    LinFetch<D, F32, 256> f0, f1;
-    float gl = 0.f;
-    auto fetch = [&](int j) {
-      const int at = j * C::CH, count = sg.count - at < C::CH ? sg.count - at : C::CH;
-      f0.load(p0 + (int64_t)at * t0.ld, t0.ld, count);
-      f1.load(p1 + (int64_t)at * t1.ld, t1.ld, count);
-      gl = gp && lane < count ? gp[(int64_t)(at + lane) * a.ld_g] : 0.f;
-      return count;
+    LinFetch<D, F32> f0, f1;
+    auto tokens = [&](int j) { return sg.count - j * C::CH < C::CH ? sg.count - j * C::CH : C::CH; };
+    auto decay = [&](int j) {
+      return gp && lane < tokens(j) ? gp[(int64_t)(j * C::CH + lane) * a.ld_g] : 0.f;
     };
-    int next = fetch(n - 1);
+    auto fetch = [&](int j) {
+      const int64_t at = (int64_t)j * C::CH;
+      f0.load(p0 + at * t0.ld, (unsigned)t0.ld, tokens(j));
+      f1.load(p1 + at * t1.ld, (unsigned)t1.ld, tokens(j));
+    };
+    const bool mine = wave == 2 * C::WAVES - 1;  // the factors are this wave's, a chunk ahead
+    float gl = 0.f;
+    fetch(n - 1);
+    if (mine) {
+      lin_factors<true>(fac + ((n - 1) & 1), nullptr, decay(n - 1), tokens(n - 1), a.scale);
+      if (n > 1) gl = decay(n - 2);
+    }
     for (int j = n - 1; j >= 0; --j) {
-      const int count = next;
+      const int count = tokens(j);
       const int64_t tok0 = (int64_t)sg.tok + (int64_t)j * C::CH;
-      if (wave == 3) lin_factors<true>(&fac, gl, a.scale);
-      f0.store(side ? v : q, count);
-      f1.store(side ? od : k, count);
+      if (mine) next_decays[lane] = gl;
+      f0.store(side ? v : q);
+      f1.store(side ? od : k);
       __syncthreads();
-      if (j > 0) next = fetch(j - 1);
-      // wave w the source tokens of row tile w
+      const LinFactors* const f = fac + (j & 1);
+      const int flags = f->flags;
+      if (mine && j > 0) lin_factors<true>(fac + (~j & 1), f, next_decays[lane], tokens(j - 1), a.scale);
+      if (j > 0) fetch(j - 1);
+      // wave w < 2 TS the source tokens of row tile w
       float cross[C::IT] = {};
-      for (int jt = w; jt < 2 * C::TS; jt += kLinWaves) {
-        const int ts = jt >> 1;
+      if (w < 2 * C::TS) {
+        const int jt = w, ts = jt >> 1;
+        const LinLane l(lane);
+        const int g = l.g, c = l.c;
         float before[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int it = 0; it < C::IT; ++it) {
           if (!lin_in<D, F32, true>(it, ts)) continue;
-          const f32x4 x = lin_gate<true>(lin_tri<D, F32>(ta, tb, it, jt, g, c), &fac, a.scale, it, jt, g, c);
-          lin_put(tri, C::FRAGS, lin_frag<D, F32, true>(it, ts), jt, lane, x);
+          const f32x4 x = lin_gate<true>(lin_tri<D, F32>(ta, tb, it, jt, g, c), f, a.scale, it, jt, g, c);
+          lin_put(tri, C::FRAGS, lin_frag<D, F32, true>(it, ts), jt, l.lane, x);
           if (side && a.flow) {
             // of source i's row of X, what comes from tokens before t = 16 it + c, if t <= i
             const f32x4 y = lin_tri<D, F32>(k, q, it, jt, g, c);
+            const float up = flags & kLinGated ? 1.f : f->up[16 * it + c];
             float sum = 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float p = prefix16(x[r] * y[r], c);
-              const float up = __shfl_up(p, 1, 16);
-              const float pre = before[r] + (c ? up : 0.f);
-              if (token_row(jt, 4 * g) + r >= 16 * it + c) sum += pre;
+              const float p = prefix16(x[r] * y[r] * up, c);
+              const float left = __shfl_up(p, 1, 16);
+              if (token_row(jt, 4 * g) + r >= 16 * it + c) sum += before[r] + (c ? left : 0.f);
               before[r] += __shfl(p, 15, 16);
             }
             cross[it] += group_sum(sum);
           }
         }
       }
+      if (flags & kLinScale) st.scale(f->pre);
       LinOut<D, F32> out;
-      out.read(st, ta, &fac, g, c);
+      {
+        const LinLane l(lane);
+        out.read(st, ta, l.g, l.c);
+      }
       if (a.flow) {
+        const LinLane l(lane);
+        const int g = l.g, c = l.c;
         if (side) {
-          float* const dump = a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * C::CT * 256) + 4 * lane;
+          if (w == 0 && lane == 0) a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] = f->s;
+          float* const dump = a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
 #pragma unroll
-          for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-            for (int ct = 0; ct < C::CT; ++ct) *(f32x4*)(dump + (mt * C::CT + ct) * 256) = st.m[mt][ct];
-          if (g == 0)
+          for (int mt = 0; mt < C::MT; ++mt) *(f32x4*)(dump + mt * 256) = st.m[mt];
+          if (w < 4 && g == 0)
 #pragma unroll
             for (int it = 0; it < C::IT; ++it) crossing[w][16 * it + c] = cross[it];
         } else {
 #pragma unroll
           for (int it = 0; it < C::IT; ++it) {
             const int row = 16 * it + c < count ? 16 * it + c : count - 1;
-            const float s = group_sum(dot_row<D, F32>(out.o[it], vp + ((int64_t)j * C::CH + row) * a.v.ld + lin_col0<D>(w, g)));
-            if (g == 0) going[w][16 * it + c] = 16 * it + c < count ? s : 0.f;
+            const float x = group_sum(dot4(out.o[it], vp + ((int64_t)j * C::CH + row) * a.v.ld + 16 * w + 4 * g));
+            if (g == 0) going[w][16 * it + c] = 16 * it + c < count ? x * f->up[16 * it + c] : 0.f;
           }
         }
       }
-      st.scale(fac.last);
+      if (flags & kLinGated) {
+        out.scale(f, c);
+        st.scale(f->last);
+      }
       __syncthreads();
-      lin_tokens<D, F32, true, true>(&out, st, tri, tb, tc, &fac, w, lane, g, c);
+      const LinLane lt(lane);
+      lin_tokens<D, F32, true, true>(&out, st, tri, tb, tc, f, w, lt.lane, lt.g, lt.c);
+      const LinLane l(lane);
+      const int g = l.g, c = l.c;
+      if (!(flags & kLinGated)) out.scale(f, c);
       if (!side) {
-        out.store((T*)a.dv + tok0 * a.ld_dv + h * D, a.ld_dv, count, w, g, c);
+        out.store((T*)a.dv + tok0 * a.ld_dv + h * D, (unsigned)a.ld_dv, count, w, g, c);
       } else if (a.dk_part) {
-        out.store(a.dk_part + (tok0 * a.heads + h) * D, (int64_t)a.heads * D, count, w, g, c);
+        out.store(a.dk_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, g, c);
       } else {
-        out.store((T*)a.dk + tok0 * a.ld_dk + hk * D, a.ld_dk, count, w, g, c);
+        out.store((T*)a.dk + tok0 * a.ld_dk + hk * D, (unsigned)a.ld_dk, count, w, g, c);
       }
       if (a.flow && wave == 0) {
         float x = 0.f, y = 0.f;
-        if (lane < C::CH)
+        if (lane < C::CH) {
 #pragma unroll
-          for (int i = 0; i < kLinWaves; ++i) {
-            x += crossing[i][lane];
-            y += going[i][lane];
-          }
+          for (int i = 0; i < 4; ++i) x += crossing[i][lane];
+#pragma unroll
+          for (int i = 0; i < C::WAVES; ++i) y += going[i][lane];
+        }
         float all = y;
 #pragma unroll
         for (int m = 1; m < 64; m *= 2) {
@@ -182,24 +191,28 @@ __global__ __launch_bounds__(512) void k_linear_dkdv(LinArgs a) {
         const float up = __shfl_up(all, 1, 64);
         if (lane < count) a.flow[(tok0 + lane) * a.heads + h] = x + (lane ? up : 0.f);
       }
+      gl = mine && j > 1 ? decay(j - 2) : 0.f;
       __syncthreads();
     }
+    st.scale(fac[0].end);
   }
   if ((sg.flags & 1) && a.dstate_in && !side) st.store(a.dstate_in + own, w, g, c);
 }
 
 // ---- dq, dg ----------------------------------------------------------------------
 template <int D, bool F32>
-__global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void k_linear_dq(LinArgs a) {
+__global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
   __shared__ __attribute__((aligned(16))) uint16_t lds[3 * C::TILE + C::TRI];
-  __shared__ LinFactors fac;
-  __shared__ float coming[kLinWaves][64], through[kLinWaves];
+  __shared__ LinFactors fac[2];
+  __shared__ float next_decays[64];
+  __shared__ float coming[C::WAVES][64], through[C::WAVES];
   const int h = blockIdx.x % a.heads;
   const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
   if (sg.count <= 0) return;
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int hk = h / (a.heads / a.heads_k);
   uint16_t* const od = lds;
   uint16_t* const v = od + C::TILE;
@@ -216,65 +229,99 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void k_linear_dq(LinA
   const T* const vp = (const T*)a.v.p + (int64_t)sg.tok * a.v.ld + h * D;
   const T* const dp = (const T*)a.d_o.p + (int64_t)sg.tok * a.d_o.ld + h * D;
   const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
-  LinFetch<D, F32, 256> fd, fv, fk;
-  float gl = 0.f;
-  auto fetch = [&](int j) {
-    const int t0 = j * C::CH, count = sg.count - t0 < C::CH ? sg.count - t0 : C::CH;
-    fd.load(dp + (int64_t)t0 * a.d_o.ld, a.d_o.ld, count);
-    fv.load(vp + (int64_t)t0 * a.v.ld, a.v.ld, count);
-    fk.load(kp + (int64_t)t0 * a.k.ld, a.k.ld, count);
-    gl = gp && lane < count ? gp[(int64_t)(t0 + lane) * a.ld_g] : 0.f;
-    return count;
+  LinFetch<D, F32> fd, fv, fk;
+  auto tokens = [&](int j) { return sg.count - j * C::CH < C::CH ? sg.count - j * C::CH : C::CH; };
+  auto decay = [&](int j) {
+    return gp && lane < tokens(j) ? gp[(int64_t)(j * C::CH + lane) * a.ld_g] : 0.f;
   };
-  int next = fetch(0);
-  for (int j = 0; j < n; ++j) {
-    const int count = next;
-    const int64_t tok0 = (int64_t)sg.tok + (int64_t)j * C::CH;
-    if (w == 3) lin_factors<false>(&fac, gl, a.scale);
-    fd.store(od, count);
-    fv.store(v, count);
-    fk.store(k, count);
-    __syncthreads();
-    if (j + 1 < n) next = fetch(j + 1);
-    for (int t = w; t < 2 * C::FRAGS; t += kLinWaves) {
-      const int f = t >> 1;
-      const int it = C::CH == 32 || f < 2 ? f : 2 + (f - 2) / 2, ts = C::CH == 32 || f < 2 ? 0 : (f - 2) & 1;
-      const int jt = 2 * ts + (t & 1);
-      const f32x4 x = lin_gate<false>(lin_tri<D, F32>(od, v, it, jt, g, c), &fac, a.scale, it, jt, g, c);
-      lin_put(tri, C::FRAGS, f, jt, lane, x);
+  auto fetch = [&](int j) {
+    const int64_t t0 = (int64_t)j * C::CH;
+    const LinLane l(lane);
+    if constexpr (F32) {
+      fd.load(dp + t0 * a.d_o.ld, (unsigned)a.d_o.ld, tokens(j));
+      fv.load(vp + t0 * a.v.ld, (unsigned)a.v.ld, tokens(j));
+      fk.load(kp + t0 * a.k.ld, (unsigned)a.k.ld, tokens(j));
+    } else {
+      lin_load<D>(od, dp + t0 * a.d_o.ld, (unsigned)a.d_o.ld, tokens(j), w, l.lane);
+      lin_load<D>(v, vp + t0 * a.v.ld, (unsigned)a.v.ld, tokens(j), w, l.lane);
+      lin_load<D>(k, kp + t0 * a.k.ld, (unsigned)a.k.ld, tokens(j), w, l.lane);
     }
+  };
+  const bool mine = w == C::WAVES - 1;  // the factors are this wave's, a chunk ahead
+  float gl = 0.f;
+  fetch(0);
+  if (mine) {
+    lin_factors<false>(fac, nullptr, decay(0), tokens(0), a.scale);
+    if (n > 1) gl = decay(1);
+  }
+  for (int j = 0; j < n; ++j) {
+    const int count = tokens(j);
+    const int64_t tok0 = (int64_t)sg.tok + (int64_t)j * C::CH;
+    if (mine) next_decays[lane] = gl;
+    if constexpr (F32) {
+      fd.store(od);
+      fv.store(v);
+      fk.store(k);
+    } else {
+      lin_wait_loads();
+    }
+    __syncthreads();
+    const LinFactors* const f = fac + (j & 1);
+    const int flags = f->flags;
+    if (mine && j + 1 < n) lin_factors<false>(fac + (~j & 1), f, next_decays[lane], tokens(j + 1), a.scale);
+    if (F32 && j + 1 < n) fetch(j + 1);
+    for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
+      const LinLane l(lane);
+      const int g = l.g, c = l.c;
+      const int fr = t >> 1;
+      const int it = C::CH == 32 || fr < 2 ? fr : 2 + (fr - 2) / 2, ts = C::CH == 32 || fr < 2 ? 0 : (fr - 2) & 1;
+      const int jt = 2 * ts + (t & 1);
+      const f32x4 x = lin_gate<false>(lin_tri<D, F32>(od, v, it, jt, g, c), f, a.scale, it, jt, g, c);
+      lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
+    }
+    if (flags & kLinScale) st.scale(f->pre);
     LinOut<D, F32> out;
-    out.read(st, od, &fac, g, c);
+    {
+      const LinLane l(lane);
+      out.read(st, od, l.g, l.c);
+    }
     if (a.flow) {
-      const float* const dump = a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * C::CT * 256) + 4 * lane;
+      const LinLane l(lane);
+      const int g = l.g, c = l.c;
+      const float* const dump = a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
       float e = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt)
+      for (int mt = 0; mt < C::MT; ++mt) {
+        const f32x4 x = *(const f32x4*)(dump + mt * 256);
 #pragma unroll
-        for (int ct = 0; ct < C::CT; ++ct) {
-          const f32x4 x = *(const f32x4*)(dump + (mt * C::CT + ct) * 256);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][ct][r], x[r], e);
-        }
+        for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][r], x[r], e);
+      }
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) e += __shfl_xor(e, m, 64);
       if (lane == 0) through[w] = e;
 #pragma unroll
       for (int it = 0; it < C::IT; ++it) {
         const int row = 16 * it + c < count ? 16 * it + c : count - 1;
-        const float s = group_sum(dot_row<D, F32>(out.o[it], qp + ((int64_t)j * C::CH + row) * a.q.ld + lin_col0<D>(w, g)));
-        if (g == 0) coming[w][16 * it + c] = 16 * it + c < count ? s : 0.f;
+        const float x = group_sum(dot4(out.o[it], qp + ((int64_t)j * C::CH + row) * a.q.ld + 16 * w + 4 * g));
+        if (g == 0) coming[w][16 * it + c] = 16 * it + c < count ? x * f->up[16 * it + c] : 0.f;
       }
     }
-    st.scale(fac.last);
+    if (flags & kLinGated) {
+      out.scale(f, c);
+      st.scale(f->last);
+    }
     __syncthreads();
-    lin_tokens<D, F32, false, true>(&out, st, tri, v, k, &fac, w, lane, g, c);
-    if (a.o_part) out.store(a.o_part + (tok0 * a.heads + h) * D, (int64_t)a.heads * D, count, w, g, c);
-    else out.store((T*)a.o + tok0 * a.ld_o + hk * D, a.ld_o, count, w, g, c);
+    const LinLane lt(lane);
+    lin_tokens<D, F32, false, true>(&out, st, tri, v, k, f, w, lt.lane, lt.g, lt.c);
+    const LinLane lo(lane);
+    const int g = lo.g, c = lo.c;
+    if (!(flags & kLinGated)) out.scale(f, c);
+    if (a.o_part) out.store(a.o_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, g, c);
+    else out.store((T*)a.o + tok0 * a.ld_o + hk * D, (unsigned)a.ld_o, count, w, g, c);
     if (a.flow && w == 0) {
       float x = 0.f, e = 0.f;
 #pragma unroll
-      for (int i = 0; i < kLinWaves; ++i) {
+      for (int i = 0; i < C::WAVES; ++i) {
         x += lane < C::CH ? coming[i][lane] : 0.f;
         e += through[i];
       }
@@ -283,7 +330,9 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void k_linear_dq(LinA
         const float o = __shfl_down(x, m, 64);
         if (lane + m < 64) x += o;
       }
-      const float d = lane < count ? a.flow[(tok0 + lane) * a.heads + h] + x + e * fac.last : 0.f;
+      // M at the chunk's start, D at its end and the decay between
+      const double power = f->s + a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] + f->cs[63];
+      const float d = lane < count ? a.flow[(tok0 + lane) * a.heads + h] + x + e * exp2_wide(power) : 0.f;
       if (a.ld_g) {
         if (lane < count) a.dg[(tok0 + lane) * a.heads + h] = d;
       } else {
@@ -294,6 +343,8 @@ __global__ __launch_bounds__(256, D == 128 && F32 ? 1 : 2) void k_linear_dq(LinA
       }
     }
     __syncthreads();
+    if (!F32 && j + 1 < n) fetch(j + 1);
+    gl = mine && j + 2 < n ? decay(j + 2) : 0.f;
   }
 }
 
@@ -343,7 +394,7 @@ __global__ __launch_bounds__(256) void k_linear_decay_sum(const float* sums, Lin
 
 template <int D>
 hipError_t dkdv_any(const LinArgs& a, bool f32, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(512);
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(8 * D);
   if (f32) hipLaunchKernelGGL((k_linear_dkdv<D, true>), grid, blk, 0, st, a);
   else hipLaunchKernelGGL((k_linear_dkdv<D, false>), grid, blk, 0, st, a);
   return hipGetLastError();
@@ -351,7 +402,7 @@ hipError_t dkdv_any(const LinArgs& a, bool f32, hipStream_t st) {
 
 template <int D>
 hipError_t dq_any(const LinArgs& a, bool f32, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(256);
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(4 * D);
   if (f32) hipLaunchKernelGGL((k_linear_dq<D, true>), grid, blk, 0, st, a);
   else hipLaunchKernelGGL((k_linear_dq<D, false>), grid, blk, 0, st, a);
   return hipGetLastError();
