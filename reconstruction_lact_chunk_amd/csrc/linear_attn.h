@@ -76,6 +76,10 @@ struct LinFactors {
   int flags;
 };
 enum { kLinGated = 1, kLinScale = 2 };
+template <bool B>
+struct LinBool {
+  static constexpr bool value = B;
+};
 constexpr double kLinSpan = 60.0;
 
 struct LinSeg {
@@ -380,6 +384,20 @@ __device__ __forceinline__ void lin_factors(LinFactors* f, const LinFactors* bef
   }
 }
 
+// What a chunk's C is multiplied with where its part of the state is taken to the end of the
+// chunks that the pass has been through, `before` them; REV: to the beginning, times scale.
+template <bool REV>
+__device__ __forceinline__ void lin_reach(LinFactors* f, const LinFactors* before, float gl, int count, float scale) {
+  const int lane = threadIdx.x & 63;
+  if (lane >= count) gl = 0.f;
+  if (gl < kMinLogDecay) gl = kMinLogDecay;
+  const double c = lin_prefix(gl * kLog2E);
+  const double last = lin_lane63(c), sum = before ? before->sum : 0.0;
+  const float w = exp2_wide(sum + (REV ? c : last - c));
+  f->dn[lane] = lane < count ? (REV ? w * scale : w) : 0.f;
+  if (lane == 0) f->sum = sum + last;
+}
+
 // Operand tile f of a triangle (row tile, token step), and back.
 template <int D, bool F32, bool REV>
 __device__ __forceinline__ constexpr int lin_frag(int it, int ts) {
@@ -404,13 +422,13 @@ __device__ __forceinline__ f32x4 lin_tri(const uint16_t* a, const uint16_t* b, i
   return acc;
 }
 
-// The same with the decays (kLinGated: all of them) and the mask.
-template <bool REV>
+// The same with the decays (GATED: all of them) and the mask.
+template <bool REV, bool GATED>
 __device__ __forceinline__ f32x4 lin_gate(const f32x4& x, const LinFactors* f, float scale, int it, int jt, int g,
                                           int c) {
   const int out = 16 * it + c, src = token_row(jt, 4 * g);
   f32x4 t;
-  if (f->flags & kLinGated) {
+  if constexpr (GATED) {
     const double co = f->cs[out];
     const int count = f->count;
 #pragma unroll
@@ -506,12 +524,19 @@ struct LinOut {
   // rows of the chunk's tokens, T elements (or fp32) of stride ld
   template <typename T>
   __device__ __forceinline__ void store(T* base, unsigned ld, int count, int w, int g, int c) const {
-#pragma unroll
-    for (int it = 0; it < C::IT; ++it) {
-      if (count < C::CH && 16 * it + c >= count) continue;
-      T* const p = (T*)((char*)base + ((16 * it + c) * ld + 16 * w + 4 * g) * (unsigned)sizeof(T));
+    const unsigned at = (c * ld + 16 * w + 4 * g) * (unsigned)sizeof(T), step = 16 * ld * (unsigned)sizeof(T);
+    auto put = [&](int it) {
+      char* const p = (char*)base + (size_t)(it * step) + at;
       if constexpr (sizeof(T) == 4) *(f32x4*)p = o[it];
       else *(u32x2*)p = u32x2{pack_bf16x2(o[it][0], o[it][1]), pack_bf16x2(o[it][2], o[it][3])};
+    };
+    if (count == C::CH) {
+#pragma unroll
+      for (int it = 0; it < C::IT; ++it) put(it);
+    } else {
+#pragma unroll
+      for (int it = 0; it < C::IT; ++it)
+        if (16 * it + c < count) put(it);
     }
   }
 };

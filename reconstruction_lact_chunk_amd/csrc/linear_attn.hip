@@ -93,8 +93,9 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
 }
 
 // ---- what a segment adds ----------------------------------------------------------
-// One workgroup to a (segment, head): the states' half of the pass, blockIdx.y 1 for the
-// gradients' (last to first).
+// One workgroup to a (segment, head), blockIdx.y 1 for the gradients.  Nothing is read from the
+// state here, so the chunks can go the other way than in the pass that follows: what this
+// one read last, and caches may still hold, is what that one reads first.
 template <int D, bool F32, bool REV>
 __device__ __forceinline__ void segment_state(const LinArgs& a, const LinSeg& sg, int h, uint16_t* lds,
                                               LinFactors* fac) {
@@ -112,7 +113,7 @@ __device__ __forceinline__ void segment_state(const LinArgs& a, const LinSeg& sg
   st.zero();
   LinFetch<D, F32> fb, fc;
   // chunk j of the pass: its first token, tokens and decays
-  auto first = [&](int j) { return (REV ? n - 1 - j : j) * C::CH; };
+  auto first = [&](int j) { return (REV ? j : n - 1 - j) * C::CH; };
   auto tokens = [&](int j) { return sg.count - first(j) < C::CH ? sg.count - first(j) : C::CH; };
   auto decay = [&](int j) {
     return gp && lane < tokens(j) ? gp[(int64_t)(first(j) + lane) * a.ld_g] : 0.f;
@@ -122,11 +123,10 @@ __device__ __forceinline__ void segment_state(const LinArgs& a, const LinSeg& sg
     fc.load(cp + (int64_t)first(j) * ct.ld, (unsigned)ct.ld, tokens(j));
   };
   const bool mine = w == C::WAVES - 1;  // the factors are this wave's, a chunk ahead
-  const float scale = REV ? a.scale : 1.f;
   float gl = 0.f;
   fetch(0);
   if (mine) {
-    lin_factors<REV>(fac, nullptr, decay(0), tokens(0), scale);
+    lin_reach<REV>(fac, nullptr, decay(0), tokens(0), a.scale);
     if (n > 1) gl = decay(1);
   }
   for (int j = 0; j < n; ++j) {
@@ -136,15 +136,12 @@ __device__ __forceinline__ void segment_state(const LinArgs& a, const LinSeg& sg
     const LinFactors* const f = fac + (j & 1);
     if (j + 1 < n) fetch(j + 1);
     if (mine && j + 1 < n) {
-      lin_factors<REV>(fac + (~j & 1), f, gl, tokens(j + 1), scale);
+      lin_reach<REV>(fac + (~j & 1), f, gl, tokens(j + 1), a.scale);
       if (j + 2 < n) gl = decay(j + 2);
     }
-    if (f->flags & kLinScale) st.scale(f->pre);
-    if (f->flags & kLinGated) st.scale(f->last);
     lin_tokens<D, F32, REV, false>(nullptr, st, nullptr, lds, lds + C::TILE, f, w, lane, g, c);
     __syncthreads();
   }
-  st.scale(fac[(n - 1) & 1].end);
   st.store(a.part[REV] + ((int64_t)(sg.slot + (REV ? -1 : 1)) * a.heads + h) * D * D, w, g, c);
   if (mine && lane == 0) a.decay[REV][(int64_t)sg.slot * a.heads + h] = exp2_wide(fac[(n - 1) & 1].sum);
 }
@@ -283,28 +280,34 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_out
         lin_factors<false>(fac + (~j & 1), f, next_decays[lane], tokens(j + 1), a.scale);
       }
       if (F32 && j + 1 < n) fetch(j + 1);
-      for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
-        const LinLane l(lane);
-        const int fr = t >> 1;
-        const int it = C::CH == 32 || fr < 2 ? fr : 2 + (fr - 2) / 2, ts = C::CH == 32 || fr < 2 ? 0 : (fr - 2) & 1;
-        const int jt = 2 * ts + (t & 1);
-        const f32x4 x = lin_gate<false>(lin_tri<D, F32>(q, k, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
-        lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
-      }
       if (flags & kLinScale) st.scale(f->pre);
-      LinOut<D, F32> out;
-      const LinLane lr(lane);
-      out.read(st, q, lr.g, lr.c);
-      if (flags & kLinGated) {
-        out.scale(f, c);
-        st.scale(f->last);
-      }
-      __syncthreads();
-      const LinLane lt(lane);
-      lin_tokens<D, F32, false, true>(&out, st, tri, k, v, f, w, lt.lane, lt.g, lt.c);
-      const LinLane lo(lane);
-      if (!(flags & kLinGated)) out.scale(f, lo.c);
-      out.store(op + (int64_t)j * C::CH * a.ld_o, (unsigned)a.ld_o, tokens(j), w, lo.g, lo.c);
+      auto chunk = [&](auto gated) {
+        constexpr bool GATED = decltype(gated)::value;
+        for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
+          const LinLane l(lane);
+          const int fr = t >> 1;
+          const int it = C::CH == 32 || fr < 2 ? fr : 2 + (fr - 2) / 2, ts = C::CH == 32 || fr < 2 ? 0 : (fr - 2) & 1;
+          const int jt = 2 * ts + (t & 1);
+          const f32x4 x =
+              lin_gate<false, GATED>(lin_tri<D, F32>(q, k, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
+          lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
+        }
+        LinOut<D, F32> out;
+        const LinLane lr(lane);
+        out.read(st, q, lr.g, lr.c);
+        if (GATED) {
+          out.scale(f, c);
+          st.scale(f->last);
+        }
+        __syncthreads();
+        const LinLane lt(lane);
+        lin_tokens<D, F32, false, true>(&out, st, tri, k, v, f, w, lt.lane, lt.g, lt.c);
+        const LinLane lo(lane);
+        if (!GATED) out.scale(f, lo.c);
+        out.store(op + (int64_t)j * C::CH * a.ld_o, (unsigned)a.ld_o, tokens(j), w, lo.g, lo.c);
+      };
+      if (flags & kLinGated) chunk(LinBool<true>{});
+      else chunk(LinBool<false>{});
       __syncthreads();
       if (!F32 && j + 1 < n) fetch(j + 1);
       gl = mine && j + 2 < n ? decay(j + 2) : 0.f;

@@ -2,6 +2,8 @@
 // of a segment to the first for dk and dv, one from the first to the last for dq and dg.
 #include "linear_attn.h"
 
+#include <type_traits>
+
 namespace zm {
 
 namespace {
@@ -22,14 +24,22 @@ __device__ __forceinline__ float prefix16(float x, int c) {
   return x;
 }
 
-// A lane's four outputs of a token times the same elements of a token tensor's row.
-__device__ __forceinline__ float dot4(const f32x4& o, const float* p) {
-  const f32x4 v = *(const f32x4*)p;
+// A lane's four outputs of a token times the same elements of a token tensor: in memory, or in
+// a tile.
+__device__ __forceinline__ float dot4(const f32x4& o, const f32x4& v) {
   return o[0] * v[0] + o[1] * v[1] + o[2] * v[2] + o[3] * v[3];
 }
-__device__ __forceinline__ float dot4(const f32x4& o, const uint16_t* p) {
-  const u32x2 v = *(const u32x2*)p;
+__device__ __forceinline__ float dot4(const f32x4& o, const u32x2& v) {
   return o[0] * bf16lo(v[0]) + o[1] * bf16hi(v[0]) + o[2] * bf16lo(v[1]) + o[3] * bf16hi(v[1]);
+}
+template <int D, bool F32>
+__device__ __forceinline__ float dot4(const f32x4& o, const uint16_t* tile, int row, int w, int g) {
+  using C = LinCfg<D, F32>;
+  float s = 0.f;
+#pragma unroll
+  for (int k = C::NT - 1; k >= 0; --k)
+    s += dot4(o, *(const u32x2*)(tile + k * C::PART + lin_at<D, F32>(row, 2 * w + (g >> 1)) + 4 * (g & 1)));
+  return s;
 }
 
 // ---- dk, dv --------------------------------------------------------------------
@@ -103,77 +113,82 @@ __global__ __launch_bounds__(8 * D) void k_linear_dkdv(LinArgs a) {
       const int flags = f->flags;
       if (mine && j > 0) lin_factors<true>(fac + (~j & 1), f, next_decays[lane], tokens(j - 1), a.scale);
       if (j > 0) fetch(j - 1);
-      // wave w < 2 TS the source tokens of row tile w
-      float cross[C::IT] = {};
-      if (w < 2 * C::TS) {
-        const int jt = w, ts = jt >> 1;
-        const LinLane l(lane);
-        const int g = l.g, c = l.c;
-        float before[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int it = 0; it < C::IT; ++it) {
-          if (!lin_in<D, F32, true>(it, ts)) continue;
-          const f32x4 x = lin_gate<true>(lin_tri<D, F32>(ta, tb, it, jt, g, c), f, a.scale, it, jt, g, c);
-          lin_put(tri, C::FRAGS, lin_frag<D, F32, true>(it, ts), jt, l.lane, x);
-          if (side && a.flow) {
-            // of source i's row of X, what comes from tokens before t = 16 it + c, if t <= i
-            const f32x4 y = lin_tri<D, F32>(k, q, it, jt, g, c);
-            const float up = flags & kLinGated ? 1.f : f->up[16 * it + c];
-            float sum = 0.f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float p = prefix16(x[r] * y[r] * up, c);
-              const float left = __shfl_up(p, 1, 16);
-              if (token_row(jt, 4 * g) + r >= 16 * it + c) sum += before[r] + (c ? left : 0.f);
-              before[r] += __shfl(p, 15, 16);
-            }
-            cross[it] += group_sum(sum);
-          }
-        }
-      }
       if (flags & kLinScale) st.scale(f->pre);
-      LinOut<D, F32> out;
-      {
-        const LinLane l(lane);
-        out.read(st, ta, l.g, l.c);
-      }
-      if (a.flow) {
-        const LinLane l(lane);
-        const int g = l.g, c = l.c;
-        if (side) {
-          if (w == 0 && lane == 0) a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] = f->s;
-          float* const dump = a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
-#pragma unroll
-          for (int mt = 0; mt < C::MT; ++mt) *(f32x4*)(dump + mt * 256) = st.m[mt];
-          if (w < 4 && g == 0)
-#pragma unroll
-            for (int it = 0; it < C::IT; ++it) crossing[w][16 * it + c] = cross[it];
-        } else {
+      auto chunk = [&](auto gated) {
+        constexpr bool GATED = decltype(gated)::value;
+        // wave w < 2 TS the source tokens of row tile w
+        float cross[C::IT] = {};
+        if (w < 2 * C::TS) {
+          const int jt = w, ts = jt >> 1;
+          const LinLane l(lane);
+          const int g = l.g, c = l.c;
+          float before[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int it = 0; it < C::IT; ++it) {
-            const int row = 16 * it + c < count ? 16 * it + c : count - 1;
-            const float x = group_sum(dot4(out.o[it], vp + ((int64_t)j * C::CH + row) * a.v.ld + 16 * w + 4 * g));
-            if (g == 0) going[w][16 * it + c] = 16 * it + c < count ? x * f->up[16 * it + c] : 0.f;
+            if (!lin_in<D, F32, true>(it, ts)) continue;
+            const f32x4 x = lin_gate<true, GATED>(lin_tri<D, F32>(ta, tb, it, jt, g, c), f, a.scale, it, jt, g, c);
+            lin_put(tri, C::FRAGS, lin_frag<D, F32, true>(it, ts), jt, l.lane, x);
+            if (side && a.flow) {
+              // of source i's row of X, what comes from tokens before t = 16 it + c, if t <= i
+              const f32x4 y = lin_tri<D, F32>(k, q, it, jt, g, c);
+              const float up = GATED ? 1.f : f->up[16 * it + c];
+              float sum = 0.f;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float p = prefix16(x[r] * y[r] * up, c);
+                const float left = __shfl_up(p, 1, 16);
+                if (token_row(jt, 4 * g) + r >= 16 * it + c) sum += before[r] + (c ? left : 0.f);
+                before[r] += __shfl(p, 15, 16);
+              }
+              cross[it] += group_sum(sum);
+            }
           }
         }
-      }
-      if (flags & kLinGated) {
-        out.scale(f, c);
-        st.scale(f->last);
-      }
-      __syncthreads();
-      const LinLane lt(lane);
-      lin_tokens<D, F32, true, true>(&out, st, tri, tb, tc, f, w, lt.lane, lt.g, lt.c);
-      const LinLane l(lane);
-      const int g = l.g, c = l.c;
-      if (!(flags & kLinGated)) out.scale(f, c);
-      if (!side) {
-        out.store((T*)a.dv + tok0 * a.ld_dv + h * D, (unsigned)a.ld_dv, count, w, g, c);
-      } else if (a.dk_part) {
-        out.store(a.dk_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, g, c);
-      } else {
-        out.store((T*)a.dk + tok0 * a.ld_dk + hk * D, (unsigned)a.ld_dk, count, w, g, c);
-      }
+        LinOut<D, F32> out;
+        {
+          const LinLane l(lane);
+          out.read(st, ta, l.g, l.c);
+        }
+        if (a.flow) {
+          const LinLane l(lane);
+          const int g = l.g, c = l.c;
+          if (side) {
+            if (w == 0 && lane == 0) a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] = f->s;
+            float* const dump =
+                a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
+#pragma unroll
+            for (int mt = 0; mt < C::MT; ++mt) *(f32x4*)(dump + mt * 256) = st.m[mt];
+            if (w < 4 && g == 0)
+#pragma unroll
+              for (int it = 0; it < C::IT; ++it) crossing[w][16 * it + c] = cross[it];
+          } else {
+#pragma unroll
+            for (int it = 0; it < C::IT; ++it) {
+              const int t = 16 * it + c;
+              const float x = group_sum(dot4<D, F32>(out.o[it], v, t, w, g));
+              if (g == 0) going[w][t] = t < count ? x * f->up[t] : 0.f;
+            }
+          }
+        }
+        if (GATED) {
+          out.scale(f, c);
+          st.scale(f->last);
+        }
+        __syncthreads();
+        const LinLane lt(lane);
+        lin_tokens<D, F32, true, true>(&out, st, tri, tb, tc, f, w, lt.lane, lt.g, lt.c);
+        const LinLane l(lane);
+        if (!GATED) out.scale(f, l.c);
+        if (!side) {
+          out.store((T*)a.dv + tok0 * a.ld_dv + h * D, (unsigned)a.ld_dv, count, w, l.g, l.c);
+        } else if (a.dk_part) {
+          out.store(a.dk_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, l.g, l.c);
+        } else {
+          out.store((T*)a.dk + tok0 * a.ld_dk + hk * D, (unsigned)a.ld_dk, count, w, l.g, l.c);
+        }
+      };
+      if (flags & kLinGated) chunk(LinBool<true>{});
+      else chunk(LinBool<false>{});
       if (a.flow && wave == 0) {
         float x = 0.f, y = 0.f;
         if (lane < C::CH) {
@@ -204,6 +219,7 @@ template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
+  using Four = std::conditional_t<F32, f32x4, u32x2>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[3 * C::TILE + C::TRI];
   __shared__ LinFactors fac[2];
   __shared__ float next_decays[64];
@@ -270,54 +286,67 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
     const int flags = f->flags;
     if (mine && j + 1 < n) lin_factors<false>(fac + (~j & 1), f, next_decays[lane], tokens(j + 1), a.scale);
     if (F32 && j + 1 < n) fetch(j + 1);
-    for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
-      const LinLane l(lane);
-      const int g = l.g, c = l.c;
-      const int fr = t >> 1;
-      const int it = C::CH == 32 || fr < 2 ? fr : 2 + (fr - 2) / 2, ts = C::CH == 32 || fr < 2 ? 0 : (fr - 2) & 1;
-      const int jt = 2 * ts + (t & 1);
-      const f32x4 x = lin_gate<false>(lin_tri<D, F32>(od, v, it, jt, g, c), f, a.scale, it, jt, g, c);
-      lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
-    }
     if (flags & kLinScale) st.scale(f->pre);
-    LinOut<D, F32> out;
-    {
-      const LinLane l(lane);
-      out.read(st, od, l.g, l.c);
-    }
-    if (a.flow) {
-      const LinLane l(lane);
-      const int g = l.g, c = l.c;
-      const float* const dump = a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
-      float e = 0.f;
+    auto chunk = [&](auto gated) {
+      constexpr bool GATED = decltype(gated)::value;
+      // q's elements of a lane's outputs are on their way meanwhile
+      Four qe[C::IT];
+      if (a.flow) {
+        const LinLane l(lane);
 #pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt) {
-        const f32x4 x = *(const f32x4*)(dump + mt * 256);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][r], x[r], e);
+        for (int it = 0; it < C::IT; ++it) {
+          const int row = 16 * it + l.c < count ? 16 * it + l.c : count - 1;
+          qe[it] = *(const Four*)(qp + ((int64_t)j * C::CH + row) * a.q.ld + 16 * w + 4 * l.g);
+        }
       }
-#pragma unroll
-      for (int m = 1; m < 64; m *= 2) e += __shfl_xor(e, m, 64);
-      if (lane == 0) through[w] = e;
-#pragma unroll
-      for (int it = 0; it < C::IT; ++it) {
-        const int row = 16 * it + c < count ? 16 * it + c : count - 1;
-        const float x = group_sum(dot4(out.o[it], qp + ((int64_t)j * C::CH + row) * a.q.ld + 16 * w + 4 * g));
-        if (g == 0) coming[w][16 * it + c] = 16 * it + c < count ? x * f->up[16 * it + c] : 0.f;
+      for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
+        const LinLane l(lane);
+        const int fr = t >> 1;
+        const int it = C::CH == 32 || fr < 2 ? fr : 2 + (fr - 2) / 2, ts = C::CH == 32 || fr < 2 ? 0 : (fr - 2) & 1;
+        const int jt = 2 * ts + (t & 1);
+        const f32x4 x =
+            lin_gate<false, GATED>(lin_tri<D, F32>(od, v, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
+        lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
       }
-    }
-    if (flags & kLinGated) {
-      out.scale(f, c);
-      st.scale(f->last);
-    }
-    __syncthreads();
-    const LinLane lt(lane);
-    lin_tokens<D, F32, false, true>(&out, st, tri, v, k, f, w, lt.lane, lt.g, lt.c);
-    const LinLane lo(lane);
-    const int g = lo.g, c = lo.c;
-    if (!(flags & kLinGated)) out.scale(f, c);
-    if (a.o_part) out.store(a.o_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, g, c);
-    else out.store((T*)a.o + tok0 * a.ld_o + hk * D, (unsigned)a.ld_o, count, w, g, c);
+      LinOut<D, F32> out;
+      {
+        const LinLane l(lane);
+        out.read(st, od, l.g, l.c);
+      }
+      if (a.flow) {
+        const LinLane l(lane);
+        const float* const dump =
+            a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
+        float e = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) {
+          const f32x4 x = *(const f32x4*)(dump + mt * 256);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][r], x[r], e);
+        }
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) e += __shfl_xor(e, m, 64);
+        if (lane == 0) through[w] = e;
+#pragma unroll
+        for (int it = 0; it < C::IT; ++it) {
+          const float x = group_sum(dot4(out.o[it], qe[it]));
+          if (l.g == 0) coming[w][16 * it + l.c] = 16 * it + l.c < count ? x * f->up[16 * it + l.c] : 0.f;
+        }
+      }
+      if (GATED) {
+        out.scale(f, c);
+        st.scale(f->last);
+      }
+      __syncthreads();
+      const LinLane lt(lane);
+      lin_tokens<D, F32, false, true>(&out, st, tri, v, k, f, w, lt.lane, lt.g, lt.c);
+      const LinLane l(lane);
+      if (!GATED) out.scale(f, l.c);
+      if (a.o_part) out.store(a.o_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, l.g, l.c);
+      else out.store((T*)a.o + tok0 * a.ld_o + hk * D, (unsigned)a.ld_o, count, w, l.g, l.c);
+    };
+    if (flags & kLinGated) chunk(LinBool<true>{});
+    else chunk(LinBool<false>{});
     if (a.flow && w == 0) {
       float x = 0.f, e = 0.f;
 #pragma unroll
