@@ -40,7 +40,7 @@ int check_ptr(const void* p, size_t align) { return p && aligned(p, align) ? ZM_
 
 struct LinPlan {
   int64_t n_chunks;
-  int n_segs, seg_chunks, chunk;
+  int n_segs, n_slots, seg_chunks, chunk;
   int64_t slots;      // states of segments that the workspace has place for
   bool split;         // a sequence can have several segments
 };
@@ -61,6 +61,7 @@ LinPlan lin_plan(const zm_linear_desc* d, int64_t n) {
   const int64_t full = n / tokens;
   p.split = n > tokens;
   p.n_segs = (int)((p.split ? full : 0) + d->n_seq);
+  p.n_slots = p.split ? (int)(full + (full < d->n_seq ? full : d->n_seq)) : 0;
   // Place for the full segments and one more of each sequence that has some.  full falls
   // where seg steps up, and with it split can; neither n / chunk nor target / heads is
   // passed, and split needs n (target - heads) > heads (ragged - chunk + 1), so that the
@@ -92,11 +93,15 @@ void common_ws(LinArgs& a, Carve& c, const zm_linear_desc* d, const LinPlan& p, 
   s.n = (int)n;
   s.n_seq = d->n_seq;
   s.n_segs = p.n_segs;
+  s.n_slots = p.n_slots;
+  // 61 sequences of 4 to 24 chunks, 16 heads: see the table's kernel
+  s.longest_first = (int64_t)p.n_segs * d->heads > 2 * kTargetWgs && p.n_segs <= kLinSorted;
   s.seg_tokens = p.seg_chunks * p.chunk;
   s.chunk = p.chunk;
   if (d->n_seq > 1) {
     s.segs = c.take<LinSeg>(p.slots + d->n_seq);
-    s.of_seq = c.take<int2>(d->n_seq + 2);
+    s.by_slot = c.take<int>(p.slots);
+    s.all = c.take<int4>(1);
   }
   for (int i = 0; i < ways && p.slots > 0; ++i) {
     a.part[i] = c.take<float>((size_t)p.slots * d->heads * d->d_head * d->d_head);
@@ -132,7 +137,8 @@ size_t backward_ws(LinArgs& a, const zm_linear_desc* d, const LinPlan& p, int64_
 
 int check_counts(const zm_linear_desc* d, int64_t n) {
   if (n < 0 || n > kMaxLinTokens || (d->n_seq == 0 && n > 0)) return ZM_ERR_INVALID_ARG;
-  // the largest grid: a block of 512 threads to each segment and head
+  // the largest grid: a block of 512 threads to each segment and head (the join's 32 to a slot
+  // and head are at most 32 times 1024 + heads)
   if ((int64_t)lin_plan(d, n).n_segs * d->heads * 2 > kMaxLinBlocks) return ZM_ERR_UNSUPPORTED;
   return ZM_OK;
 }
@@ -205,7 +211,7 @@ int zm_linear_attention(const zm_linear_desc* desc, int64_t n, const int32_t* of
   const bool f32 = desc->io_dtype == ZM_F32;
   if (a.sq.segs) ZM_HIP(launch_linear_table(a.sq, st));
   if (p.split) {
-    ZM_HIP(launch_linear_states(a, desc->d_head, f32, false, st));
+    ZM_HIP(launch_linear_states(a, desc->d_head, f32, st));
     ZM_HIP(launch_linear_join(a, desc->d_head, false, st));
   }
   ZM_HIP(launch_linear_out(a, desc->d_head, f32, st));
@@ -300,10 +306,8 @@ int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const in
     a.dg = one ? sums : dg;
     if (!dg) a.flow = nullptr;
     if (a.sq.segs) ZM_HIP(launch_linear_table(a.sq, st));
-    if (p.split) {
-      ZM_HIP(launch_linear_states(a, d, f32, true, st));
-      ZM_HIP(launch_linear_join(a, d, true, st));
-    }
+    if (p.split || a.flow) ZM_HIP(launch_linear_grad_states(a, d, f32, st));
+    if (p.split) ZM_HIP(launch_linear_join(a, d, true, st));
     ZM_HIP(launch_linear_dkdv(a, d, f32, st));
     if (n > 0) ZM_HIP(launch_linear_dq(a, d, f32, st));
     if (n > 0 && a.o_part) {

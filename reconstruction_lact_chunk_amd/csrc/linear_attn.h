@@ -62,7 +62,7 @@ struct LinCfg {
 };
 
 // What a chunk's tokens are multiplied with; computed by one wave.
-struct LinFactors {
+struct alignas(16) LinFactors {
   float up[64];    // of outputs; kLinGated: of A M^ alone
   float dn[64];    // of C in the state and, unless kLinGated, of T's columns
   double cs[64];   // sums of the chunk's decays, powers of two
@@ -87,15 +87,19 @@ struct LinSeg {
   int seq, flags;   // 1 first | 2 last of its sequence
   int chunk0;       // chunks before it (each segment but a sequence's last has seg_chunks)
   int slot;         // of its state, in a sequence of several segments
-  int pad[2];
+  int segs;         // of its sequence
+  int pad;
 };
+constexpr int kLinSorted = 512;  // segments that the table puts in order
 
 struct LinSeqs {
   const int* offsets;   // [n_seq + 1] or null: one sequence of all n tokens
   LinSeg* segs;         // null without a table (one sequence)
-  int2* of_seq;         // [n_seq] {first slot, segments}, then {first token, end}, {chunks, -}
+  int* by_slot;         // [slots] the segment, -1: unused
+  int4* all;            // {first token, end, chunks, -} of all sequences together
   int n, n_seq;
-  int n_segs;           // upper bound over every content of offsets
+  int n_segs, n_slots;  // upper bounds over every content of offsets
+  bool longest_first;   // the table's order, else that of the tokens
   int seg_tokens;       // tokens of a segment, a multiple of the chunk
   int chunk;
 };
@@ -129,7 +133,7 @@ struct LinArgs {
   int64_t ld_dv;
   float* o_part;       // dq and dk to each value head [n][heads][d], where these share key heads
   float* dk_part;
-  float* flow;         // [n][heads]: the part of dg that the reverse pass forms, or null without g
+  float* flow;         // [n][heads]: the parts of dg that the first two passes form, or null without g
   float* d_dump;       // D^T at every chunk's end, less a power of two
   double* d_exp;       // [chunks][heads] that power
   float* dg;           // [n][heads], or, with ld_g = 0, the chunks' sums [chunks][heads]
@@ -137,7 +141,7 @@ struct LinArgs {
 
 // First token and end of all sequences together.
 __device__ __forceinline__ int2 lin_range(const LinSeqs& s) {
-  if (s.segs) return s.of_seq[s.n_seq];
+  if (s.segs) return int2{s.all->x, s.all->y};
   int a = 0, e = s.n;
   if (s.offsets) {
     a = clampi(s.offsets[0], 0, s.n);
@@ -169,6 +173,20 @@ __device__ __forceinline__ LinSeg lin_seg(const LinSeqs& s, int si) {
   g.flags = (si == 0 ? 1 : 0) | (si == segs - 1 ? 2 : 0);
   g.chunk0 = (int)(at / s.chunk);
   g.slot = si;
+  g.segs = segs;
+  return g;
+}
+// The segment whose state is in a slot: of sequences of several segments only.
+__device__ __forceinline__ LinSeg lin_slot(const LinSeqs& s, int slot) {
+  LinSeg g;
+  if (s.segs) {
+    const int i = s.by_slot[slot];
+    g.count = -1;
+    if (i >= 0) g = s.segs[i];
+  } else {
+    g = lin_seg(s, slot);
+    if (g.count >= 0 && g.segs < 2) g.count = -1;
+  }
   return g;
 }
 
@@ -331,6 +349,19 @@ __device__ __forceinline__ double lin_prefix(double x) {
   x = lin_add_from<0x142, 0xa>(x);  // lane 15 to row 1, 47 to row 3
   return lin_add_from<0x143, 0xc>(x);  // lane 31 to rows 2 and 3
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float lin_add_from(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float lin_prefix16(float x) {  // within 16 lanes
+  x = lin_add_from<0x111, 0xf>(x);
+  x = lin_add_from<0x112, 0xf>(x);
+  x = lin_add_from<0x114, 0xf>(x);
+  return lin_add_from<0x118, 0xf>(x);
+}
+__device__ __forceinline__ float lin_prefix(float x) {
+  return lin_add_from<0x143, 0xc>(lin_add_from<0x142, 0xa>(lin_prefix16(x)));
+}
 __device__ __forceinline__ double lin_lane63(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
   const unsigned lo = __builtin_amdgcn_readlane((unsigned)b, 63), hi = __builtin_amdgcn_readlane((unsigned)(b >> 32), 63);
@@ -385,16 +416,14 @@ __device__ __forceinline__ void lin_factors(LinFactors* f, const LinFactors* bef
 }
 
 // What a chunk's C is multiplied with where its part of the state is taken to the end of the
-// chunks that the pass has been through, `before` them; REV: to the beginning, times scale.
-template <bool REV>
-__device__ __forceinline__ void lin_reach(LinFactors* f, const LinFactors* before, float gl, int count, float scale) {
+// chunks behind it, `after` them.
+__device__ __forceinline__ void lin_reach(LinFactors* f, const LinFactors* after, float gl, int count) {
   const int lane = threadIdx.x & 63;
   if (lane >= count) gl = 0.f;
   if (gl < kMinLogDecay) gl = kMinLogDecay;
   const double c = lin_prefix(gl * kLog2E);
-  const double last = lin_lane63(c), sum = before ? before->sum : 0.0;
-  const float w = exp2_wide(sum + (REV ? c : last - c));
-  f->dn[lane] = lane < count ? (REV ? w * scale : w) : 0.f;
+  const double last = lin_lane63(c), sum = after ? after->sum : 0.0;
+  f->dn[lane] = lane < count ? exp2_wide(sum + last - c) : 0.f;
   if (lane == 0) f->sum = sum + last;
 }
 
@@ -544,7 +573,7 @@ struct LinOut {
 // out += T C and M^ <- M^ + B^T (dn o C).
 template <int D, bool F32, bool REV, bool OUT>
 __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>& st, const uint16_t* frags,
-                                           const uint16_t* b, const uint16_t* cc, const LinFactors* f, int w, int lane,
+                                           const uint16_t* b, const uint16_t* cc, const float* dn, int w, int lane,
                                            int g, int c) {
   using C = LinCfg<D, F32>;
 #pragma unroll
@@ -577,7 +606,7 @@ __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>
         x[2 * i + 1] += bf16hi(p1[i]) + bf16hi(p2[i]);
       }
     }
-    const f32x4 w0 = *(const f32x4*)(f->dn + 32 * ts + dtau(g, 0)), w1 = *(const f32x4*)(f->dn + 32 * ts + dtau(g, 4));
+    const f32x4 w0 = *(const f32x4*)(dn + 32 * ts + dtau(g, 0)), w1 = *(const f32x4*)(dn + 32 * ts + dtau(g, 4));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[e] *= w0[e];
@@ -592,13 +621,14 @@ __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>
 // ---- launchers ----------------------------------------------------------------
 // The table of segments (n_seq > 1).
 hipError_t launch_linear_table(const LinSeqs& s, hipStream_t st);
-// What each segment adds to the state, all but the last of a sequence; with both, the
-// gradients' too, all but the first.
-hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, bool both, hipStream_t st);
+// What each segment of a sequence adds to the state, all but its last.
+hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_join(const LinArgs& a, int d, bool both, hipStream_t st);
 // The outputs and last states.
 hipError_t launch_linear_out(const LinArgs& a, int d, bool f32, hipStream_t st);
-// dk, dv, flow, d_dump and the first states' gradient; then dq and dg.
+// Gradients: what segments add to states and their gradients, and dg's part within the chunks;
+// dk, dv, dg's part to the chunks' ends, d_dump and the first states' gradient; dq and dg.
+hipError_t launch_linear_grad_states(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_dkdv(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_dq(const LinArgs& a, int d, bool f32, hipStream_t st);
 // y [n][heads_k][d] from x [n][heads][d] summed over the value heads of a key head.

@@ -8,9 +8,11 @@ namespace {
 
 // ---- table --------------------------------------------------------------------
 // One workgroup: the clamped, nondecreasing offsets, the prefix sums of chunks, segments
-// and slots, and every segment's entry.
+// and slots, and every segment's entry; longest first where there are more workgroups than
+// run at once, so that long ones do not end last.
 __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
-  __shared__ int part[4][16], total;
+  __shared__ int part[4][16], total, slots;
+  __shared__ LinSeg seg_l[kLinSorted];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, per = (s.n_seq + 1023) / 1024;
   const int b0 = t * per < s.n_seq ? t * per : s.n_seq, b1 = b0 + per < s.n_seq ? b0 + per : s.n_seq;
   // running maximum of the clamped ends
@@ -65,7 +67,6 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
     if (e < run) e = run;
     const int len = e - run;
     const int k = lin_segs(s, len);
-    s.of_seq[b] = int2{at[2], k};
     for (int i = 0; i < k; ++i) {
       const int64_t from = (int64_t)i * s.seg_tokens;
       LinSeg g;
@@ -75,8 +76,15 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
       g.flags = (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0);
       g.chunk0 = at[0] + (int)(from / s.chunk);
       g.slot = at[2] + i;
-      g.pad[0] = g.pad[1] = 0;
-      s.segs[at[1] + i] = g;
+      g.segs = k;
+      g.pad = 0;
+      const int si = at[1] + i;
+      if (s.longest_first) {
+        seg_l[si] = g;
+      } else {
+        s.segs[si] = g;
+        if (k > 1) s.by_slot[g.slot] = si;
+      }
     }
     at[0] += lin_chunks(s, len);
     at[1] += k;
@@ -85,124 +93,117 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
   }
   if (t == 1023) {  // behind the last sequence, whosever that is
     total = at[1];
-    s.of_seq[s.n_seq] = int2{start, run};
-    s.of_seq[s.n_seq + 1] = int2{at[0], 0};
+    slots = at[2];
+    *s.all = int4{start, run, at[0], 0};
   }
   __syncthreads();
+  if (s.longest_first && t < total) {
+    const int mine = seg_l[t].count;
+    int rank = 0;
+    for (int i = 0; i < total; ++i) {
+      const int c = seg_l[i].count;
+      rank += c > mine || (c == mine && i < t);
+    }
+    s.segs[rank] = seg_l[t];
+    if (seg_l[t].segs > 1) s.by_slot[seg_l[t].slot] = rank;
+  }
   for (int i = total + t; i < s.n_segs; i += 1024) s.segs[i].count = -1;
+  for (int i = slots + t; i < s.n_slots; i += 1024) s.by_slot[i] = -1;
 }
 
 // ---- what a segment adds ----------------------------------------------------------
-// One workgroup to a (segment, head), blockIdx.y 1 for the gradients.  Nothing is read from the
-// state here, so the chunks can go the other way than in the pass that follows: what this
-// one read last, and caches may still hold, is what that one reads first.
-template <int D, bool F32, bool REV>
-__device__ __forceinline__ void segment_state(const LinArgs& a, const LinSeg& sg, int h, uint16_t* lds,
-                                              LinFactors* fac) {
+// One workgroup to a (segment, head).  Nothing is read from the state here, so the chunks go
+// last to first: what this pass read last, and caches may still hold, is what the next
+// one reads first (100 frames: 135 -> 116 us).
+template <int D, bool F32>
+__global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * C::TILE];
+  __shared__ LinFactors fac[2];
+  const int h = blockIdx.x % a.heads;
+  const LinSeg sg = lin_slot(a.sq, blockIdx.x / a.heads);
+  if (sg.count <= 0 || (sg.flags & 2)) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int hk = h / (a.heads / a.heads_k);
-  const LinTokens bt = REV ? a.q : a.k, ct = REV ? a.d_o : a.v;
-  const T* const bp = (const T*)bt.p + (int64_t)sg.tok * bt.ld + hk * D;
-  const T* const cp = (const T*)ct.p + (int64_t)sg.tok * ct.ld + h * D;
+  const T* const kp = (const T*)a.k.p + (int64_t)sg.tok * a.k.ld + hk * D;
+  const T* const vp = (const T*)a.v.p + (int64_t)sg.tok * a.v.ld + h * D;
   const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
   const int n = (sg.count + C::CH - 1) / C::CH;
   LinState<D, F32> st;
   st.zero();
-  LinFetch<D, F32> fb, fc;
-  // chunk j of the pass: its first token, tokens and decays
-  auto first = [&](int j) { return (REV ? j : n - 1 - j) * C::CH; };
-  auto tokens = [&](int j) { return sg.count - first(j) < C::CH ? sg.count - first(j) : C::CH; };
+  LinFetch<D, F32> fk, fv;
+  auto tokens = [&](int j) { return sg.count - j * C::CH < C::CH ? sg.count - j * C::CH : C::CH; };
   auto decay = [&](int j) {
-    return gp && lane < tokens(j) ? gp[(int64_t)(first(j) + lane) * a.ld_g] : 0.f;
+    return gp && lane < tokens(j) ? gp[(int64_t)(j * C::CH + lane) * a.ld_g] : 0.f;
   };
   auto fetch = [&](int j) {
-    fb.load(bp + (int64_t)first(j) * bt.ld, (unsigned)bt.ld, tokens(j));
-    fc.load(cp + (int64_t)first(j) * ct.ld, (unsigned)ct.ld, tokens(j));
+    fk.load(kp + (int64_t)j * C::CH * a.k.ld, (unsigned)a.k.ld, tokens(j));
+    fv.load(vp + (int64_t)j * C::CH * a.v.ld, (unsigned)a.v.ld, tokens(j));
   };
   const bool mine = w == C::WAVES - 1;  // the factors are this wave's, a chunk ahead
   float gl = 0.f;
-  fetch(0);
+  fetch(n - 1);
   if (mine) {
-    lin_reach<REV>(fac, nullptr, decay(0), tokens(0), a.scale);
-    if (n > 1) gl = decay(1);
+    lin_reach(fac + ((n - 1) & 1), nullptr, decay(n - 1), tokens(n - 1));
+    if (n > 1) gl = decay(n - 2);
   }
-  for (int j = 0; j < n; ++j) {
-    fb.store(lds);
-    fc.store(lds + C::TILE);
+  for (int j = n - 1; j >= 0; --j) {
+    fk.store(lds);
+    fv.store(lds + C::TILE);
     __syncthreads();
     const LinFactors* const f = fac + (j & 1);
-    if (j + 1 < n) fetch(j + 1);
-    if (mine && j + 1 < n) {
-      lin_reach<REV>(fac + (~j & 1), f, gl, tokens(j + 1), a.scale);
-      if (j + 2 < n) gl = decay(j + 2);
+    if (j > 0) fetch(j - 1);
+    if (mine && j > 0) {
+      lin_reach(fac + (~j & 1), f, gl, tokens(j - 1));
+      if (j > 1) gl = decay(j - 2);
     }
-    lin_tokens<D, F32, REV, false>(nullptr, st, nullptr, lds, lds + C::TILE, f, w, lane, g, c);
+    lin_tokens<D, F32, false, false>(nullptr, st, nullptr, lds, lds + C::TILE, f->dn, w, lane, g, c);
     __syncthreads();
   }
-  st.store(a.part[REV] + ((int64_t)(sg.slot + (REV ? -1 : 1)) * a.heads + h) * D * D, w, g, c);
-  if (mine && lane == 0) a.decay[REV][(int64_t)sg.slot * a.heads + h] = exp2_wide(fac[(n - 1) & 1].sum);
-}
-
-template <int D, bool F32>
-__global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
-  using C = LinCfg<D, F32>;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * C::TILE];
-  __shared__ LinFactors fac[2];
-  const int h = blockIdx.x % a.heads;
-  const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
-  if (sg.count <= 0) return;
-  if (blockIdx.y == 0) {
-    if (!(sg.flags & 2)) segment_state<D, F32, false>(a, sg, h, lds, fac);
-  } else {
-    if (!(sg.flags & 1)) segment_state<D, F32, true>(a, sg, h, lds, fac);
-  }
+  st.store(a.part[0] + ((int64_t)(sg.slot + 1) * a.heads + h) * D * D, w, g, c);
+  if (mine && lane == 0) a.decay[0][(int64_t)sg.slot * a.heads + h] = exp2_wide(fac[0].sum);
 }
 
 // ---- join ------------------------------------------------------------------------
-// Four elements of a state a thread, a sequence's segments in order: each one's slot takes
-// the state at its start.  Loads of eight segments are in flight.
-__global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways, int64_t work) {
+// A block to 1024 elements of a state of a head, of the sequence whose first slot it has; a
+// thread four of them, the segments in order: each one's slot takes the state at its start
+// (the gradients: the other way, at its end).  Loads of 16 segments are in flight.
+__global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways) {
   const int blocks = dd / 1024;  // of a state
-  for (int64_t x = blockIdx.x; x < work; x += gridDim.x) {
-    const int el = 4 * ((int)(x % blocks) * 256 + threadIdx.x);
-    const int64_t y = x / blocks, z = y / a.heads;
-    const int h = (int)(y % a.heads), rev = (int)(z % ways);
-    const int64_t b = z / ways;
-    int2 s = {0, 0};  // first slot, segments
-    if (a.sq.segs) {
-      s = a.sq.of_seq[b];
-    } else {
-      const int2 r = lin_range(a.sq);
-      s.y = lin_segs(a.sq, r.y - r.x);
+  unsigned x = blockIdx.x;
+  const int el = 4 * ((int)(x % blocks) * 256 + threadIdx.x);
+  x /= blocks;
+  const int h = x % a.heads;
+  x /= a.heads;
+  const int rev = x % ways;
+  const LinSeg sg = lin_slot(a.sq, x / ways);
+  if (sg.count < 0 || !(sg.flags & 1)) return;
+  const int n = sg.segs;
+  const float* const init = rev ? a.dstate_out : a.state_in;
+  f32x4 m = {0.f, 0.f, 0.f, 0.f};
+  if (init) m = *(const f32x4*)(init + ((int64_t)sg.seq * a.heads + h) * dd + el);
+  const int64_t first = (int64_t)(rev ? sg.slot + n - 1 : sg.slot) * a.heads + h, step = rev ? -a.heads : a.heads;
+  float* const part = a.part[rev] + el;
+  const float* const decay = a.decay[rev];
+  *(f32x4*)(part + first * dd) = m;
+  constexpr int U = 16;
+  for (int i0 = 1; i0 < n; i0 += U) {
+    f32x4 add[U];
+    float f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = first + (i0 + u < n ? i0 + u : n - 1) * step;
+      add[u] = *(const f32x4*)(part + at * dd);
+      f[u] = decay[at - step];
     }
-    if (s.y < 2) continue;
-    const float* const init = rev ? a.dstate_out : a.state_in;
-    f32x4 m = {0.f, 0.f, 0.f, 0.f};
-    if (init) m = *(const f32x4*)(init + (b * a.heads + h) * dd + el);
-    const int64_t first = ((int64_t)(rev ? s.x + s.y - 1 : s.x) * a.heads + h), step = rev ? -a.heads : a.heads;
-    float* const part = a.part[rev] + el;
-    const float* const decay = a.decay[rev];
-    *(f32x4*)(part + first * dd) = m;
-    constexpr int U = 8;
-    for (int i0 = 1; i0 < s.y; i0 += U) {
-      f32x4 add[U];
-      float f[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t at = first + (i0 + u < s.y ? i0 + u : s.y - 1) * step;
-        add[u] = *(const f32x4*)(part + at * dd);
-        f[u] = decay[at - step];
-      }
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= n) break;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i0 + u >= s.y) break;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[r] = fmaf(m[r], f[u], add[u][r]);
-        *(f32x4*)(part + (first + (i0 + u) * step) * dd) = m;
-      }
+      for (int r = 0; r < 4; ++r) m[r] = fmaf(m[r], f[u], add[u][r]);
+      *(f32x4*)(part + (first + (i0 + u) * step) * dd) = m;
     }
   }
 }
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_out
         }
         __syncthreads();
         const LinLane lt(lane);
-        lin_tokens<D, F32, false, true>(&out, st, tri, k, v, f, w, lt.lane, lt.g, lt.c);
+        lin_tokens<D, F32, false, true>(&out, st, tri, k, v, f->dn, w, lt.lane, lt.g, lt.c);
         const LinLane lo(lane);
         if (!GATED) out.scale(f, lo.c);
         out.store(op + (int64_t)j * C::CH * a.ld_o, (unsigned)a.ld_o, tokens(j), w, lo.g, lo.c);
@@ -318,8 +319,8 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_out
 }
 
 template <int D>
-hipError_t states_any(const LinArgs& a, bool f32, bool both, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads), both ? 2 : 1), blk(4 * D);
+hipError_t states_any(const LinArgs& a, bool f32, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.sq.n_slots * a.heads)), blk(4 * D);
   if (f32) hipLaunchKernelGGL((k_linear_states<D, true>), grid, blk, 0, st, a);
   else hipLaunchKernelGGL((k_linear_states<D, false>), grid, blk, 0, st, a);
   return hipGetLastError();
@@ -340,15 +341,14 @@ hipError_t launch_linear_table(const LinSeqs& s, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, bool both, hipStream_t st) {
-  return d == 128 ? states_any<128>(a, f32, both, st) : states_any<64>(a, f32, both, st);
+hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, hipStream_t st) {
+  return d == 128 ? states_any<128>(a, f32, st) : states_any<64>(a, f32, st);
 }
 
 hipError_t launch_linear_join(const LinArgs& a, int d, bool both, hipStream_t st) {
   const int ways = both ? 2 : 1;
-  const int64_t work = (int64_t)a.sq.n_seq * ways * a.heads * (d * d / 1024);
-  const int64_t blocks = work < 64 * kTargetWgs ? work : 64 * kTargetWgs;
-  hipLaunchKernelGGL(k_linear_join, dim3((unsigned)blocks), dim3(256), 0, st, a, d * d, ways, work);
+  const int64_t blocks = (int64_t)a.sq.n_slots * ways * a.heads * (d * d / 1024);
+  hipLaunchKernelGGL(k_linear_join, dim3((unsigned)blocks), dim3(256), 0, st, a, d * d, ways);
   return hipGetLastError();
 }
 

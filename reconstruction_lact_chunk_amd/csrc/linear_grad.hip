@@ -1,5 +1,6 @@
-// Gradients of linear attention with decays (linear_attn.h): one pass from the last chunk
-// of a segment to the first for dk and dv, one from the first to the last for dq and dg.
+// Gradients of linear attention with decays (linear_attn.h): what segments add to the states
+// and their gradients, one pass from the last chunk of a segment to the first for dk and dv,
+// one from the first to the last for dq and dg.
 #include "linear_attn.h"
 
 #include <type_traits>
@@ -13,205 +14,346 @@ __device__ __forceinline__ float group_sum(float x) {
   x += __shfl_xor(x, 16, 64);
   return x + __shfl_xor(x, 32, 64);
 }
-
-// Sum of the lanes before, and of all up to this one, of 16.
-__device__ __forceinline__ float prefix16(float x, int c) {
-#pragma unroll
-  for (int m = 1; m < 16; m *= 2) {
-    const float o = __shfl_up(x, m, 16);
-    if (c >= m) x += o;
-  }
-  return x;
+// Within 16 lanes: of the lanes before, and of all.
+__device__ __forceinline__ float from_left(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x111, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float row16_sum(float x) {  // rotated by 8, 4, 2, 1
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x124, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x122, 0xf, 0xf, true));
+  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x121, 0xf, 0xf, true));
 }
 
-// A lane's four outputs of a token times the same elements of a token tensor: in memory, or in
-// a tile.
+// A lane's four outputs of a token times the same elements of a token tensor.
 __device__ __forceinline__ float dot4(const f32x4& o, const f32x4& v) {
   return o[0] * v[0] + o[1] * v[1] + o[2] * v[2] + o[3] * v[3];
 }
 __device__ __forceinline__ float dot4(const f32x4& o, const u32x2& v) {
   return o[0] * bf16lo(v[0]) + o[1] * bf16hi(v[0]) + o[2] * bf16lo(v[1]) + o[3] * bf16hi(v[1]);
 }
-template <int D, bool F32>
-__device__ __forceinline__ float dot4(const f32x4& o, const uint16_t* tile, int row, int w, int g) {
-  using C = LinCfg<D, F32>;
-  float s = 0.f;
-#pragma unroll
-  for (int k = C::NT - 1; k >= 0; --k)
-    s += dot4(o, *(const u32x2*)(tile + k * C::PART + lin_at<D, F32>(row, 2 * w + (g >> 1)) + 4 * (g & 1)));
-  return s;
-}
+template <bool F32>
+using Four = std::conditional_t<F32, f32x4, u32x2>;
 
-// ---- dk, dv --------------------------------------------------------------------
-// One workgroup to a (segment, head), D / 16 waves each for dv (state D) and dk (D^T).
-// The dk waves leave D^T at the chunk's end for the other pass.
+// ---- what a segment adds, and dg within the chunks -----------------------------------
+// One workgroup to a (segment, head), all of q, k, v, dO read once: M and D of the segment (the
+// state's part at its end, the gradient's at its start), and per chunk
+//   sum over i >= t > j of X_ij,  X_ij = T_ij (dO_i.v_j),
+// from both triangles: units of two 16 x 16 tiles, columns j in prefix sums over a row's lanes,
+// then sums over the rows i.  A row's sum over columns 0..31 counts for all t in 32..i.
 template <int D, bool F32>
-__global__ __launch_bounds__(8 * D) void k_linear_dkdv(LinArgs a) {
+__global__ __launch_bounds__(4 * D, F32 && D == 128 ? 2 : 4) void k_linear_grad_states(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[4 * C::TILE + 2 * C::TRI];
+  constexpr int UNITS = C::CH == 64 ? 6 : 2;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[4 * C::TILE];
   __shared__ LinFactors fac[2];
-  __shared__ float next_decays[64];
-  __shared__ float crossing[4][64], going[C::WAVES][64];
+  __shared__ __attribute__((aligned(16))) float to_end[2][64], to_start[2][64];  // of V in M, of dO in D
+  __shared__ __attribute__((aligned(16))) float rows[64], crossing[UNITS][32], next_decays[64];
   const int h = blockIdx.x % a.heads;
   const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
-  if (sg.count < 0) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), side = wave / C::WAVES, w = wave % C::WAVES;  // side 1: dk
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const bool need_m = !(sg.flags & 2), need_d = !(sg.flags & 1);
+  if (sg.count <= 0 || !(need_m || need_d || a.flow)) return;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
   const int hk = h / (a.heads / a.heads_k);
   uint16_t* const q = lds;
   uint16_t* const k = q + C::TILE;
   uint16_t* const v = k + C::TILE;
   uint16_t* const od = v + C::TILE;
-  uint16_t* const tri = od + C::TILE + side * C::TRI;
-  const uint16_t* const ta = side ? v : k;
-  const uint16_t* const tb = side ? od : q;
-  const uint16_t* const tc = side ? q : od;
+  const T* const qp = (const T*)a.q.p + (int64_t)sg.tok * a.q.ld + hk * D;
+  const T* const kp = (const T*)a.k.p + (int64_t)sg.tok * a.k.ld + hk * D;
+  const T* const vp = (const T*)a.v.p + (int64_t)sg.tok * a.v.ld + h * D;
+  const T* const dp = (const T*)a.d_o.p + (int64_t)sg.tok * a.d_o.ld + h * D;
+  const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
+  const int n = (sg.count + C::CH - 1) / C::CH;
+  LinState<D, F32> m, d;
+  m.zero();
+  d.zero();
+  LinFetch<D, F32> fq, fk, fv, fd;
+  auto tokens = [&](int j) { return sg.count - j * C::CH < C::CH ? sg.count - j * C::CH : C::CH; };
+  auto decay = [&](int j) {
+    return gp && lane < tokens(j) ? gp[(int64_t)(j * C::CH + lane) * a.ld_g] : 0.f;
+  };
+  auto fetch = [&](int j) {
+    const int64_t t0 = (int64_t)j * C::CH;
+    if constexpr (F32) {
+      fq.load(qp + t0 * a.q.ld, (unsigned)a.q.ld, tokens(j));
+      fk.load(kp + t0 * a.k.ld, (unsigned)a.k.ld, tokens(j));
+      fv.load(vp + t0 * a.v.ld, (unsigned)a.v.ld, tokens(j));
+      fd.load(dp + t0 * a.d_o.ld, (unsigned)a.d_o.ld, tokens(j));
+    } else {
+      const LinLane l(lane);
+      lin_load<D>(q, qp + t0 * a.q.ld, (unsigned)a.q.ld, tokens(j), w, l.lane);
+      lin_load<D>(k, kp + t0 * a.k.ld, (unsigned)a.k.ld, tokens(j), w, l.lane);
+      lin_load<D>(v, vp + t0 * a.v.ld, (unsigned)a.v.ld, tokens(j), w, l.lane);
+      lin_load<D>(od, dp + t0 * a.d_o.ld, (unsigned)a.d_o.ld, tokens(j), w, l.lane);
+    }
+  };
+  // the factors of chunk j (one wave): T's as for the pass from the last chunk to the first
+  auto factors = [&](int j, float gl) {
+    LinFactors* const f = fac + (j & 1);
+    const double before = j > 0 ? fac[~j & 1].sum : 0.0;
+    lin_factors<true>(f, nullptr, gl, tokens(j), a.scale);
+    const bool in = lane < tokens(j);
+    to_end[j & 1][lane] = in ? f->up[lane] : 0.f;
+    to_start[j & 1][lane] = in ? a.scale * exp2_wide(before + f->cs[lane]) : 0.f;
+    if (lane == 0) f->sum += before;
+  };
+  const bool mine = w == C::WAVES - 1;
+  float gl = 0.f;
+  fetch(0);
+  if (mine) {
+    factors(0, decay(0));
+    if (n > 1) gl = decay(1);
+  }
+  for (int j = 0; j < n; ++j) {
+    const int count = tokens(j);
+    if (mine) next_decays[lane] = gl;
+    if constexpr (F32) {
+      fq.store(q);
+      fk.store(k);
+      fv.store(v);
+      fd.store(od);
+    } else {
+      lin_wait_loads();
+    }
+    __syncthreads();
+    const LinFactors* const f = fac + (j & 1);
+    if (mine && j + 1 < n) factors(j + 1, next_decays[lane]);
+    if (F32 && j + 1 < n) fetch(j + 1);
+    if (a.flow) {
+      auto cross = [&](auto gated) {
+        constexpr bool GATED = decltype(gated)::value;
+        for (int u = w; u < UNITS; u += C::WAVES) {
+          const LinLane l(lane);
+          const int jt = u < 2 ? u : 2 + ((u - 2) >> 1), pair = u < 2 ? 0 : (u - 2) & 1;
+          const int src = token_row(jt, 4 * l.g);
+          float before[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int it = 2 * pair + i;
+            const f32x4 x = lin_gate<true, GATED>(lin_tri<D, F32>(v, od, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
+            const f32x4 y = lin_tri<D, F32>(k, q, it, jt, l.g, l.c);
+            const float up = GATED ? 1.f : f->up[16 * it + l.c];
+            float sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float z = x[r] * y[r] * up, p = lin_prefix16(z);
+              if (src + r >= 16 * it + l.c) sum += before[r] + from_left(p);
+              before[r] += row16_sum(z);
+            }
+            sum = group_sum(sum);
+            if (l.g == 0) crossing[u][16 * i + l.c] = sum;
+          }
+          if (pair == 0 && l.c == 0) *(f32x4*)(rows + src) = f32x4{before[0], before[1], before[2], before[3]};
+        }
+      };
+      if (f->flags & kLinGated) cross(LinBool<true>{});
+      else cross(LinBool<false>{});
+    }
+    if (need_m) {
+      m.scale(f->last);
+      const LinLane l(lane);
+      lin_tokens<D, F32, false, false>(nullptr, m, nullptr, k, v, to_end[j & 1], w, l.lane, l.g, l.c);
+    }
+    if (need_d) {
+      const LinLane l(lane);
+      lin_tokens<D, F32, true, false>(nullptr, d, nullptr, q, od, to_start[j & 1], w, l.lane, l.g, l.c);
+    }
+    __syncthreads();
+    if (!F32 && j + 1 < n) fetch(j + 1);
+    gl = mine && j + 2 < n ? decay(j + 2) : 0.f;
+    if (a.flow && w == 0) {
+      float x = 0.f;
+      if constexpr (C::CH == 64) {
+        // rows from the last one down in the lanes' order: prefix sums are sums over i >= t
+        const float below = lin_prefix(lane < 32 ? rows[63 - lane] : 0.f);
+        const int t = 63 - lane;
+        x = t < 32 ? crossing[0][t] + crossing[1][t] + crossing[2][t] + crossing[4][t]
+                   : crossing[3][t - 32] + crossing[5][t - 32] + below;
+        if (t < count) a.flow[((int64_t)sg.tok + (int64_t)j * C::CH + t) * a.heads + h] = x;
+      } else {
+        x = lane < 32 ? crossing[0][lane] + crossing[1][lane] : 0.f;
+        if (lane < count) a.flow[((int64_t)sg.tok + (int64_t)j * C::CH + lane) * a.heads + h] = x;
+      }
+    }
+  }
+  const LinLane l(lane);
+  const int64_t dd = (int64_t)D * D;
+  if (need_m) m.store(a.part[0] + ((int64_t)(sg.slot + 1) * a.heads + h) * dd, w, l.g, l.c);
+  if (need_d) d.store(a.part[1] + ((int64_t)(sg.slot - 1) * a.heads + h) * dd, w, l.g, l.c);
+  if (mine && lane == 0) {
+    const float all = exp2_wide(fac[(n - 1) & 1].sum);
+    if (need_m) a.decay[0][(int64_t)sg.slot * a.heads + h] = all;
+    if (need_d) a.decay[1][(int64_t)sg.slot * a.heads + h] = all;
+  }
+}
+
+// ---- dk, dv --------------------------------------------------------------------
+// One workgroup to a (segment, head, side): SIDE 0 dv (state D) with dg's part to the chunk's
+// end, 1 dk (D^T), which leaves D^T at the chunks' ends for the pass that follows.
+template <int D, bool F32, int SIDE>
+__device__ __forceinline__ void back_pass(const LinArgs& a, const LinSeg& sg, int h, uint16_t* lds, LinFactors* fac,
+                                          float (*going)[64], float* next_decays) {
+  using C = LinCfg<D, F32>;
+  using T = typename Tok<F32>::T;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int hk = h / (a.heads / a.heads_k);
+  uint16_t* const ta = lds;
+  uint16_t* const tb = ta + C::TILE;
+  uint16_t* const tc = tb + C::TILE;
+  uint16_t* const tri = tc + C::TILE;
   LinState<D, F32> st;
   const int64_t own = ((int64_t)sg.seq * a.heads + h) * D * D;
   const float* const from = sg.flags != 3 ? a.part[1] + ((int64_t)sg.slot * a.heads + h) * D * D
                             : a.dstate_out ? a.dstate_out + own : nullptr;
-  if (!from) st.zero();
-  else if (side) st.template load<true>(from, w, g, c);
-  else st.template load<false>(from, w, g, c);
   const int n = (sg.count + C::CH - 1) / C::CH;
-  if (n > 0) {
-    const T* const qp = (const T*)a.q.p + (int64_t)sg.tok * a.q.ld + hk * D;
-    const T* const kp = (const T*)a.k.p + (int64_t)sg.tok * a.k.ld + hk * D;
-    const T* const vp = (const T*)a.v.p + (int64_t)sg.tok * a.v.ld + h * D;
-    const T* const dp = (const T*)a.d_o.p + (int64_t)sg.tok * a.d_o.ld + h * D;
-    const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
-    // a half of the waves fetches q and k, the other v and dO
-    const LinTokens t0 = side ? a.v : a.q, t1 = side ? a.d_o : a.k;
-    const T* const p0 = side ? vp : qp;
-    const T* const p1 = side ? dp : kp;
-    LinFetch<D, F32> f0, f1;
-    auto tokens = [&](int j) { return sg.count - j * C::CH < C::CH ? sg.count - j * C::CH : C::CH; };
-    auto decay = [&](int j) {
-      return gp && lane < tokens(j) ? gp[(int64_t)(j * C::CH + lane) * a.ld_g] : 0.f;
-    };
-    auto fetch = [&](int j) {
-      const int64_t at = (int64_t)j * C::CH;
-      f0.load(p0 + at * t0.ld, (unsigned)t0.ld, tokens(j));
-      f1.load(p1 + at * t1.ld, (unsigned)t1.ld, tokens(j));
-    };
-    const bool mine = wave == 2 * C::WAVES - 1;  // the factors are this wave's, a chunk ahead
-    float gl = 0.f;
-    fetch(n - 1);
-    if (mine) {
-      lin_factors<true>(fac + ((n - 1) & 1), nullptr, decay(n - 1), tokens(n - 1), a.scale);
-      if (n > 1) gl = decay(n - 2);
+  const LinTokens at = SIDE ? a.v : a.k, bt = SIDE ? a.d_o : a.q, ct = SIDE ? a.q : a.d_o;
+  const T* const ap = (const T*)at.p + (int64_t)sg.tok * at.ld + (SIDE ? h : hk) * D;
+  const T* const bp = (const T*)bt.p + (int64_t)sg.tok * bt.ld + (SIDE ? h : hk) * D;
+  const T* const cp = (const T*)ct.p + (int64_t)sg.tok * ct.ld + (SIDE ? hk : h) * D;
+  const T* const vp = (const T*)a.v.p + (int64_t)sg.tok * a.v.ld + h * D;
+  const float* const gp = a.g ? a.g + (int64_t)sg.tok * a.ld_g + h : nullptr;
+  LinFetch<D, F32> fa, fb, fc;
+  auto tokens = [&](int j) { return sg.count - j * C::CH < C::CH ? sg.count - j * C::CH : C::CH; };
+  auto decay = [&](int j) {
+    return gp && lane < tokens(j) ? gp[(int64_t)(j * C::CH + lane) * a.ld_g] : 0.f;
+  };
+  auto fetch = [&](int j) {
+    const int64_t t0 = (int64_t)j * C::CH;
+    if constexpr (F32) {
+      fa.load(ap + t0 * at.ld, (unsigned)at.ld, tokens(j));
+      fb.load(bp + t0 * bt.ld, (unsigned)bt.ld, tokens(j));
+      fc.load(cp + t0 * ct.ld, (unsigned)ct.ld, tokens(j));
+    } else {
+      const LinLane l(lane);
+      lin_load<D>(ta, ap + t0 * at.ld, (unsigned)at.ld, tokens(j), w, l.lane);
+      lin_load<D>(tb, bp + t0 * bt.ld, (unsigned)bt.ld, tokens(j), w, l.lane);
+      lin_load<D>(tc, cp + t0 * ct.ld, (unsigned)ct.ld, tokens(j), w, l.lane);
     }
-    for (int j = n - 1; j >= 0; --j) {
-      const int count = tokens(j);
-      const int64_t tok0 = (int64_t)sg.tok + (int64_t)j * C::CH;
-      if (mine) next_decays[lane] = gl;
-      f0.store(side ? v : q);
-      f1.store(side ? od : k);
-      __syncthreads();
-      const LinFactors* const f = fac + (j & 1);
-      const int flags = f->flags;
-      if (mine && j > 0) lin_factors<true>(fac + (~j & 1), f, next_decays[lane], tokens(j - 1), a.scale);
-      if (j > 0) fetch(j - 1);
-      if (flags & kLinScale) st.scale(f->pre);
-      auto chunk = [&](auto gated) {
-        constexpr bool GATED = decltype(gated)::value;
-        // wave w < 2 TS the source tokens of row tile w
-        float cross[C::IT] = {};
-        if (w < 2 * C::TS) {
-          const int jt = w, ts = jt >> 1;
-          const LinLane l(lane);
-          const int g = l.g, c = l.c;
-          float before[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int it = 0; it < C::IT; ++it) {
-            if (!lin_in<D, F32, true>(it, ts)) continue;
-            const f32x4 x = lin_gate<true, GATED>(lin_tri<D, F32>(ta, tb, it, jt, g, c), f, a.scale, it, jt, g, c);
-            lin_put(tri, C::FRAGS, lin_frag<D, F32, true>(it, ts), jt, l.lane, x);
-            if (side && a.flow) {
-              // of source i's row of X, what comes from tokens before t = 16 it + c, if t <= i
-              const f32x4 y = lin_tri<D, F32>(k, q, it, jt, g, c);
-              const float up = GATED ? 1.f : f->up[16 * it + c];
-              float sum = 0.f;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float p = prefix16(x[r] * y[r] * up, c);
-                const float left = __shfl_up(p, 1, 16);
-                if (token_row(jt, 4 * g) + r >= 16 * it + c) sum += before[r] + (c ? left : 0.f);
-                before[r] += __shfl(p, 15, 16);
-              }
-              cross[it] += group_sum(sum);
-            }
-          }
-        }
-        LinOut<D, F32> out;
-        {
-          const LinLane l(lane);
-          out.read(st, ta, l.g, l.c);
-        }
-        if (a.flow) {
-          const LinLane l(lane);
-          const int g = l.g, c = l.c;
-          if (side) {
-            if (w == 0 && lane == 0) a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] = f->s;
-            float* const dump =
-                a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
-#pragma unroll
-            for (int mt = 0; mt < C::MT; ++mt) *(f32x4*)(dump + mt * 256) = st.m[mt];
-            if (w < 4 && g == 0)
-#pragma unroll
-              for (int it = 0; it < C::IT; ++it) crossing[w][16 * it + c] = cross[it];
-          } else {
-#pragma unroll
-            for (int it = 0; it < C::IT; ++it) {
-              const int t = 16 * it + c;
-              const float x = group_sum(dot4<D, F32>(out.o[it], v, t, w, g));
-              if (g == 0) going[w][t] = t < count ? x * f->up[t] : 0.f;
-            }
-          }
-        }
-        if (GATED) {
-          out.scale(f, c);
-          st.scale(f->last);
-        }
-        __syncthreads();
-        const LinLane lt(lane);
-        lin_tokens<D, F32, true, true>(&out, st, tri, tb, tc, f, w, lt.lane, lt.g, lt.c);
-        const LinLane l(lane);
-        if (!GATED) out.scale(f, l.c);
-        if (!side) {
-          out.store((T*)a.dv + tok0 * a.ld_dv + h * D, (unsigned)a.ld_dv, count, w, l.g, l.c);
-        } else if (a.dk_part) {
-          out.store(a.dk_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, l.g, l.c);
-        } else {
-          out.store((T*)a.dk + tok0 * a.ld_dk + hk * D, (unsigned)a.ld_dk, count, w, l.g, l.c);
-        }
-      };
-      if (flags & kLinGated) chunk(LinBool<true>{});
-      else chunk(LinBool<false>{});
-      if (a.flow && wave == 0) {
-        float x = 0.f, y = 0.f;
-        if (lane < C::CH) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x += crossing[i][lane];
-#pragma unroll
-          for (int i = 0; i < C::WAVES; ++i) y += going[i][lane];
-        }
-        float all = y;
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-          const float o = __shfl_up(all, m, 64);
-          if (lane >= m) all += o;
-        }
-        const float up = __shfl_up(all, 1, 64);
-        if (lane < count) a.flow[(tok0 + lane) * a.heads + h] = x + (lane ? up : 0.f);
-      }
-      gl = mine && j > 1 ? decay(j - 2) : 0.f;
-      __syncthreads();
-    }
-    st.scale(fac[0].end);
+  };
+  const bool mine = w == C::WAVES - 1;  // the factors are this wave's, a chunk ahead
+  float gl = 0.f;
+  if (n > 0) fetch(n - 1);
+  {
+    const LinLane l(lane);
+    if (!from) st.zero();
+    else st.template load<SIDE != 0>(from, w, l.g, l.c);
   }
-  if ((sg.flags & 1) && a.dstate_in && !side) st.store(a.dstate_in + own, w, g, c);
+  if (n > 0 && mine) {
+    lin_factors<true>(fac + ((n - 1) & 1), nullptr, decay(n - 1), tokens(n - 1), a.scale);
+    if (n > 1) gl = decay(n - 2);
+  }
+  for (int j = n - 1; j >= 0; --j) {
+    const int count = tokens(j);
+    const int64_t tok0 = (int64_t)sg.tok + (int64_t)j * C::CH;
+    if (mine) next_decays[lane] = gl;
+    if constexpr (F32) {
+      fa.store(ta);
+      fb.store(tb);
+      fc.store(tc);
+    } else {
+      lin_wait_loads();
+    }
+    __syncthreads();
+    const LinFactors* const f = fac + (j & 1);
+    const int flags = f->flags;
+    if (mine && j > 0) lin_factors<true>(fac + (~j & 1), f, next_decays[lane], tokens(j - 1), a.scale);
+    if (F32 && j > 0) fetch(j - 1);
+    if (flags & kLinScale) st.scale(f->pre);
+    auto chunk = [&](auto gated) {
+      constexpr bool GATED = decltype(gated)::value;
+      // v's elements of a lane's outputs are on their way meanwhile
+      Four<F32> ve[C::IT];
+      if (SIDE == 0 && a.flow) {
+        const LinLane l(lane);
+#pragma unroll
+        for (int it = 0; it < C::IT; ++it) {
+          const int row = 16 * it + l.c < count ? 16 * it + l.c : count - 1;
+          ve[it] = *(const Four<F32>*)(vp + ((int64_t)j * C::CH + row) * a.v.ld + 16 * w + 4 * l.g);
+        }
+      }
+      if (SIDE == 1 && a.flow) {
+        const LinLane l(lane);
+        if (w == 0 && lane == 0) a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] = f->s;
+        float* const dump = a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) *(f32x4*)(dump + mt * 256) = st.m[mt];
+      }
+      for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
+        const LinLane l(lane);
+        const int fr = t >> 1;
+        const int it = C::CH == 32 ? fr : fr < 4 ? fr >> 1 : fr - 2, ts = C::CH == 32 ? 0 : fr < 4 ? fr & 1 : 1;
+        const int jt = 2 * ts + (t & 1);
+        const f32x4 x = lin_gate<true, GATED>(lin_tri<D, F32>(ta, tb, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
+        lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
+      }
+      LinOut<D, F32> out;
+      {
+        const LinLane l(lane);
+        out.read(st, ta, l.g, l.c);
+      }
+      if (SIDE == 0 && a.flow) {
+        const LinLane l(lane);
+#pragma unroll
+        for (int it = 0; it < C::IT; ++it) {
+          const int t = 16 * it + l.c;
+          const float x = group_sum(dot4(out.o[it], ve[it]));
+          if (l.g == 0) going[w][t] = t < count ? x * f->up[t] : 0.f;
+        }
+      }
+      if (GATED) {
+        const LinLane l(lane);
+        out.scale(f, l.c);
+        st.scale(f->last);
+      }
+      __syncthreads();
+      const LinLane lt(lane);
+      lin_tokens<D, F32, true, true>(&out, st, tri, tb, tc, f->dn, w, lt.lane, lt.g, lt.c);
+      const LinLane l(lane);
+      if (!GATED) out.scale(f, l.c);
+      if (SIDE == 0) {
+        out.store((T*)a.dv + tok0 * a.ld_dv + h * D, (unsigned)a.ld_dv, count, w, l.g, l.c);
+      } else if (a.dk_part) {
+        out.store(a.dk_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, l.g, l.c);
+      } else {
+        out.store((T*)a.dk + tok0 * a.ld_dk + hk * D, (unsigned)a.ld_dk, count, w, l.g, l.c);
+      }
+    };
+    if (flags & kLinGated) chunk(LinBool<true>{});
+    else chunk(LinBool<false>{});
+    if (SIDE == 0 && a.flow && w == 0) {
+      float y = 0.f;
+      if (lane < C::CH)
+#pragma unroll
+        for (int i = 0; i < C::WAVES; ++i) y += going[i][lane];
+      const float up = __shfl_up(lin_prefix(y), 1, 64);  // of the tokens before
+      if (lane < count) a.flow[(tok0 + lane) * a.heads + h] += lane ? up : 0.f;
+    }
+    __syncthreads();
+    if (!F32 && j > 0) fetch(j - 1);
+    gl = mine && j > 1 ? decay(j - 2) : 0.f;
+  }
+  if (SIDE == 0 && (sg.flags & 1) && a.dstate_in) {
+    const LinLane l(lane);
+    if (n > 0) st.scale(fac[0].end);
+    st.store(a.dstate_in + own, w, l.g, l.c);
+  }
+}
+
+template <int D, bool F32>
+__global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dkdv(LinArgs a) {
+  using C = LinCfg<D, F32>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[3 * C::TILE + C::TRI];
+  __shared__ LinFactors fac[2];
+  __shared__ float going[C::WAVES][64], next_decays[64];
+  const int h = blockIdx.x % a.heads;
+  const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
+  if (sg.count < 0) return;
+  if (blockIdx.y == 0) back_pass<D, F32, 0>(a, sg, h, lds, fac, going, next_decays);
+  else if (sg.count > 0) back_pass<D, F32, 1>(a, sg, h, lds, fac, going, next_decays);
 }
 
 // ---- dq, dg ----------------------------------------------------------------------
@@ -219,7 +361,6 @@ template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
-  using Four = std::conditional_t<F32, f32x4, u32x2>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[3 * C::TILE + C::TRI];
   __shared__ LinFactors fac[2];
   __shared__ float next_decays[64];
@@ -289,15 +430,20 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
     if (flags & kLinScale) st.scale(f->pre);
     auto chunk = [&](auto gated) {
       constexpr bool GATED = decltype(gated)::value;
-      // q's elements of a lane's outputs are on their way meanwhile
-      Four qe[C::IT];
+      // q's elements of a lane's outputs and D^T are on their way meanwhile
+      f32x4 de[C::MT];
+      Four<F32> qe[C::IT];
       if (a.flow) {
         const LinLane l(lane);
 #pragma unroll
         for (int it = 0; it < C::IT; ++it) {
           const int row = 16 * it + l.c < count ? 16 * it + l.c : count - 1;
-          qe[it] = *(const Four*)(qp + ((int64_t)j * C::CH + row) * a.q.ld + 16 * w + 4 * l.g);
+          qe[it] = *(const Four<F32>*)(qp + ((int64_t)j * C::CH + row) * a.q.ld + 16 * w + 4 * l.g);
         }
+        const float* const dump =
+            a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) de[mt] = *(const f32x4*)(dump + mt * 256);
       }
       for (int t = w; t < 2 * C::FRAGS; t += C::WAVES) {
         const LinLane l(lane);
@@ -308,6 +454,15 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
             lin_gate<false, GATED>(lin_tri<D, F32>(od, v, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
         lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
       }
+      if (a.flow) {
+        float e = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][r], de[mt][r], e);
+        e = lin_prefix(e);
+        if (lane == 63) through[w] = e;
+      }
       LinOut<D, F32> out;
       {
         const LinLane l(lane);
@@ -315,18 +470,6 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
       }
       if (a.flow) {
         const LinLane l(lane);
-        const float* const dump =
-            a.d_dump + (((int64_t)sg.chunk0 + j) * a.heads + h) * D * D + w * (C::MT * 256) + 4 * l.lane;
-        float e = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt) {
-          const f32x4 x = *(const f32x4*)(dump + mt * 256);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][r], x[r], e);
-        }
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) e += __shfl_xor(e, m, 64);
-        if (lane == 0) through[w] = e;
 #pragma unroll
         for (int it = 0; it < C::IT; ++it) {
           const float x = group_sum(dot4(out.o[it], qe[it]));
@@ -339,7 +482,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
       }
       __syncthreads();
       const LinLane lt(lane);
-      lin_tokens<D, F32, false, true>(&out, st, tri, v, k, f, w, lt.lane, lt.g, lt.c);
+      lin_tokens<D, F32, false, true>(&out, st, tri, v, k, f->dn, w, lt.lane, lt.g, lt.c);
       const LinLane l(lane);
       if (!GATED) out.scale(f, l.c);
       if (a.o_part) out.store(a.o_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, l.g, l.c);
@@ -348,27 +491,23 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
     if (flags & kLinGated) chunk(LinBool<true>{});
     else chunk(LinBool<false>{});
     if (a.flow && w == 0) {
+      // tokens from the last one down in the lanes' order: prefix sums are sums over i >= t
+      const int t = 63 - lane;
       float x = 0.f, e = 0.f;
 #pragma unroll
       for (int i = 0; i < C::WAVES; ++i) {
-        x += lane < C::CH ? coming[i][lane] : 0.f;
+        x += t < C::CH ? coming[i][t] : 0.f;
         e += through[i];
       }
-#pragma unroll
-      for (int m = 1; m < 64; m *= 2) {
-        const float o = __shfl_down(x, m, 64);
-        if (lane + m < 64) x += o;
-      }
+      x = lin_prefix(x);
       // M at the chunk's start, D at its end and the decay between
       const double power = f->s + a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] + f->cs[63];
-      const float d = lane < count ? a.flow[(tok0 + lane) * a.heads + h] + x + e * exp2_wide(power) : 0.f;
+      const float d = t < count ? a.flow[(tok0 + t) * a.heads + h] + x + e * exp2_wide(power) : 0.f;
       if (a.ld_g) {
-        if (lane < count) a.dg[(tok0 + lane) * a.heads + h] = d;
+        if (t < count) a.dg[(tok0 + t) * a.heads + h] = d;
       } else {
-        float s = d;
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) s += __shfl_xor(s, m, 64);
-        if (lane == 0) a.dg[((int64_t)sg.chunk0 + j) * a.heads + h] = s;
+        const float s = lin_prefix(d);
+        if (lane == 63) a.dg[((int64_t)sg.chunk0 + j) * a.heads + h] = s;
       }
     }
     __syncthreads();
@@ -411,7 +550,7 @@ __global__ __launch_bounds__(256) void k_linear_groups(const float* x, T* y, int
 __global__ __launch_bounds__(256) void k_linear_decay_sum(const float* sums, LinSeqs sq, int heads, float* dg) {
   __shared__ double red[4];
   const int2 range = sq.segs || sq.n_seq == 0 ? int2{0, 0} : lin_range(sq);
-  const int chunks = sq.segs ? sq.of_seq[sq.n_seq + 1].x : lin_chunks(sq, range.y - range.x);
+  const int chunks = sq.segs ? sq.all->z : lin_chunks(sq, range.y - range.x);
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < chunks; i += 256) s += (double)sums[i * heads + blockIdx.x];
 #pragma unroll
@@ -422,8 +561,16 @@ __global__ __launch_bounds__(256) void k_linear_decay_sum(const float* sums, Lin
 }
 
 template <int D>
+hipError_t grad_states_any(const LinArgs& a, bool f32, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(4 * D);
+  if (f32) hipLaunchKernelGGL((k_linear_grad_states<D, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((k_linear_grad_states<D, false>), grid, blk, 0, st, a);
+  return hipGetLastError();
+}
+
+template <int D>
 hipError_t dkdv_any(const LinArgs& a, bool f32, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads)), blk(8 * D);
+  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads), 2), blk(4 * D);
   if (f32) hipLaunchKernelGGL((k_linear_dkdv<D, true>), grid, blk, 0, st, a);
   else hipLaunchKernelGGL((k_linear_dkdv<D, false>), grid, blk, 0, st, a);
   return hipGetLastError();
@@ -438,6 +585,10 @@ hipError_t dq_any(const LinArgs& a, bool f32, hipStream_t st) {
 }
 
 }  // namespace
+
+hipError_t launch_linear_grad_states(const LinArgs& a, int d, bool f32, hipStream_t st) {
+  return d == 128 ? grad_states_any<128>(a, f32, st) : grad_states_any<64>(a, f32, st);
+}
 
 hipError_t launch_linear_dkdv(const LinArgs& a, int d, bool f32, hipStream_t st) {
   return d == 128 ? dkdv_any<128>(a, f32, st) : dkdv_any<64>(a, f32, st);
