@@ -46,13 +46,17 @@ struct LinPlan {
 };
 
 // Upper bounds over every way n tokens can fall into n_seq sequences.
-LinPlan lin_plan(const zm_linear_desc* d, int64_t n) {
+LinPlan lin_plan(const zm_linear_desc* d, int64_t n, bool back = false) {
   LinPlan p;
   p.chunk = d->io_dtype == ZM_F32 ? 32 : 64;
   const int64_t ragged = (int64_t)(p.chunk - 1) * d->n_seq;
   p.n_chunks = (n + ragged) / p.chunk;
   // about this many workgroups in all
+#ifdef BT
+  const int64_t target = back ? BT : 2 * kTargetWgs;
+#else
   const int64_t target = 2 * kTargetWgs;
+#endif
   int64_t seg = ceil_div(p.n_chunks * d->heads, target);
   if (seg < 1) seg = 1;
   p.seg_chunks = (int)seg;
@@ -98,7 +102,7 @@ void common_ws(LinArgs& a, Carve& c, const zm_linear_desc* d, const LinPlan& p, 
   s.longest_first = (int64_t)p.n_segs * d->heads > 2 * kTargetWgs && p.n_segs <= kLinSorted;
   s.seg_tokens = p.seg_chunks * p.chunk;
   s.chunk = p.chunk;
-  if (d->n_seq > 1) {
+  if (d->n_seq > kLinWaveSeqs) {
     s.segs = c.take<LinSeg>(p.slots + d->n_seq);
     s.by_slot = c.take<int>(p.slots);
     s.all = c.take<int4>(1);
@@ -251,7 +255,7 @@ int zm_linear_attention_backward_workspace_size(const zm_linear_desc* desc, int6
   ZM_TRY(check_counts(desc, n));
   LinArgs a{};
   float* sums;
-  *bytes = backward_ws(a, desc, lin_plan(desc, n), n, nullptr, nullptr, &sums);
+  *bytes = backward_ws(a, desc, lin_plan(desc, n, true), n, nullptr, nullptr, &sums);
   return ZM_OK;
 }
 
@@ -281,7 +285,7 @@ int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const in
     }
   }
   ZM_TRY(check_apart(dstate_in, {state_in}));
-  const LinPlan p = lin_plan(desc, n);
+  const LinPlan p = lin_plan(desc, n, true);
   LinArgs a{};
   float* sums;
   ZM_TRY(check_workspace(workspace, workspace_bytes, backward_ws(a, desc, p, n, offsets, workspace, &sums)));
@@ -310,10 +314,7 @@ int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const in
     if (p.split) ZM_HIP(launch_linear_join(a, d, true, st));
     ZM_HIP(launch_linear_dkdv(a, d, f32, st));
     if (n > 0) ZM_HIP(launch_linear_dq(a, d, f32, st));
-    if (n > 0 && a.o_part) {
-      ZM_HIP(launch_linear_groups(a.o_part, dq, ld_dq, a, d, f32, st));
-      ZM_HIP(launch_linear_groups(a.dk_part, dk, ld_dk, a, d, f32, st));
-    }
+    if (n > 0 && a.o_part) ZM_HIP(launch_linear_groups(a, d, f32, st));
   }
   if (dg && one) ZM_HIP(launch_linear_decay_sum(sums, a.sq, desc->heads, dg, st));
   return ZM_OK;

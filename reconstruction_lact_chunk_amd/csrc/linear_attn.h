@@ -90,11 +90,12 @@ struct LinSeg {
   int segs;         // of its sequence
   int pad;
 };
-constexpr int kLinSorted = 512;  // segments that the table puts in order
+constexpr int kLinWaveSeqs = 64;  // sequences that need no table
+constexpr int kLinSorted = 512;   // segments that the table puts in order
 
 struct LinSeqs {
   const int* offsets;   // [n_seq + 1] or null: one sequence of all n tokens
-  LinSeg* segs;         // null without a table (one sequence)
+  LinSeg* segs;         // null without a table (up to kLinWaveSeqs sequences)
   int* by_slot;         // [slots] the segment, -1: unused
   int4* all;            // {first token, end, chunks, -} of all sequences together
   int n, n_seq;
@@ -139,16 +140,6 @@ struct LinArgs {
   float* dg;           // [n][heads], or, with ld_g = 0, the chunks' sums [chunks][heads]
 };
 
-// First token and end of all sequences together.
-__device__ __forceinline__ int2 lin_range(const LinSeqs& s) {
-  if (s.segs) return int2{s.all->x, s.all->y};
-  int a = 0, e = s.n;
-  if (s.offsets) {
-    a = clampi(s.offsets[0], 0, s.n);
-    e = clampi(s.offsets[1], a, s.n);
-  }
-  return int2{a, e};
-}
 // Segments of a sequence of len tokens, and its chunks.
 __device__ __forceinline__ int lin_segs(const LinSeqs& s, int len) {
   return len > 0 ? (int)(((int64_t)len + s.seg_tokens - 1) / s.seg_tokens) : 1;
@@ -157,37 +148,134 @@ __device__ __forceinline__ int lin_chunks(const LinSeqs& s, int len) {
   return (int)(((int64_t)len + s.chunk - 1) / s.chunk);
 }
 
-__device__ __forceinline__ LinSeg lin_seg(const LinSeqs& s, int si) {
-  if (s.segs) return s.segs[si];
-  const int2 r = lin_range(s);
-  const int a = r.x, len = r.y - r.x, segs = lin_segs(s, len);
-  LinSeg g;
-  if (si >= segs) {
-    g.count = -1;
+// Sums, and the largest, over the lanes up to each one: shifts within 16 lanes, then the
+// rows' last lanes to the next row and to the upper half.  No addresses, as exchanges
+// through LDS take them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lin_add_from(int x) {
+  return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lin_max_from(int x) {
+  const int o = __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);  // of nothing: 0
+  return o > x ? o : x;
+}
+__device__ __forceinline__ int lin_prefix(int x) {
+  x = lin_add_from<0x111, 0xf>(x);  // one lane on
+  x = lin_add_from<0x112, 0xf>(x);
+  x = lin_add_from<0x114, 0xf>(x);
+  x = lin_add_from<0x118, 0xf>(x);
+  x = lin_add_from<0x142, 0xa>(x);  // lane 15 to row 1, 47 to row 3
+  return lin_add_from<0x143, 0xc>(x);  // lane 31 to rows 2 and 3
+}
+__device__ __forceinline__ int lin_prefix_max(int x) {  // x >= 0
+  x = lin_max_from<0x111, 0xf>(x);
+  x = lin_max_from<0x112, 0xf>(x);
+  x = lin_max_from<0x114, 0xf>(x);
+  x = lin_max_from<0x118, 0xf>(x);
+  x = lin_max_from<0x142, 0xa>(x);
+  return lin_max_from<0x143, 0xc>(x);
+}
+
+// Up to 64 sequences, a lane to each: what the table holds of more of them.  Every lane of a
+// wave calls this.
+struct LinWave {
+  int begin, len, segs;    // of the lane's sequence; none past the last
+  int chunk0, slot0;       // before it
+  int first, end;          // of all sequences together
+  int chunks;              // of all
+
+  __device__ __forceinline__ explicit LinWave(const LinSeqs& s) {
+    const int lane = threadIdx.x & 63;
+    const bool in = lane < s.n_seq;
+    int e = 0;
+    first = 0;
+    if (s.offsets) {
+      first = clampi(s.offsets[0], 0, s.n);
+      if (in) e = clampi(s.offsets[lane + 1], 0, s.n);
+    } else if (in) {
+      e = s.n;
+    }
+    if (e < first) e = first;
+    e = lin_prefix_max(e);  // nondecreasing
+    const int left = __shfl_up(e, 1, 64);
+    begin = lane ? left : first;
+    len = in ? e - begin : 0;
+    segs = in ? lin_segs(s, len) : 0;
+    const int c = lin_chunks(s, len), k = segs > 1 ? segs : 0;
+    const int cs = lin_prefix(c);
+    chunk0 = cs - c;
+    slot0 = lin_prefix(k) - k;
+    end = __builtin_amdgcn_readlane(e, 63);
+    chunks = __builtin_amdgcn_readlane(cs, 63);
+  }
+  // Segment i of lane b's sequence, the same in every lane.
+  __device__ __forceinline__ LinSeg get(const LinSeqs& s, int b, int i) const {
+    LinSeg g;
+    const int k = __builtin_amdgcn_readlane(segs, b), l = __builtin_amdgcn_readlane(len, b);
+    const int64_t from = (int64_t)i * s.seg_tokens;
+    g.tok = __builtin_amdgcn_readlane(begin, b) + (int)from;
+    g.count = l - from < s.seg_tokens ? (int)(l - from) : s.seg_tokens;
+    g.seq = b;
+    g.flags = (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0);
+    g.chunk0 = __builtin_amdgcn_readlane(chunk0, b) + (int)(from / s.chunk);
+    g.slot = __builtin_amdgcn_readlane(slot0, b) + i;
+    g.segs = k;
+    g.pad = 0;
     return g;
   }
-  const int64_t at = (int64_t)si * s.seg_tokens;
-  g.tok = a + (int)at;
-  g.count = len - at < s.seg_tokens ? (int)(len - at) : s.seg_tokens;
-  g.seq = 0;
-  g.flags = (si == 0 ? 1 : 0) | (si == segs - 1 ? 2 : 0);
-  g.chunk0 = (int)(at / s.chunk);
-  g.slot = si;
-  g.segs = segs;
-  return g;
+};
+
+// First token and end of all sequences together, and their chunks.
+__device__ __forceinline__ int4 lin_all(const LinSeqs& s) {
+  if (s.segs) return *s.all;
+  if (s.n_seq == 0) return int4{0, 0, 0, 0};
+  const LinWave w(s);
+  return int4{w.first, w.end, w.chunks, 0};
+}
+
+// Segment si: the full ones (which are a sequence's but its last) in the order of the tokens,
+// then the others, longest first, so that long ones do not end last where there are more
+// workgroups than run at once.
+__device__ __forceinline__ LinSeg lin_seg(const LinSeqs& s, int si) {
+  if (s.segs) return s.segs[si];
+  const LinWave w(s);
+  const int lane = threadIdx.x & 63;
+  LinSeg none;
+  none.count = -1;
+  const int full = w.segs > 0 ? w.segs - 1 : 0, before = lin_prefix(full) - full;
+  const int all = __builtin_amdgcn_readlane(before + full, 63);
+  if (si < all) {
+    const uint64_t at = __ballot(full > 0 && before <= si && si < before + full);
+    const int b = __builtin_ctzll(at);
+    return w.get(s, b, si - __builtin_amdgcn_readlane(before, b));
+  }
+  si -= all;
+  if (si >= s.n_seq) return none;
+  const int rest = w.segs > 0 ? w.len - full * s.seg_tokens : -1;  // len < 2^31
+  int rank = 0;
+  for (int i = 0; i < s.n_seq; ++i) {
+    const int o = __builtin_amdgcn_readlane(rest, i);
+    rank += o > rest || (o == rest && i < lane);
+  }
+  const uint64_t at = __ballot(lane < s.n_seq && rank == si);
+  const int b = __builtin_ctzll(at);
+  return w.get(s, b, __builtin_amdgcn_readlane(full, b));
 }
 // The segment whose state is in a slot: of sequences of several segments only.
 __device__ __forceinline__ LinSeg lin_slot(const LinSeqs& s, int slot) {
   LinSeg g;
+  g.count = -1;
   if (s.segs) {
     const int i = s.by_slot[slot];
-    g.count = -1;
     if (i >= 0) g = s.segs[i];
-  } else {
-    g = lin_seg(s, slot);
-    if (g.count >= 0 && g.segs < 2) g.count = -1;
+    return g;
   }
-  return g;
+  const LinWave w(s);
+  const uint64_t at = __ballot(w.segs > 1 && w.slot0 <= slot && slot < w.slot0 + w.segs);
+  if (at == 0) return g;
+  const int b = __builtin_ctzll(at);
+  return w.get(s, b, slot - __builtin_amdgcn_readlane(w.slot0, b));
 }
 
 // x as three bf16 parts, each what 8 bits hold of what the ones before leave, cut off: the sum
@@ -332,8 +420,6 @@ __device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_columns(const uint16_t*
   return lin_read_tr<D, F32>(t, ts, 2 * w + ((c & 3) >> 1), 4 * (c & 1), g, c);
 }
 
-// Sums over the lanes up to each one: shifts within 16 lanes, then the rows' last lanes to
-// the next row and to the upper half.  No addresses, as exchanges through LDS take them.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double lin_add_from(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
@@ -619,7 +705,7 @@ __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>
 }
 
 // ---- launchers ----------------------------------------------------------------
-// The table of segments (n_seq > 1).
+// The table of segments (n_seq > kLinWaveSeqs).
 hipError_t launch_linear_table(const LinSeqs& s, hipStream_t st);
 // What each segment of a sequence adds to the state, all but its last.
 hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, hipStream_t st);
@@ -631,9 +717,8 @@ hipError_t launch_linear_out(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_grad_states(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_dkdv(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_dq(const LinArgs& a, int d, bool f32, hipStream_t st);
-// y [n][heads_k][d] from x [n][heads][d] summed over the value heads of a key head.
-hipError_t launch_linear_groups(const float* x, void* y, int64_t ld_y, const LinArgs& a, int d, bool f32,
-                                hipStream_t st);
+// dq and dk from o_part and dk_part, summed over the value heads of a key head.
+hipError_t launch_linear_groups(const LinArgs& a, int d, bool f32, hipStream_t st);
 // dg [heads] from the chunks' sums.
 hipError_t launch_linear_decay_sum(const float* sums, const LinSeqs& s, int heads, float* dg, hipStream_t st);
 

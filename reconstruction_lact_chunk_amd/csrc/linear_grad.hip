@@ -517,13 +517,15 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
 }
 
 // ---- sums ------------------------------------------------------------------------
-// Eight elements a thread: the value heads of a key head in order.  Rows outside the
-// sequences are left as they are.
+// Eight elements a thread: the value heads of a key head in order, blockIdx.y 0 dq, 1 dk.
+// Rows outside the sequences are left as they are.
 template <typename T>
-__global__ __launch_bounds__(256) void k_linear_groups(const float* x, T* y, int64_t ldy, LinSeqs sq, int heads,
-                                                       int heads_k, int d) {
-  const int per = heads_k * d / 8, rep = heads / heads_k;
-  const int2 range = lin_range(sq);
+__global__ __launch_bounds__(256) void k_linear_groups(LinArgs a, int d) {
+  const int heads = a.heads, per = a.heads_k * d / 8, rep = heads / a.heads_k;
+  const float* const x = blockIdx.y ? a.dk_part : a.o_part;
+  T* const y = (T*)(blockIdx.y ? a.dk : a.o);
+  const int64_t ldy = blockIdx.y ? a.ld_dk : a.ld_o;
+  const int4 range = lin_all(a.sq);
   const int64_t all = (int64_t)(range.y - range.x) * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const int64_t t = range.x + i / per;
@@ -549,8 +551,7 @@ __global__ __launch_bounds__(256) void k_linear_groups(const float* x, T* y, int
 // A workgroup to a head; the chunks' sums in 64 bits, always in the same order.
 __global__ __launch_bounds__(256) void k_linear_decay_sum(const float* sums, LinSeqs sq, int heads, float* dg) {
   __shared__ double red[4];
-  const int2 range = sq.segs || sq.n_seq == 0 ? int2{0, 0} : lin_range(sq);
-  const int chunks = sq.segs ? sq.all->z : lin_chunks(sq, range.y - range.x);
+  const int chunks = lin_all(sq).z;
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < chunks; i += 256) s += (double)sums[i * heads + blockIdx.x];
 #pragma unroll
@@ -598,14 +599,12 @@ hipError_t launch_linear_dq(const LinArgs& a, int d, bool f32, hipStream_t st) {
   return d == 128 ? dq_any<128>(a, f32, st) : dq_any<64>(a, f32, st);
 }
 
-hipError_t launch_linear_groups(const float* x, void* y, int64_t ld_y, const LinArgs& a, int d, bool f32,
-                                hipStream_t st) {
+hipError_t launch_linear_groups(const LinArgs& a, int d, bool f32, hipStream_t st) {
   int64_t blocks = ceil_div((int64_t)a.sq.n * (a.heads_k * d / 8), 256);
-  if (blocks > 8 * kTargetWgs) blocks = 8 * kTargetWgs;
-  if (f32) hipLaunchKernelGGL((k_linear_groups<float>), dim3((unsigned)blocks), dim3(256), 0, st, x, (float*)y, ld_y,
-                              a.sq, a.heads, a.heads_k, d);
-  else hipLaunchKernelGGL((k_linear_groups<uint16_t>), dim3((unsigned)blocks), dim3(256), 0, st, x, (uint16_t*)y, ld_y,
-                          a.sq, a.heads, a.heads_k, d);
+  if (blocks > 4 * kTargetWgs) blocks = 4 * kTargetWgs;
+  const dim3 grid((unsigned)blocks, 2);
+  if (f32) hipLaunchKernelGGL((k_linear_groups<float>), grid, dim3(256), 0, st, a, d);
+  else hipLaunchKernelGGL((k_linear_groups<uint16_t>), grid, dim3(256), 0, st, a, d);
   return hipGetLastError();
 }
 
