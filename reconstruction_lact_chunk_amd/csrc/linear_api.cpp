@@ -40,24 +40,30 @@ int check_ptr(const void* p, size_t align) { return p && aligned(p, align) ? ZM_
 
 struct LinPlan {
   int64_t n_chunks;
-  int n_segs, n_slots, seg_chunks, chunk;
+  int n_segs, n_slots, n_split, seg_chunks, chunk;
   int64_t slots;      // states of segments that the workspace has place for
+  int64_t splits;     // sequences of several segments, the same
   bool split;         // a sequence can have several segments
 };
 
 // Upper bounds over every way n tokens can fall into n_seq sequences.
-LinPlan lin_plan(const zm_linear_desc* d, int64_t n, bool back = false) {
+LinPlan lin_plan(const zm_linear_desc* d, int64_t n) {
   LinPlan p;
   p.chunk = d->io_dtype == ZM_F32 ? 32 : 64;
   const int64_t ragged = (int64_t)(p.chunk - 1) * d->n_seq;
   p.n_chunks = (n + ragged) / p.chunk;
-  // about this many workgroups in all
-#ifdef BT
-  const int64_t target = back ? BT : 2 * kTargetWgs;
-#else
+  // About this many workgroups in all, two to a compute unit.  8 heads of 128, bf16, us at
+  // 256 / 512 / 1024: 10992 tokens 71 / 69 / 83, 40000 tokens 194 / 162 / 190.
   const int64_t target = 2 * kTargetWgs;
-#endif
   int64_t seg = ceil_div(p.n_chunks * d->heads, target);
+  // Segments of one chunk make the join long: 3000 tokens (47 chunks) of 8 heads 42 us, in
+  // segments of two 36; 10000 of 2 heads 55 and 43; 1374 of 8 heads 31 and 34.
+  const int64_t each = d->n_seq > 0 ? p.n_chunks / d->n_seq : 0;
+  if (seg < 2 && each > 32) seg = 2;
+  if (seg < each / 128) seg = each / 128;
+  // Two chunks one after the other take less than two launches more: 128 tokens 18 us against
+  // 24, 256 tokens 27 against 24.
+  if (n <= 2 * p.chunk) seg = p.n_chunks;
   if (seg < 1) seg = 1;
   p.seg_chunks = (int)seg;
   const int64_t tokens = seg * p.chunk;
@@ -65,15 +71,17 @@ LinPlan lin_plan(const zm_linear_desc* d, int64_t n, bool back = false) {
   const int64_t full = n / tokens;
   p.split = n > tokens;
   p.n_segs = (int)((p.split ? full : 0) + d->n_seq);
-  p.n_slots = p.split ? (int)(full + (full < d->n_seq ? full : d->n_seq)) : 0;
+  p.n_split = p.split ? (int)(full < d->n_seq ? full : d->n_seq) : 0;
+  p.n_slots = p.split ? (int)full + p.n_split : 0;
   // Place for the full segments and one more of each sequence that has some.  full falls
   // where seg steps up, and with it split can; neither n / chunk nor target / heads is
   // passed, and split needs n (target - heads) > heads (ragged - chunk + 1), so that the
   // workspace never decreases with n.
-  p.slots = 0;
+  p.slots = p.splits = 0;
   if (n > p.chunk && n * (target - d->heads) > d->heads * (ragged - p.chunk + 1)) {
     const int64_t most = target / d->heads, all = n / p.chunk, room = all < most ? all : most;
-    p.slots = room + (room < d->n_seq ? room : d->n_seq);
+    p.splits = room < d->n_seq ? room : d->n_seq;
+    p.slots = room + p.splits;
   }
   return p;
 }
@@ -98,13 +106,15 @@ void common_ws(LinArgs& a, Carve& c, const zm_linear_desc* d, const LinPlan& p, 
   s.n_seq = d->n_seq;
   s.n_segs = p.n_segs;
   s.n_slots = p.n_slots;
-  // 61 sequences of 4 to 24 chunks, 16 heads: see the table's kernel
+  s.n_split = p.n_split;
+  // 61 sequences of 4 to 24 chunks, 16 heads: 353 -> 291 us
   s.longest_first = (int64_t)p.n_segs * d->heads > 2 * kTargetWgs && p.n_segs <= kLinSorted;
   s.seg_tokens = p.seg_chunks * p.chunk;
   s.chunk = p.chunk;
   if (d->n_seq > kLinWaveSeqs) {
     s.segs = c.take<LinSeg>(p.slots + d->n_seq);
     s.by_slot = c.take<int>(p.slots);
+    s.by_split = c.take<int>(p.splits);
     s.all = c.take<int4>(1);
   }
   for (int i = 0; i < ways && p.slots > 0; ++i) {
@@ -141,8 +151,8 @@ size_t backward_ws(LinArgs& a, const zm_linear_desc* d, const LinPlan& p, int64_
 
 int check_counts(const zm_linear_desc* d, int64_t n) {
   if (n < 0 || n > kMaxLinTokens || (d->n_seq == 0 && n > 0)) return ZM_ERR_INVALID_ARG;
-  // the largest grid: a block of 512 threads to each segment and head (the join's 32 to a slot
-  // and head are at most 32 times 1024 + heads)
+  // the largest grid: a block of 512 threads to each segment and head (the join's 32 to a
+  // split sequence and head are at most 32 times 512)
   if ((int64_t)lin_plan(d, n).n_segs * d->heads * 2 > kMaxLinBlocks) return ZM_ERR_UNSUPPORTED;
   return ZM_OK;
 }
@@ -255,7 +265,7 @@ int zm_linear_attention_backward_workspace_size(const zm_linear_desc* desc, int6
   ZM_TRY(check_counts(desc, n));
   LinArgs a{};
   float* sums;
-  *bytes = backward_ws(a, desc, lin_plan(desc, n, true), n, nullptr, nullptr, &sums);
+  *bytes = backward_ws(a, desc, lin_plan(desc, n), n, nullptr, nullptr, &sums);
   return ZM_OK;
 }
 
@@ -285,7 +295,7 @@ int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const in
     }
   }
   ZM_TRY(check_apart(dstate_in, {state_in}));
-  const LinPlan p = lin_plan(desc, n, true);
+  const LinPlan p = lin_plan(desc, n);
   LinArgs a{};
   float* sums;
   ZM_TRY(check_workspace(workspace, workspace_bytes, backward_ws(a, desc, p, n, offsets, workspace, &sums)));

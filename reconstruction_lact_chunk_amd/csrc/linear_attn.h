@@ -88,7 +88,7 @@ struct LinSeg {
   int chunk0;       // chunks before it (each segment but a sequence's last has seg_chunks)
   int slot;         // of its state, in a sequence of several segments
   int segs;         // of its sequence
-  int pad;
+  int split;        // of its sequence, among those of several segments (in a table)
 };
 constexpr int kLinWaveSeqs = 64;  // sequences that need no table
 constexpr int kLinSorted = 512;   // segments that the table puts in order
@@ -97,9 +97,11 @@ struct LinSeqs {
   const int* offsets;   // [n_seq + 1] or null: one sequence of all n tokens
   LinSeg* segs;         // null without a table (up to kLinWaveSeqs sequences)
   int* by_slot;         // [slots] the segment, -1: unused
+  int* by_split;        // [n_split] the first segment of each sequence of several, -1: unused
   int4* all;            // {first token, end, chunks, -} of all sequences together
   int n, n_seq;
   int n_segs, n_slots;  // upper bounds over every content of offsets
+  int n_split;          // the same of the sequences of several segments
   bool longest_first;   // the table's order, else that of the tokens
   int seg_tokens;       // tokens of a segment, a multiple of the chunk
   int chunk;
@@ -221,7 +223,7 @@ struct LinWave {
     g.chunk0 = __builtin_amdgcn_readlane(chunk0, b) + (int)(from / s.chunk);
     g.slot = __builtin_amdgcn_readlane(slot0, b) + i;
     g.segs = k;
-    g.pad = 0;
+    g.split = 0;
     return g;
   }
 };
@@ -276,6 +278,22 @@ __device__ __forceinline__ LinSeg lin_slot(const LinSeqs& s, int slot) {
   if (at == 0) return g;
   const int b = __builtin_ctzll(at);
   return w.get(s, b, slot - __builtin_amdgcn_readlane(w.slot0, b));
+}
+
+// The first segment of the r-th sequence of several.
+__device__ __forceinline__ LinSeg lin_split(const LinSeqs& s, int r) {
+  LinSeg g;
+  g.count = -1;
+  if (s.segs) {
+    const int i = s.by_split[r];
+    if (i >= 0) g = s.segs[i];
+    return g;
+  }
+  const LinWave w(s);
+  const int split = w.segs > 1 ? 1 : 0, upto = lin_prefix(split);
+  const uint64_t at = __ballot(split && upto == r + 1);
+  if (at == 0) return g;
+  return w.get(s, __builtin_ctzll(at), 0);
 }
 
 // x as three bf16 parts, each what 8 bits hold of what the ones before leave, cut off: the sum

@@ -7,11 +7,11 @@ namespace zm {
 namespace {
 
 // ---- table --------------------------------------------------------------------
-// One workgroup: the clamped, nondecreasing offsets, the prefix sums of chunks, segments
-// and slots, and every segment's entry; longest first where there are more workgroups than
+// One workgroup: the clamped, nondecreasing offsets, the prefix sums of chunks, segments,
+// slots and sequences of several segments, and every segment's entry; longest first where there are more workgroups than
 // run at once, so that long ones do not end last.
 __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
-  __shared__ int part[4][16], total, slots;
+  __shared__ int part[5][16], total, slots, splits;
   __shared__ LinSeg seg_l[kLinSorted];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, per = (s.n_seq + 1023) / 1024;
   const int b0 = t * per < s.n_seq ? t * per : s.n_seq, b1 = b0 + per < s.n_seq ? b0 + per : s.n_seq;
@@ -34,8 +34,8 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
   for (int i = 0; i < w; ++i)
     if (part[0][i] > run) run = part[0][i];
   const int run0 = run;
-  // chunks, segments and slots before this thread's sequences
-  int v[3] = {0, 0, 0};
+  // chunks, segments, slots and sequences of several before this thread's sequences
+  int v[4] = {0, 0, 0, 0};
   for (int b = b0; b < b1; ++b) {
     int e = clampi(s.offsets[b + 1], 0, s.n);
     if (e < run) e = run;
@@ -43,11 +43,12 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
     v[0] += lin_chunks(s, e - run);
     v[1] += k;
     v[2] += k > 1 ? k : 0;
+    v[3] += k > 1;
     run = e;
   }
-  int at[3];
+  int at[4];
 #pragma unroll
-  for (int j = 0; j < 3; ++j) {
+  for (int j = 0; j < 4; ++j) {
     int x = v[j];
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
   __syncthreads();
   for (int i = 0; i < w; ++i)
 #pragma unroll
-    for (int j = 0; j < 3; ++j) at[j] += part[1 + j][i];
+    for (int j = 0; j < 4; ++j) at[j] += part[1 + j][i];
   run = run0;
   for (int b = b0; b < b1; ++b) {
     int e = clampi(s.offsets[b + 1], 0, s.n);
@@ -77,23 +78,28 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
       g.chunk0 = at[0] + (int)(from / s.chunk);
       g.slot = at[2] + i;
       g.segs = k;
-      g.pad = 0;
+      g.split = at[3];
       const int si = at[1] + i;
       if (s.longest_first) {
         seg_l[si] = g;
       } else {
         s.segs[si] = g;
-        if (k > 1) s.by_slot[g.slot] = si;
+        if (k > 1) {
+          s.by_slot[g.slot] = si;
+          if (i == 0) s.by_split[g.split] = si;
+        }
       }
     }
     at[0] += lin_chunks(s, len);
     at[1] += k;
     at[2] += k > 1 ? k : 0;
+    at[3] += k > 1;
     run = e;
   }
   if (t == 1023) {  // behind the last sequence, whosever that is
     total = at[1];
     slots = at[2];
+    splits = at[3];
     *s.all = int4{start, run, at[0], 0};
   }
   __syncthreads();
@@ -105,10 +111,14 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
       rank += c > mine || (c == mine && i < t);
     }
     s.segs[rank] = seg_l[t];
-    if (seg_l[t].segs > 1) s.by_slot[seg_l[t].slot] = rank;
+    if (seg_l[t].segs > 1) {
+      s.by_slot[seg_l[t].slot] = rank;
+      if (seg_l[t].flags & 1) s.by_split[seg_l[t].split] = rank;
+    }
   }
   for (int i = total + t; i < s.n_segs; i += 1024) s.segs[i].count = -1;
   for (int i = slots + t; i < s.n_slots; i += 1024) s.by_slot[i] = -1;
+  for (int i = splits + t; i < s.n_split; i += 1024) s.by_split[i] = -1;
 }
 
 // ---- what a segment adds ----------------------------------------------------------
@@ -167,8 +177,8 @@ __global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
 }
 
 // ---- join ------------------------------------------------------------------------
-// A block to 1024 elements of a state of a head, of the sequence whose first slot it has; a
-// thread four of them, the segments in order: each one's slot takes the state at its start
+// A block to 1024 elements of a state of a head of a sequence of several segments, a
+// thread to four of them, the segments in order: each one's slot takes the state at its start
 // (the gradients: the other way, at its end).  Loads of 16 segments are in flight.
 __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways) {
   const int blocks = dd / 1024;  // of a state
@@ -178,8 +188,8 @@ __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways
   const int h = x % a.heads;
   x /= a.heads;
   const int rev = x % ways;
-  const LinSeg sg = lin_slot(a.sq, x / ways);
-  if (sg.count < 0 || !(sg.flags & 1)) return;
+  const LinSeg sg = lin_split(a.sq, x / ways);
+  if (sg.count < 0) return;
   const int n = sg.segs;
   const float* const init = rev ? a.dstate_out : a.state_in;
   f32x4 m = {0.f, 0.f, 0.f, 0.f};
@@ -347,7 +357,7 @@ hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, hipStream_t s
 
 hipError_t launch_linear_join(const LinArgs& a, int d, bool both, hipStream_t st) {
   const int ways = both ? 2 : 1;
-  const int64_t blocks = (int64_t)a.sq.n_slots * ways * a.heads * (d * d / 1024);
+  const int64_t blocks = (int64_t)a.sq.n_split * ways * a.heads * (d * d / 1024);
   hipLaunchKernelGGL(k_linear_join, dim3((unsigned)blocks), dim3(256), 0, st, a, d * d, ways);
   return hipGetLastError();
 }

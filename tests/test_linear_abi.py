@@ -34,7 +34,7 @@ def places(names, same=None, **kw):
     return p
 
 
-def forward(n=4, same=None, size=1 << 40, d=None, **kw):
+def forward(n=2000, same=None, size=1 << 40, d=None, **kw):
     names = INPUTS + ("o", "state_out", "ws")
     p = places(names, same, **kw)
     d = d if d is not None else desc(**{k: v for k, v in kw.items() if k not in names})
