@@ -8,7 +8,7 @@ namespace zm {
 // Tensors of one launch: its arguments hold them, so that no table has to be copied to the
 // device (a captured launch keeps it); 3.6 KB of the 4 KB of arguments.
 constexpr int kClipTensors = 128;
-constexpr int kClipPieceBytes = 32 * 1024;      // of one type's elements, a step of a workgroup
+constexpr int kClipPieceBytes = 16 * 1024;      // of one type's elements, a step of a workgroup
 constexpr int kClipBlocks = 4 * kTargetWgs;     // workgroups of a launch at most, each with a partial sum
 
 struct ClipTable {

@@ -162,7 +162,8 @@ __device__ __forceinline__ void piece_scale(const void* p, void* q, int64_t n, i
       unpack<T>(raw[i], v);
 #pragma unroll
       for (int j = 0; j < E; ++j) v[j] = (float)((double)v[j] * c);
-      *(u32x4*)(y + e) = pack<T>(v);
+      // past the caches, which then keep the elements still to be read: 24 layers' 277 MB 173 -> 148 us
+      __builtin_nontemporal_store(pack<T>(v), (u32x4*)(y + e));
     } else if (alike && e < n && e + E > 0) {  // a word at an end
       for (int j = 0; j < E; ++j)
         if (e + j >= 0 && e + j < n) put(y + e + j, (float)((double)get(pc.x + e + j) * c));

@@ -71,7 +71,7 @@ __device__ __forceinline__ void put_row(T* p, const float (*x)[2][V], const int 
         Vec<T, V> v;
 #pragma unroll
         for (int j = 0; j < V; ++j) v.e[j] = from_f<T>(x[i][s][j]);
-        store_v<T, V>(p + c[i][s], v);
+        stream_v<T, V>(p + c[i][s], v);
       }
 }
 template <int V, int NG>
