@@ -178,7 +178,7 @@ __global__ __launch_bounds__(256) void k_norm_rotary(NormRotaryArgs a, Plan pl) 
 // through LDS, and the sums go to the workgroup's slot, which k_norm_rotary_params adds in
 // order (no atomics).
 template <typename T, int V, bool ADJ, int NG>
-__global__ __launch_bounds__(256) void k_norm_rotary_backward(NormRotaryArgs a, Plan pl) {
+__global__ __launch_bounds__(256, V == 4 ? 4 : 1) void k_norm_rotary_backward(NormRotaryArgs a, Plan pl) {
   const RotaryArgs& r = a.r;
   extern __shared__ float sums[];  // [4 waves][4][d], with params
   const int row = threadIdx.x / pl.lanes, lane = threadIdx.x - row * pl.lanes, rows = 256 / pl.lanes;
@@ -328,9 +328,10 @@ template <typename T, int V, bool ADJ, int NG>
 hipError_t forward_launch(const NormRotaryArgs& a, hipStream_t st) {
   Plan pl = plan_of<V>(a.r);
   const int all = a.r.q.heads + a.r.k.heads;
-  // Threads for eight waves on each SIMD, as far as the heads can be split: a thread with
-  // many heads forms its angles once, one with few starts sooner.
-  const int64_t want = (int64_t)kTargetWgs * 4 * 8 * 64;
+  // Threads for four waves on each SIMD, as far as the heads can be split: a thread with
+  // many heads forms its angles once, one with few starts sooner (one frame: 6.3 us, for eight
+  // waves 8.0, for one 7.0).
+  const int64_t want = (int64_t)kTargetWgs * 4 * 4 * 64;
   int64_t splits = ceil_div(want, a.r.n * pl.lanes);
   if (splits > all) splits = all;
   pl.heads_each = (int)ceil_div(all, splits);
@@ -360,12 +361,12 @@ hipError_t backward_launch(const NormRotaryArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Runs of 8 or 4 pairs where they fit, else of one: a lane then has one group, or two
-// where a head has more than 64 pairs.
+// Runs of 4 pairs where they fit, else of one: a lane then has one group, or two where a
+// head has more than 64 pairs.  Runs of 8 (bf16, 8 + 8 heads of 128, us against runs of 4): one
+// frame 7.5 and 6.3, 100 frames 214 and 211, their gradients 29 and 17, 330 and 326.
 #define ZM_NORM_ROTARY(F, T)                                                                           \
   do {                                                                                                 \
     const bool adj = a.r.layout == 1;                                                                  \
-    if (rotary_fits(a.r, 8)) return adj ? F<T, 8, true, 1>(a, st) : F<T, 8, false, 1>(a, st);          \
     if (rotary_fits(a.r, 4)) return adj ? F<T, 4, true, 1>(a, st) : F<T, 4, false, 1>(a, st);          \
     if (a.r.d <= 128) return adj ? F<T, 1, true, 1>(a, st) : F<T, 1, false, 1>(a, st);                 \
     return adj ? F<T, 1, true, 2>(a, st) : F<T, 1, false, 2>(a, st);                                   \
