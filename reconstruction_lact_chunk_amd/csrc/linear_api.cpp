@@ -119,7 +119,7 @@ void common_ws(LinArgs& a, Carve& c, const zm_linear_desc* d, const LinPlan& p, 
   }
   for (int i = 0; i < ways && p.slots > 0; ++i) {
     a.part[i] = c.take<float>((size_t)p.slots * d->heads * d->d_head * d->d_head);
-    a.decay[i] = c.take<float>((size_t)p.slots * d->heads);
+    a.decay[i] = c.take<float2>((size_t)p.slots * d->heads);
   }
   a.heads = d->heads;
   a.heads_k = d->heads_k;

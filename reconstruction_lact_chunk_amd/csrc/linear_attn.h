@@ -131,7 +131,7 @@ struct LinArgs {
   // gradients at their ends.  Before the join what the segment before (behind) adds is there.
   // So no pass reads state_in or dstate_out where another segment replaces it.
   float* part[2];
-  float* decay[2];     // [slots][heads] factor of a segment
+  float2* decay[2];    // [slots][heads] factor of a segment in two parts
   void* o;             // o, or dq
   int64_t ld_o;
   void* dk;
@@ -455,6 +455,13 @@ __device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_row_dims(const uint16_t
 template <int D, bool F32>
 __device__ __forceinline__ Parts<LinCfg<D, F32>::NT> lin_columns(const uint16_t* t, int w, int ts, int g, int c) {
   return lin_read_tr<D, F32>(t, ts, 2 * w + ((c & 3) >> 1), 4 * (c & 1), g, c);
+}
+
+// 2^x in two parts, 48 bits.
+__device__ __forceinline__ float2 lin_exp2_parts(double x) {
+  const double f = exp2(x);
+  const float hi = (float)f, rest = (float)(f - hi);
+  return float2{hi, fabsf(rest) < INFINITY ? rest : 0.f};
 }
 
 template <int CTRL, int ROWS>

@@ -173,13 +173,15 @@ __global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
     __syncthreads();
   }
   st.store(a.part[0] + ((int64_t)(sg.slot + 1) * a.heads + h) * D * D, w, g, c);
-  if (mine && lane == 0) a.decay[0][(int64_t)sg.slot * a.heads + h] = exp2_wide(fac[0].sum);
+  if (mine && lane == 0) a.decay[0][(int64_t)sg.slot * a.heads + h] = lin_exp2_parts(fac[0].sum);
 }
 
 // ---- join ------------------------------------------------------------------------
 // A block to 1024 elements of a state of a head of a sequence of several segments, a
 // thread to four of them, the segments in order: each one's slot takes the state at its start
-// (the gradients: the other way, at its end).  Loads of 16 segments are in flight.
+// (the gradients: the other way, at its end).  Loads of 16 segments are in flight.  The
+// decays are taken in two parts: where they are all alike, a rounding to 24 bits would be too, and add
+// up over the segments.
 __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways) {
   const int blocks = dd / 1024;  // of a state
   unsigned x = blockIdx.x;
@@ -196,12 +198,12 @@ __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways
   if (init) m = *(const f32x4*)(init + ((int64_t)sg.seq * a.heads + h) * dd + el);
   const int64_t first = (int64_t)(rev ? sg.slot + n - 1 : sg.slot) * a.heads + h, step = rev ? -a.heads : a.heads;
   float* const part = a.part[rev] + el;
-  const float* const decay = a.decay[rev];
+  const float2* const decay = a.decay[rev];
   *(f32x4*)(part + first * dd) = m;
   constexpr int U = 16;
   for (int i0 = 1; i0 < n; i0 += U) {
     f32x4 add[U];
-    float f[U];
+    float2 f[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t at = first + (i0 + u < n ? i0 + u : n - 1) * step;
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways
     for (int u = 0; u < U; ++u) {
       if (i0 + u >= n) break;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) m[r] = fmaf(m[r], f[u], add[u][r]);
+      for (int r = 0; r < 4; ++r) m[r] = fmaf(m[r], f[u].x, fmaf(m[r], f[u].y, add[u][r]));
       *(f32x4*)(part + (first + (i0 + u) * step) * dd) = m;
     }
   }

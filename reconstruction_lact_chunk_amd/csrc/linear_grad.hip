@@ -184,7 +184,7 @@ __global__ __launch_bounds__(4 * D, F32 && D == 128 ? 2 : 4) void k_linear_grad_
   if (need_m) m.store(a.part[0] + ((int64_t)(sg.slot + 1) * a.heads + h) * dd, w, l.g, l.c);
   if (need_d) d.store(a.part[1] + ((int64_t)(sg.slot - 1) * a.heads + h) * dd, w, l.g, l.c);
   if (mine && lane == 0) {
-    const float all = exp2_wide(fac[(n - 1) & 1].sum);
+    const float2 all = lin_exp2_parts(fac[(n - 1) & 1].sum);
     if (need_m) a.decay[0][(int64_t)sg.slot * a.heads + h] = all;
     if (need_d) a.decay[1][(int64_t)sg.slot * a.heads + h] = all;
   }
