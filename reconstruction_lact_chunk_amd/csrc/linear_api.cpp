@@ -153,7 +153,7 @@ int check_counts(const zm_linear_desc* d, int64_t n) {
   if (n < 0 || n > kMaxLinTokens || (d->n_seq == 0 && n > 0)) return ZM_ERR_INVALID_ARG;
   // the largest grid: a block of 512 threads to each segment and head (the join's 32 to a
   // split sequence and head are at most 32 times 512)
-  if ((int64_t)lin_plan(d, n).n_segs * d->heads * 2 > kMaxLinBlocks) return ZM_ERR_UNSUPPORTED;
+  if (d->n_seq > kMaxLinBlocks || (int64_t)lin_plan(d, n).n_segs * d->heads * 2 > kMaxLinBlocks) return ZM_ERR_UNSUPPORTED;
   return ZM_OK;
 }
 

@@ -80,7 +80,7 @@ def test_refusals(bad, want):
 
 @pytest.mark.parametrize("bad,want", [
     (dict(n=-1), INVALID), (dict(n=1 << 31), INVALID), (dict(n_seq=0), INVALID), (dict(offsets=None), INVALID),
-    (dict(offsets=(1 << 20) + 2), INVALID), (dict(n_seq=1 << 24), UNSUPPORTED), (dict(ws=None), WORKSPACE),
+    (dict(offsets=(1 << 20) + 2), INVALID), (dict(n_seq=1 << 24), UNSUPPORTED), (dict(n_seq=(1 << 31) - 1), UNSUPPORTED), (dict(ws=None), WORKSPACE),
     (dict(ws=(1 << 20) + 128), INVALID), (dict(size=64), WORKSPACE)])
 def test_refusals_of_whole_sequences(bad, want):
     assert forward(**bad) == want
