@@ -473,11 +473,12 @@ typedef struct zm_linear_desc {
 } zm_linear_desc;
 
 /* Bytes of workspace of zm_linear_attention for n tokens in desc->n_seq sequences (never less
- * for more tokens): at most 1024 / heads + 1 states to a head. */
+ * for more tokens): at most 1024 / heads states to a head, and past 64 sequences a table of 32
+ * bytes to a sequence. */
 ZM_API int zm_linear_attention_workspace_size(const zm_linear_desc* desc, int64_t n, size_t* bytes);
 
-/* Whole sequences, a chunk of tokens at a time (fp32 states, products of 24 bits up to a
- * state and up to an output's own rounding).  state_in: the states before the first tokens or
+/* Whole sequences, a chunk of tokens at a time (fp32 states; products of 24 bits up to a state, a
+ * gradient and an fp32 output, a term of a bf16 output to 2^-16 before that is rounded).  state_in: the states before the first tokens or
  * NULL (zeros); state_out: receives the states after the last ones, or NULL; it may be state_in.
  * o and state_out must not overlap other arrays (the same pointer is refused).  Rows of o
  * outside every sequence are left as they were.  Bitwise reproducible.  A sequence is cut into

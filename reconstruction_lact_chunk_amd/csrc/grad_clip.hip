@@ -5,6 +5,10 @@
 // range, and a conversion and a multiply-add an element hide behind the loads); the partial sums
 // go to the workgroups' slots and every workgroup of the scaling adds all of them in the
 // same order, so there is no third launch, no atomic, and the same bits every time.
+// 277 MB of 24 layers' gradients (two launches of each kernel): 49 us for the squares, 100 for the
+// scaling, which finds part of its input in the caches: 832 MB of reads and writes at 5.6 TB/s.  Next
+// piece's loads ahead of this one's sums: 2% slower; pieces of 32 or 8 KB 153 and 164 us against 149 of
+// 16 KB, of 2048 workgroups 161.  6 MB: 4 + 5 us.
 #include "grad_clip.h"
 
 namespace zm {

@@ -151,8 +151,8 @@ size_t backward_ws(LinArgs& a, const zm_linear_desc* d, const LinPlan& p, int64_
 
 int check_counts(const zm_linear_desc* d, int64_t n) {
   if (n < 0 || n > kMaxLinTokens || (d->n_seq == 0 && n > 0)) return ZM_ERR_INVALID_ARG;
-  // the largest grid: a block of 512 threads to each segment and head (the join's 32 to a
-  // split sequence and head are at most 32 times 512)
+  // the largest grid: a block of 512 threads to each segment and head (the join's
+  // 128 waves to a split sequence and head are at most 128 times 512)
   if (d->n_seq > kMaxLinBlocks || (int64_t)lin_plan(d, n).n_segs * d->heads * 2 > kMaxLinBlocks) return ZM_ERR_UNSUPPORTED;
   return ZM_OK;
 }

