@@ -8,10 +8,10 @@
 // statistics are formed again in the gradient.  A group of V pairs is a lane's, so that a
 // head's row lies in the registers of a power of two of lanes and its sums take
 // few exchanges; the angles of a lane's pairs are formed once for all heads of a token.
-// Results are stored past the caches (fp32 40 frames 132 -> 119 us, the gradient of 100
-// frames 337 -> 328).  54,960 fp32 tokens of 20 heads of 64: 119 us, 4.7 TB/s; gradient of 137,400
-// bf16 tokens of 16 heads of 128: 325 us, 5.2 TB/s; one frame of 1374 tokens 7.7 us, loads, angles and
-// exchanges one after the other.
+// 54,960 fp32 tokens of 20 heads of 64: 139 us, 4.1 TB/s; gradient of 137,400 bf16 tokens of 16 heads
+// of 128: 338 us, 5.0 TB/s; one frame of 1374 tokens 7.7 us, loads, angles and exchanges one after the
+// other.  Stores past the caches gave 3 to 5% for 8 + 8 heads and whole rotations (that gradient 328 us) and
+// cost 3 to 30% for other heads and sections (those fp32 tokens 151 us): not taken.
 #include "rotary_dev.h"
 
 namespace zm {
@@ -75,7 +75,7 @@ __device__ __forceinline__ void put_row(T* p, const float (*x)[2][V], const int 
         Vec<T, V> v;
 #pragma unroll
         for (int j = 0; j < V; ++j) v.e[j] = from_f<T>(x[i][s][j]);
-        stream_v<T, V>(p + c[i][s], v);
+        store_v<T, V>(p + c[i][s], v);
       }
 }
 template <int V, int NG>

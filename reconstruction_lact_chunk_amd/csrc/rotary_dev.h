@@ -53,20 +53,6 @@ __device__ __forceinline__ void store_v(T* p, const Vec<T, V>& r) {
     for (int i = 0; i < V; ++i) p[i] = r.e[i];
   }
 }
-// Past the caches, for rows that are written once and not read by the same kernel.
-template <typename T, int V>
-__device__ __forceinline__ void stream_v(T* p, const Vec<T, V>& r) {
-  constexpr int B = V * (int)sizeof(T);
-  if constexpr (B % 16 == 0) {
-#pragma unroll
-    for (int i = 0; i < B / 16; ++i) __builtin_nontemporal_store(((const u32x4*)&r)[i], (u32x4*)p + i);
-  } else if constexpr (B == 8) {
-    __builtin_nontemporal_store(*(const u32x2*)&r, (u32x2*)p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = r.e[i];
-  }
-}
 
 // First dims c0, c1 of the two runs of V elements of group grp: a rotated one of V pairs, or
 // of the unrotated tail.
