@@ -324,7 +324,10 @@ int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const in
     if (p.split) ZM_HIP(launch_linear_join(a, d, true, st));
     ZM_HIP(launch_linear_dkdv(a, d, f32, st));
     if (n > 0) ZM_HIP(launch_linear_dq(a, d, f32, st));
-    if (n > 0 && a.o_part) ZM_HIP(launch_linear_groups(a, d, f32, st));
+    if (n > 0 && a.o_part) {
+      ZM_HIP(launch_linear_groups(a, d, f32, one ? dg : nullptr, st));
+      return ZM_OK;
+    }
   }
   if (dg && one) ZM_HIP(launch_linear_decay_sum(sums, a.sq, desc->heads, dg, st));
   return ZM_OK;

@@ -775,9 +775,10 @@ hipError_t launch_linear_out(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_grad_states(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_dkdv(const LinArgs& a, int d, bool f32, hipStream_t st);
 hipError_t launch_linear_dq(const LinArgs& a, int d, bool f32, hipStream_t st);
-// dq and dk from o_part and dk_part, summed over the value heads of a key head.
-hipError_t launch_linear_groups(const LinArgs& a, int d, bool f32, hipStream_t st);
-// dg [heads] from the chunks' sums.
+// dq and dk from o_part and dk_part, summed over the value heads of a key head, and, unless dg is
+// null, dg [heads] from the chunks' sums a.dg.
+hipError_t launch_linear_groups(const LinArgs& a, int d, bool f32, float* dg, hipStream_t st);
+// dg alone.
 hipError_t launch_linear_decay_sum(const float* sums, const LinSeqs& s, int heads, float* dg, hipStream_t st);
 
 struct LinStepArgs {

@@ -42,8 +42,10 @@ using Four = std::conditional_t<F32, f32x4, u32x2>;
 // from both triangles: units of two 16 x 16 tiles, columns j in prefix sums over a row's lanes,
 // then sums over the rows i.  A row's sum over columns 0..31 counts for all t in 32..i.
 // 10,992 tokens of 8 heads of 128, bf16: 54 us; 4123 fp32 tokens of 6 heads of 64 17 us.
+// Two workgroups of d = 128 to a compute unit fit with 46 registers spilled: a frame's whole gradient 60.6 us
+// against 56.8, of 60 frames 1187 against 1164, of 40 packed sequences 938 against 952.
 template <int D, bool F32>
-__global__ __launch_bounds__(4 * D, F32 && D == 128 ? 2 : 4) void k_linear_grad_states(LinArgs a) {
+__global__ __launch_bounds__(4 * D, F32 || D == 128 ? 2 : 4) void k_linear_grad_states(LinArgs a) {
   using C = LinCfg<D, F32>;
   using T = typename Tok<F32>::T;
   constexpr int UNITS = C::CH == 64 ? 6 : 2;
@@ -521,17 +523,37 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
 }
 
 // ---- sums ------------------------------------------------------------------------
+// dg [heads]: a workgroup to a head, the chunks' sums in 64 bits, always in the same order.
+__device__ __forceinline__ void decay_sum(const float* sums, const LinSeqs& sq, int heads, int h, float* dg) {
+  __shared__ double red[4];
+  const int chunks = lin_all(sq).z;
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < chunks; i += 256) s += (double)sums[i * heads + h];
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) s += __shfl_xor(s, m, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) dg[h] = (float)(red[0] + red[1] + red[2] + red[3]);
+}
+__global__ __launch_bounds__(256) void k_linear_decay_sum(const float* sums, LinSeqs sq, int heads, float* dg) {
+  decay_sum(sums, sq, heads, blockIdx.x, dg);
+}
+
 // Eight elements a thread: the value heads of a key head in order, blockIdx.y 0 dq, 1 dk.
-// Rows outside the sequences are left as they are.
+// Rows outside the sequences are left as they are.  Workgroups past `blocks` form dg [heads].
 template <typename T>
-__global__ __launch_bounds__(256) void k_linear_groups(LinArgs a, int d) {
+__global__ __launch_bounds__(256) void k_linear_groups(LinArgs a, int d, int blocks, float* dg) {
+  if ((int)blockIdx.x >= blocks) {
+    if (blockIdx.y == 0) decay_sum(a.dg, a.sq, a.heads, blockIdx.x - blocks, dg);
+    return;
+  }
   const int heads = a.heads, per = a.heads_k * d / 8, rep = heads / a.heads_k;
   const float* const x = blockIdx.y ? a.dk_part : a.o_part;
   T* const y = (T*)(blockIdx.y ? a.dk : a.o);
   const int64_t ldy = blockIdx.y ? a.ld_dk : a.ld_o;
   const int4 range = lin_all(a.sq);
   const int64_t all = (int64_t)(range.y - range.x) * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)blocks * 256) {
     const int64_t t = range.x + i / per;
     const int col = 8 * (int)(i % per), hk = col / d, e = col % d;
     const float* const p = x + (t * heads + (int64_t)hk * rep) * d + e;
@@ -550,19 +572,6 @@ __global__ __launch_bounds__(256) void k_linear_groups(LinArgs a, int d) {
                           pack_bf16x2(s[6], s[7])};
     }
   }
-}
-
-// A workgroup to a head; the chunks' sums in 64 bits, always in the same order.
-__global__ __launch_bounds__(256) void k_linear_decay_sum(const float* sums, LinSeqs sq, int heads, float* dg) {
-  __shared__ double red[4];
-  const int chunks = lin_all(sq).z;
-  double s = 0.0;
-  for (int64_t i = threadIdx.x; i < chunks; i += 256) s += (double)sums[i * heads + blockIdx.x];
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) s += __shfl_xor(s, m, 64);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) dg[blockIdx.x] = (float)(red[0] + red[1] + red[2] + red[3]);
 }
 
 template <int D>
@@ -603,12 +612,12 @@ hipError_t launch_linear_dq(const LinArgs& a, int d, bool f32, hipStream_t st) {
   return d == 128 ? dq_any<128>(a, f32, st) : dq_any<64>(a, f32, st);
 }
 
-hipError_t launch_linear_groups(const LinArgs& a, int d, bool f32, hipStream_t st) {
+hipError_t launch_linear_groups(const LinArgs& a, int d, bool f32, float* dg, hipStream_t st) {
   int64_t blocks = ceil_div((int64_t)a.sq.n * (a.heads_k * d / 8), 256);
   if (blocks > 4 * kTargetWgs) blocks = 4 * kTargetWgs;
-  const dim3 grid((unsigned)blocks, 2);
-  if (f32) hipLaunchKernelGGL((k_linear_groups<float>), grid, dim3(256), 0, st, a, d);
-  else hipLaunchKernelGGL((k_linear_groups<uint16_t>), grid, dim3(256), 0, st, a, d);
+  const dim3 grid((unsigned)blocks + (dg ? a.heads : 0), 2);
+  if (f32) hipLaunchKernelGGL((k_linear_groups<float>), grid, dim3(256), 0, st, a, d, (int)blocks, dg);
+  else hipLaunchKernelGGL((k_linear_groups<uint16_t>), grid, dim3(256), 0, st, a, d, (int)blocks, dg);
   return hipGetLastError();
 }
 
