@@ -146,12 +146,13 @@ struct LinArgs {
   float* dg;           // [n][heads], or, with ld_g = 0, the chunks' sums [chunks][heads]
 };
 
-// Segments of a sequence of len tokens, and its chunks.
+// Segments of a sequence of len tokens, and its chunks (len and seg_tokens are under 2^31: 32
+// bits without a sign hold their sum).
 __device__ __forceinline__ int lin_segs(const LinSeqs& s, int len) {
-  return len > 0 ? (int)(((int64_t)len + s.seg_tokens - 1) / s.seg_tokens) : 1;
+  return len > 0 ? (int)(((unsigned)len + s.seg_tokens - 1) / (unsigned)s.seg_tokens) : 1;
 }
 __device__ __forceinline__ int lin_chunks(const LinSeqs& s, int len) {
-  return (int)(((int64_t)len + s.chunk - 1) / s.chunk);
+  return (int)(((unsigned)len + s.chunk - 1) >> (s.chunk == 64 ? 6 : 5));
 }
 
 // Sums, and the largest, over the lanes up to each one: shifts within 16 lanes, then the
@@ -219,12 +220,12 @@ struct LinWave {
   __device__ __forceinline__ LinSeg get(const LinSeqs& s, int b, int i) const {
     LinSeg g;
     const int k = __builtin_amdgcn_readlane(segs, b), l = __builtin_amdgcn_readlane(len, b);
-    const int64_t from = (int64_t)i * s.seg_tokens;
-    g.tok = __builtin_amdgcn_readlane(begin, b) + (int)from;
-    g.count = l - from < s.seg_tokens ? (int)(l - from) : s.seg_tokens;
+    const int from = i * s.seg_tokens;  // < l, or 0
+    g.tok = __builtin_amdgcn_readlane(begin, b) + from;
+    g.count = l - from < s.seg_tokens ? l - from : s.seg_tokens;
     g.seq = b;
     g.flags = (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0);
-    g.chunk0 = __builtin_amdgcn_readlane(chunk0, b) + (int)(from / s.chunk);
+    g.chunk0 = __builtin_amdgcn_readlane(chunk0, b) + lin_chunks(s, from);
     g.slot = __builtin_amdgcn_readlane(slot0, b) + i;
     g.segs = k;
     g.split = 0;

@@ -69,13 +69,13 @@ __global__ __launch_bounds__(1024) void k_linear_table(LinSeqs s) {
     const int len = e - run;
     const int k = lin_segs(s, len);
     for (int i = 0; i < k; ++i) {
-      const int64_t from = (int64_t)i * s.seg_tokens;
+      const int from = i * s.seg_tokens;  // < len, or 0
       LinSeg g;
-      g.tok = run + (int)from;
-      g.count = len - from < s.seg_tokens ? (int)(len - from) : s.seg_tokens;
+      g.tok = run + from;
+      g.count = len - from < s.seg_tokens ? len - from : s.seg_tokens;
       g.seq = b;
       g.flags = (i == 0 ? 1 : 0) | (i == k - 1 ? 2 : 0);
-      g.chunk0 = at[0] + (int)(from / s.chunk);
+      g.chunk0 = at[0] + lin_chunks(s, from);
       g.slot = at[2] + i;
       g.segs = k;
       g.split = at[3];
