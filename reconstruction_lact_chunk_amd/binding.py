@@ -724,6 +724,8 @@ def _heads_rows(name, t, n, heads, d, dtype):
         raise ZmError(f"{name}: dtype {t.dtype}, the call needs bf16 or fp32 throughout")
     if t.shape != (n, heads, d):
         raise ZmError(f"{name}: shape {tuple(t.shape)} != [{n}, {heads}, {d}]")
+    if t.is_contiguous() and t.numel() > 0:
+        return heads * d
     if n > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
         raise ZmError(f"{name}: token tensors need unit stride on d and d on heads")
     return t.stride(0) if n > 1 else heads * d
@@ -926,10 +928,11 @@ def _linear_inputs(q, k, v, g, scale):
            _heads_rows("v", v, n, h, d, q.dtype)]
     ld_g = 0
     if g is not None:
-        if g.dtype != torch.float32 or (g.shape != (n, h) and g.shape != (h,)) \
-                or (g.numel() > 0 and g.stride(-1) != 1 and h > 1):
+        shape = g.shape
+        if g.dtype != torch.float32 or (shape != (n, h) and shape != (h,)) \
+                or (h > 1 and g.stride(-1) != 1 and g.numel() > 0):
             raise ZmError(f"g must be fp32 [{n}, {h}] or [{h}] with unit stride on the heads")
-        if g.dim() == 2:
+        if len(shape) == 2:
             ld_g = g.stride(0) if n > 1 else h
             if ld_g < h:
                 raise ZmError("g's rows overlap: pass [heads] for one decay to each head")
