@@ -726,9 +726,10 @@ def _heads_rows(name, t, n, heads, d, dtype):
         raise ZmError(f"{name}: shape {tuple(t.shape)} != [{n}, {heads}, {d}]")
     if t.is_contiguous() and t.numel() > 0:
         return heads * d
-    if n > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    ld, ld_h, ld_d = t.stride()
+    if n > 0 and (ld_d != 1 or (heads > 1 and ld_h != d)):
         raise ZmError(f"{name}: token tensors need unit stride on d and d on heads")
-    return t.stride(0) if n > 1 else heads * d
+    return ld if n > 1 else heads * d
 
 
 def _rotary_inputs(q, k, pos, freqs, sections):
