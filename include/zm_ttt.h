@@ -477,9 +477,9 @@ typedef struct zm_linear_desc {
  * bytes to a sequence. */
 ZM_API int zm_linear_attention_workspace_size(const zm_linear_desc* desc, int64_t n, size_t* bytes);
 
-/* Whole sequences, a chunk of tokens at a time (fp32 states; products of 24 bits up to a state, a
- * gradient and an fp32 output, a term of a bf16 output to 2^-16 before that is rounded).  state_in: the states before the first tokens or
- * NULL (zeros); state_out: receives the states after the last ones, or NULL; it may be state_in.
+/* Whole sequences, a chunk of tokens at a time (fp32 states; products of 24 bits up to the
+ * rounding of an output).  state_in: the states before the first tokens or NULL (zeros);
+ * state_out: receives the states after the last ones, or NULL; it may be state_in.
  * o and state_out must not overlap other arrays (the same pointer is refused).  Rows of o
  * outside every sequence are left as they were.  Bitwise reproducible.  A sequence is cut into
  * segments of a length that follows from n, n_seq, heads and io_dtype alone, which run side by

@@ -32,10 +32,8 @@
 //
 // Matrix products run on v_mfma_f32_16x16x32_bf16, operands in fp32 (states, T, w o C,
 // fp32 tokens) as a sum of three bf16 parts (delta_rule.h): 24 bits, so states, gradients and
-// fp32 outputs are as exact as fp32 products would leave them.  Outputs o in bf16 take the
-// state and T in two parts, each rounded to the nearest: 2^-16 of a term at most, where the
-// output's own rounding is 2^-8 (54321 tokens of 16 heads 302 -> 272 us, 100 frames
-// 478 -> 442).
+// outputs up to their own rounding are as exact as fp32 products would leave them, also where an
+// output's terms cancel.
 //
 // A wave holds 16 columns of the state and all its rows; its accumulators are operands of
 // the next product as they are.  Outputs are formed transposed, so that a lane has four
@@ -61,7 +59,6 @@ struct LinCfg {
   static constexpr int PITCH = F32 ? D + 16 : D; // elements of a row in LDS
   static constexpr int PART = CH * PITCH;        // elements of one part of a tile
   static constexpr int TILE = NT * PART;
-  static constexpr int OP = F32 ? 3 : 2;         // parts of the states and T in the outputs o
   static constexpr int TRI = 3 * FRAGS * kFragElems;
 };
 
@@ -321,24 +318,9 @@ __device__ __forceinline__ Parts<3> cut8(const float* x) {
   }
   return out;
 }
-// x as two parts, each rounded to the nearest: off by 2^-16 of x at most.
-__device__ __forceinline__ Parts<2> round8(const float* x) {
-  Parts<2> out;
-  u32x4 hi, lo;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    lo[i] = pack_bf16x2(x[2 * i] - bf16lo(hi[i]), x[2 * i + 1] - bf16hi(hi[i]));
-  }
-  out.p[0] = as_bf16x8(hi);
-  out.p[1] = as_bf16x8(lo);
-  return out;
-}
-template <int P>
-__device__ __forceinline__ Parts<P> cut_tiles(const f32x4& a, const f32x4& b) {
+__device__ __forceinline__ Parts<3> cut_tiles(const f32x4& a, const f32x4& b) {
   const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  if constexpr (P == 3) return cut8(x);
-  else return round8(x);
+  return cut8(x);
 }
 
 // Tiles of token rows in LDS.  bf16: the row's granules (8 elements) in the order p ^
@@ -605,21 +587,8 @@ __device__ __forceinline__ f32x4 lin_gate(const f32x4& x, const LinFactors* f, f
   return t;
 }
 
-// Four sources of a triangle's tile into its operand tiles (P parts): element 4 (jt & 1) + r of
-// lane.
-template <int P>
+// Four sources of a triangle's tile into its operand tiles: element 4 (jt & 1) + r of lane.
 __device__ __forceinline__ void lin_put(uint16_t* frags, int frags_each, int fi, int jt, int lane, const f32x4& t) {
-  if constexpr (P == 2) {
-    u32x2 hi, lo;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      hi[i] = pack_bf16x2(t[2 * i], t[2 * i + 1]);
-      lo[i] = pack_bf16x2(t[2 * i] - bf16lo(hi[i]), t[2 * i + 1] - bf16hi(hi[i]));
-    }
-    *(u32x2*)(frags + fi * kFragElems + lane * 8 + 4 * (jt & 1)) = hi;
-    *(u32x2*)(frags + (frags_each + fi) * kFragElems + lane * 8 + 4 * (jt & 1)) = lo;
-    return;
-  }
   unsigned r[4] = {__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3])};
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
@@ -676,15 +645,14 @@ struct LinOut {
   f32x4 o[C::IT];  // dims 16 w + 4 g + r of token 16 it + c
 
   // A M^
-  template <int P>
   __device__ __forceinline__ void read(const LinState<D, F32>& st, const uint16_t* a, int g, int c) {
 #pragma unroll
     for (int it = 0; it < C::IT; ++it) o[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < C::KS; ++s) {
-      const Parts<P> mp = cut_tiles<P>(st.m[2 * s], st.m[2 * s + 1]);
+      const Parts<3> mp = cut_tiles(st.m[2 * s], st.m[2 * s + 1]);
 #pragma unroll
-      for (int it = 0; it < C::IT; ++it) mma<P - 1>(o[it], mp, lin_row<D, F32>(a, 16 * it + c, 4 * s + g));
+      for (int it = 0; it < C::IT; ++it) mma<2>(o[it], mp, lin_row<D, F32>(a, 16 * it + c, 4 * s + g));
     }
   }
   __device__ __forceinline__ void scale(const LinFactors* f, int c) {
@@ -715,8 +683,8 @@ struct LinOut {
   }
 };
 
-// out += T C (T in OUT parts, 0: without outputs) and M^ <- M^ + B^T (dn o C).
-template <int D, bool F32, bool REV, int OUT>
+// out += T C and M^ <- M^ + B^T (dn o C).
+template <int D, bool F32, bool REV, bool OUT>
 __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>& st, const uint16_t* frags,
                                            const uint16_t* b, const uint16_t* cc, const float* dn, int w, int lane,
                                            int g, int c) {
@@ -724,15 +692,15 @@ __device__ __forceinline__ void lin_tokens(LinOut<D, F32>* out, LinState<D, F32>
 #pragma unroll
   for (int ts = 0; ts < C::TS; ++ts) {
     const auto cf = lin_columns<D, F32>(cc, w, ts, g, c);
-    if constexpr (OUT > 0) {
+    if constexpr (OUT) {
 #pragma unroll
       for (int it = 0; it < C::IT; ++it) {
         if (!lin_in<D, F32, REV>(it, ts)) continue;
-        Parts<OUT> t;
+        Parts<3> t;
 #pragma unroll
-        for (int p = 0; p < OUT; ++p)
+        for (int p = 0; p < 3; ++p)
           t.p[p] = *(const bf16x8*)(frags + (p * C::FRAGS + lin_frag<D, F32, REV>(it, ts)) * kFragElems + lane * 8);
-        mma<OUT - 1>(out->o[it], cf, t);
+        mma<2>(out->o[it], cf, t);
       }
     }
     float x[8];

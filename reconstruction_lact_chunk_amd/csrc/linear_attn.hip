@@ -169,7 +169,7 @@ __global__ __launch_bounds__(4 * D, 4) void k_linear_states(LinArgs a) {
       lin_reach(fac + (~j & 1), f, gl, tokens(j - 1));
       if (j > 1) gl = decay(j - 2);
     }
-    lin_tokens<D, F32, false, 0>(nullptr, st, nullptr, lds, lds + C::TILE, f->dn, w, lane, g, c);
+    lin_tokens<D, F32, false, false>(nullptr, st, nullptr, lds, lds + C::TILE, f->dn, w, lane, g, c);
     __syncthreads();
   }
   st.store(a.part[0] + ((int64_t)(sg.slot + 1) * a.heads + h) * D * D, w, g, c);
@@ -314,18 +314,18 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_out
           const int jt = 2 * ts + (t & 1);
           const f32x4 x =
               lin_gate<false, GATED>(lin_tri<D, F32>(q, k, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
-          lin_put<C::OP>(tri, C::FRAGS, fr, jt, l.lane, x);
+          lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
         }
         LinOut<D, F32> out;
         const LinLane lr(lane);
-        out.template read<C::OP>(st, q, lr.g, lr.c);
+        out.read(st, q, lr.g, lr.c);
         if (GATED) {
           out.scale(f, c);
           st.scale(f->last);
         }
         __syncthreads();
         const LinLane lt(lane);
-        lin_tokens<D, F32, false, C::OP>(&out, st, tri, k, v, f->dn, w, lt.lane, lt.g, lt.c);
+        lin_tokens<D, F32, false, true>(&out, st, tri, k, v, f->dn, w, lt.lane, lt.g, lt.c);
         const LinLane lo(lane);
         if (!GATED) out.scale(f, lo.c);
         out.store(op + (int64_t)j * C::CH * a.ld_o, (unsigned)a.ld_o, tokens(j), w, lo.g, lo.c);

@@ -158,11 +158,11 @@ __global__ __launch_bounds__(4 * D, F32 || D == 128 ? 2 : 4) void k_linear_grad_
     if (need_m) {
       m.scale(f->last);
       const LinLane l(lane);
-      lin_tokens<D, F32, false, 0>(nullptr, m, nullptr, k, v, to_end[j & 1], w, l.lane, l.g, l.c);
+      lin_tokens<D, F32, false, false>(nullptr, m, nullptr, k, v, to_end[j & 1], w, l.lane, l.g, l.c);
     }
     if (need_d) {
       const LinLane l(lane);
-      lin_tokens<D, F32, true, 0>(nullptr, d, nullptr, q, od, to_start[j & 1], w, l.lane, l.g, l.c);
+      lin_tokens<D, F32, true, false>(nullptr, d, nullptr, q, od, to_start[j & 1], w, l.lane, l.g, l.c);
     }
     __syncthreads();
     if (!F32 && j + 1 < n) fetch(j + 1);
@@ -293,12 +293,12 @@ __device__ __forceinline__ void back_pass(const LinArgs& a, const LinSeg& sg, in
         const int it = C::CH == 32 ? fr : fr < 4 ? fr >> 1 : fr - 2, ts = C::CH == 32 ? 0 : fr < 4 ? fr & 1 : 1;
         const int jt = 2 * ts + (t & 1);
         const f32x4 x = lin_gate<true, GATED>(lin_tri<D, F32>(ta, tb, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
-        lin_put<3>(tri, C::FRAGS, fr, jt, l.lane, x);
+        lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
       }
       LinOut<D, F32> out;
       {
         const LinLane l(lane);
-        out.template read<3>(st, ta, l.g, l.c);
+        out.read(st, ta, l.g, l.c);
       }
       if (SIDE == 0 && a.flow) {
         const LinLane l(lane);
@@ -316,7 +316,7 @@ __device__ __forceinline__ void back_pass(const LinArgs& a, const LinSeg& sg, in
       }
       __syncthreads();
       const LinLane lt(lane);
-      lin_tokens<D, F32, true, 3>(&out, st, tri, tb, tc, f->dn, w, lt.lane, lt.g, lt.c);
+      lin_tokens<D, F32, true, true>(&out, st, tri, tb, tc, f->dn, w, lt.lane, lt.g, lt.c);
       const LinLane l(lane);
       if (!GATED) out.scale(f, l.c);
       if (SIDE == 0) {
@@ -458,7 +458,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
         const int jt = 2 * ts + (t & 1);
         const f32x4 x =
             lin_gate<false, GATED>(lin_tri<D, F32>(od, v, it, jt, l.g, l.c), f, a.scale, it, jt, l.g, l.c);
-        lin_put<3>(tri, C::FRAGS, fr, jt, l.lane, x);
+        lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
       }
       if (a.flow) {
         float e = 0.f;
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
       LinOut<D, F32> out;
       {
         const LinLane l(lane);
-        out.template read<3>(st, od, l.g, l.c);
+        out.read(st, od, l.g, l.c);
       }
       if (a.flow) {
         const LinLane l(lane);
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
       }
       __syncthreads();
       const LinLane lt(lane);
-      lin_tokens<D, F32, false, 3>(&out, st, tri, v, k, f->dn, w, lt.lane, lt.g, lt.c);
+      lin_tokens<D, F32, false, true>(&out, st, tri, v, k, f->dn, w, lt.lane, lt.g, lt.c);
       const LinLane l(lane);
       if (!GATED) out.scale(f, l.c);
       if (a.o_part) out.store(a.o_part + (tok0 * a.heads + h) * D, (unsigned)(a.heads * D), count, w, l.g, l.c);
