@@ -349,7 +349,7 @@ __device__ __forceinline__ void back_pass(const LinArgs& a, const LinSeg& sg, in
 }
 
 template <int D, bool F32>
-__global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dkdv(LinArgs a) {
+__global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dkdv(LinArgs a, int side) {
   using C = LinCfg<D, F32>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[3 * C::TILE + C::TRI];
   __shared__ LinFactors fac[2];
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dkd
   const int h = blockIdx.x % a.heads;
   const LinSeg sg = lin_seg(a.sq, blockIdx.x / a.heads);
   if (sg.count < 0) return;
-  if (blockIdx.y == 0) back_pass<D, F32, 0>(a, sg, h, lds, fac, going, next_decays);
+  if (side + blockIdx.y == 0) back_pass<D, F32, 0>(a, sg, h, lds, fac, going, next_decays);
   else if (sg.count > 0) back_pass<D, F32, 1>(a, sg, h, lds, fac, going, next_decays);
 }
 
@@ -584,10 +584,20 @@ hipError_t grad_states_any(const LinArgs& a, bool f32, hipStream_t st) {
 
 template <int D>
 hipError_t dkdv_any(const LinArgs& a, bool f32, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.sq.n_segs * a.heads), 2), blk(4 * D);
-  if (f32) hipLaunchKernelGGL((k_linear_dkdv<D, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((k_linear_dkdv<D, false>), grid, blk, 0, st, a);
-  return hipGetLastError();
+  const unsigned blocks = (unsigned)((int64_t)a.sq.n_segs * a.heads);
+  auto sides = [&](int first, int count) {
+    const dim3 grid(blocks, count), blk(4 * D);
+    if (f32) hipLaunchKernelGGL((k_linear_dkdv<D, true>), grid, blk, 0, st, a, first);
+    else hipLaunchKernelGGL((k_linear_dkdv<D, false>), grid, blk, 0, st, a, first);
+    return hipGetLastError();
+  };
+  // Of a sequence in one segment both sides start from dstate_out, and side 0 ends with
+  // dstate_in.  Where that is the same array side 1 is a launch before side 0's; not where the
+  // only sequence is known to be cut: its segments start from part[1].
+  const bool cut = !a.sq.offsets && a.sq.n > a.sq.seg_tokens;
+  if (!a.dstate_in || a.dstate_in != a.dstate_out || cut) return sides(0, 2);
+  const hipError_t e = sides(1, 1);
+  return e != hipSuccess ? e : sides(0, 1);
 }
 
 template <int D>
