@@ -439,8 +439,10 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
       // q's elements of a lane's outputs and D^T are on their way meanwhile
       f32x4 de[C::MT];
       Four<F32> qe[C::IT];
+      double d_exp = 0.0;
       if (a.flow) {
         const LinLane l(lane);
+        d_exp = a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h];
 #pragma unroll
         for (int it = 0; it < C::IT; ++it) {
           const int row = 16 * it + l.c < count ? 16 * it + l.c : count - 1;
@@ -461,11 +463,15 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
         lin_put(tri, C::FRAGS, fr, jt, l.lane, x);
       }
       if (a.flow) {
+        // M at the chunk's start, D at its end and the decay between.  Both are held less powers of
+        // up to 2^60, so each takes half of the exponent before they meet: their product with neither could
+        // be past fp32's range where the sum is not.
+        const float half = exp2_wide(0.5 * (f->s + d_exp + f->cs[63]));
         float e = 0.f;
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][r], de[mt][r], e);
+          for (int r = 0; r < 4; ++r) e = fmaf(st.m[mt][r] * half, de[mt][r] * half, e);
         e = lin_prefix(e);
         if (lane == 63) through[w] = e;
       }
@@ -506,9 +512,7 @@ __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_dq(
         e += through[i];
       }
       x = lin_prefix(x);
-      // M at the chunk's start, D at its end and the decay between
-      const double power = f->s + a.d_exp[((int64_t)sg.chunk0 + j) * a.heads + h] + f->cs[63];
-      const float d = t < count ? a.flow[(tok0 + t) * a.heads + h] + x + e * exp2_wide(power) : 0.f;
+      const float d = t < count ? a.flow[(tok0 + t) * a.heads + h] + x + e : 0.f;
       if (a.ld_g) {
         if (t < count) a.dg[(tok0 + t) * a.heads + h] = d;
       } else {

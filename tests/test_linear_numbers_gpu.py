@@ -1,12 +1,14 @@
-"""What numbers linear attention holds on the way: outputs of bf16 tokens whose terms cancel.
+"""What numbers linear attention holds on the way: outputs of bf16 tokens whose terms cancel, and
+the gradient where decays, lengths and values make the held states large.
 
-Tolerances.  Operands of 24 bits are exact (three parts of 8), so are their products with +1 and -1, and
-what the matrix instructions' sums round is named at each test; on top comes the output's own
-rounding, half a step of 2^-7."""
+Tolerances.  Where terms cancel: operands of 24 bits are exact (three parts of 8), so are their products
+with +1 and -1, and what the matrix instructions' sums round is named at each test; on top comes
+the output's own rounding, half a step of 2^-7.  Otherwise those of linear_reference.py."""
 import pytest
 import torch
 
 import reconstruction_lact_chunk_amd as zm
+from linear_reference import check, chunks
 
 pytestmark = pytest.mark.gpu
 B = torch.bfloat16
@@ -53,3 +55,65 @@ def test_products_of_tokens_that_cancel(d):
     off = (o[2].double() - want).abs() - HALF * want.abs()
     assert off.max() <= (2 * 2 + 3 * 4) * 2.0 ** -24, f"{off.max().item():.3g}"
     assert not o[:2].any()
+
+
+def whole(q, k, v, do, g, scale):
+    """dq, dk, dv and dg of one sequence of one head from zero states, in 64 bits, from
+    o_i = scale sum_{j <= i} exp(g_{j+1} + .. + g_i) (q_i.k_j) v_j as it stands:
+    dg_t is the sum of X_ij = G_ij (q_i.k_j) (do_i.v_j) over i >= t > j."""
+    q, k, v, do, g = (x.double() for x in (q, k, v, do, g))
+    c = torch.cumsum(g, 0)
+    n = len(c)
+    low = torch.ones((n, n), dtype=torch.bool, device=q.device).tril()
+    G = scale * torch.exp(torch.where(low, c[:, None] - c[None], -torch.inf))
+    A, P = q @ k.T.contiguous(), do @ v.T.contiguous()
+    X = G * A * P
+    before = torch.cumsum(X, 1)  # [i, t - 1]: j < t
+    upto = torch.flip(torch.cumsum(torch.flip(before, (0,)), 0), (0,))  # [t, t' - 1]: i >= t
+    dg = torch.cat([torch.zeros(1, dtype=torch.float64, device=q.device), torch.diagonal(upto, -1)])
+    return (G * P) @ k, (G * P).T.contiguous() @ q, (G * A).T.contiguous() @ do, dg
+
+
+# Sequences of 34 chunks in one segment each: in the middle one the states are held less 2^55
+# from either side, as a decay of 2^-3.3 a chunk makes them.
+@pytest.mark.parametrize("kind", ["mean", "loss scale"])
+@pytest.mark.parametrize("decay", ["token", "head"])
+@pytest.mark.parametrize("d,dtype", [(64, B), (128, B), (64, torch.float32), (128, torch.float32)])
+def test_dg_in_long_segments(d, dtype, decay, kind):
+    h, n_seq, ch = 16, 32, 32 if dtype == torch.float32 else 64
+    length = 34 * ch
+    n = n_seq * length
+    print(f"case linear long segments d={d} {dtype} {decay} {kind}", flush=True)
+    gen = seeded(d + n)
+
+    def tokens(mean, size):
+        x = torch.empty((n, h, d), dtype=dtype, device="cuda")
+        for i in range(h):
+            x[:, i] = ((torch.randn((n, d), generator=gen, device="cuda") + mean) * size).to(dtype)
+        return x
+
+    if kind == "mean":
+        q, k, v, do = tokens(1.0, 1.0), tokens(1.0, 1.0), tokens(1.0, 8.0), tokens(1.0, 8.0)
+    else:
+        q, k, v, do = tokens(0.0, 1.0), tokens(0.0, 1.0), tokens(0.0, 1.0), tokens(0.0, 65536.0)
+    rate = -3.3 * 0.6931471805599453 / ch
+    head = torch.full((h,), rate, device="cuda")
+    head[1::2] *= 1.02
+    g = head if decay == "head" else (head * (0.5 + torch.rand((n, h), generator=gen, device="cuda")))
+    offsets = torch.arange(0, n + 1, length, dtype=torch.int32, device="cuda")
+    got = dict(zip(("dq", "dk", "dv", "dg"), zm.linear_attention_backward(do, q, k, v, g, offsets=offsets)))
+    for i in (0, 9):
+        of_head = 0.0, 0.0
+        for b in (0, 17, 31) if decay == "token" else range(n_seq):
+            at = slice(b * length, (b + 1) * length)
+            x = [t[at, i] for t in (q, k, v, do)]
+            gi = g[at, i] if decay == "token" else g[i].expand(length)
+            want, size = whole(*x, gi, d ** -0.5), whole(*(t.abs() for t in x), gi, d ** -0.5)
+            steps = 2 * chunks(length, dtype) + 2
+            for name, w, s in zip(("dq", "dk", "dv"), want, size):
+                check(name, got[name][at, i], w, s, steps)
+            if decay == "token":
+                check("dg", got["dg"][at, i], want[3], size[3], steps)
+            of_head = of_head[0] + want[3].sum(), of_head[1] + size[3].sum()
+        if decay == "head":
+            check("dg", got["dg"][i], *of_head, steps)
