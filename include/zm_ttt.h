@@ -453,13 +453,17 @@ ZM_API int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const in
 /* Linear attention with decays: the linear fast weight f_S(x) = S x written by adding
  * v_t k_t^T (the delta rule above without taking S k_t off), with a decay to each head:
  *   S_t = a_t S_{t-1} + v_t k_t^T,  a_t = exp(g_t),  o_t = scale S_t q_t.
- * Tokens, heads, offsets and states as for zm_delta_rule.  g (log decay, any value below 60;
- * -inf resets the state) is fp32, token t's of value head h at g[t ld_g + h]: ld_g >= heads, or
- * ld_g = 0 for one decay to each head, the same for every token; NULL: no decay, a = 1.
+ * Tokens, heads, offsets and states as for zm_delta_rule.  g (log decay; -inf resets the state)
+ * is fp32, token t's of value head h at g[t ld_g + h]: ld_g >= heads, or ld_g = 0 for one decay
+ * to each head, the same for every token; NULL: no decay, a = 1.  A decay may be above 0, but no run of a
+ * sequence's tokens may have a sum of g over 40.
  * A token that is not finite can make NaN, in its heads, of the outputs of the 64 tokens
  * (fp32: 32) that it is taken with (counted from its sequence's first) and of later ones and of its
  * sequence's gradients; earlier chunks' outputs and other sequences stay as they are.
- * Values of tokens and states stay below 2^60 in size. */
+ * Products are held beside powers of two of up to 2^60.  So all of these stay below 2^60: values of tokens
+ * and states (those on the way too), |q|.|k|, |S| |q|, and |k| |v| and (|q|.|k|) |v| added up over 64 tokens; in the gradient the same
+ * with d_o and states' gradients in the places of others, and where dg is wanted also (|q|.|k|) (|d_o|.|v|),
+ * (|S| |q|).|d_o| and <|S|, |dS|>.  Tokens up to 2^10 and states up to 2^20 in size do. */
 typedef struct zm_linear_desc {
   int32_t heads;      /* value heads, 1..64, a multiple of heads_k */
   int32_t heads_k;    /* query/key heads */

@@ -8,7 +8,9 @@ import pytest
 import torch
 
 import reconstruction_lact_chunk_amd as zm
-from linear_reference import check, chunks
+import test_linear_attention_gpu as forwards
+import test_linear_backward_gpu as backwards
+from linear_reference import check, chunks, inputs
 
 pytestmark = pytest.mark.gpu
 B = torch.bfloat16
@@ -117,3 +119,36 @@ def test_dg_in_long_segments(d, dtype, decay, kind):
             of_head = of_head[0] + want[3].sum(), of_head[1] + size[3].sum()
         if decay == "head":
             check("dg", got["dg"][i], *of_head, steps)
+
+
+# Values near the largest that the operator takes: 2^11 and states of 2^22, with |q|.|k| up to 2^29, (|q|.|k|)
+# (|do|.|v|) up to 2^58, (|S| |q|).|do| up to 2^57 and <|S|, |dS|> of 2^56, below 2^60 all of them; a decay of 0.63 a token
+# takes the powers beside them to 2^58 within a chunk of 64.
+@pytest.mark.parametrize("decay", [0.63, 0.3, 0.02, 0.0])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [B, torch.float32])
+def test_large_values(dtype, d, decay):
+    n, h, size = 200, 2, 2.0 ** (11 if d == 64 else 10.5)
+    print(f"case linear large values d={d} {dtype} decay {decay}", flush=True)
+    x = inputs(n, h, 1, d, dtype, 3, decay=decay)
+    for name in "qkv":
+        x[name] = (x[name].float() * size).to(dtype)
+    x["g"] = torch.full_like(x["g"], -decay)
+    x["state"] *= size * size
+    do, dstate = backwards.grads_in(x, 4)
+    do, dstate = (do.float() * size).to(dtype), dstate * (size * size)
+    forwards.compare(x, forwards.run(x))
+    backwards.compare(backwards.run(do, dstate, x), do, dstate, x)
+
+
+@pytest.mark.parametrize("dtype", [B, torch.float32])
+def test_growing_states(dtype):
+    """77 tokens of a = exp(0.5), 2^55 in all, down again and up once more."""
+    n = 240
+    x = inputs(n, 2, 2, 64, dtype, 5)
+    x["g"][:] = -0.5
+    x["g"][20:97] = 0.5
+    x["g"][180:] = 0.5
+    do, dstate = backwards.grads_in(x, 6)
+    forwards.compare(x, forwards.run(x))
+    backwards.compare(backwards.run(do, dstate, x), do, dstate, x)
