@@ -1125,10 +1125,16 @@ def norm_rotary_backward(dq_out, dk_out, q, k, pos, freqs, sections, q_gamma=Non
     return out
 
 
+def _places(tensors):
+    return list(map(torch.Tensor.data_ptr, tensors)), list(map(torch.Tensor.numel, tensors))
+
+
 class TensorList:
     """Gradients (contiguous bf16 or fp32 tensors of one GPU) laid out once for grad_norm and
-    clip_grads; out: where the clipped ones go (None: in place).  It keeps the tensors alive, and
-    they keep their memory: one whose storage is exchanged needs a new list."""
+    clip_grads; out: where the clipped ones go (None: in place).  It is of these tensors: a call
+    refuses one that has since moved or changed its size (x.data = y, set_, resize_), and a
+    gradient that is another tensor than before, as after zero_grad(set_to_none=True), torch's
+    default, needs a new list (with set_to_none=False the same ones stay)."""
 
     def __init__(self, tensors, out=None):
         self.tensors = list(tensors)
@@ -1145,6 +1151,13 @@ class TensorList:
             self.array[i] = Tensor(x.data_ptr(), y.data_ptr(), x.numel(), _IO[x.dtype], 0)
         if self.tensors:
             _same_gpu(*self.tensors, *(() if out is None else self.out))
+        self._laid_out = _places(self.tensors), None if out is None else _places(self.out)
+
+    def check(self):
+        """ZmError unless every tensor lies where it did when the list was built."""
+        at, out_at = self._laid_out
+        if _places(self.tensors) != at or (out_at and _places(self.out) != out_at):
+            raise ZmError("a tensor of the list has moved or changed its size: build a new TensorList")
 
     def __len__(self):
         return len(self.tensors)
@@ -1177,7 +1190,10 @@ def _norm_call(tensors, norm, workspace):
 def grad_norm(tensors, norm=None, workspace=None):
     """The root of the sum of all squares of a list of tensors (or a TensorList), summed in
     64 bits; returns norm, fp32 of one element."""
-    tensors = tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+    if isinstance(tensors, TensorList):
+        tensors.check()
+    else:
+        tensors = TensorList(tensors)
     norm, ws = _norm_call(tensors, norm, workspace)
     _run("zm_grad_norm", norm.device, tensors.array, len(tensors), _ptr(norm), _ptr(ws),
          _ws_bytes(ws))
@@ -1191,6 +1207,7 @@ def clip_grads(tensors, max_norm, out=None, norm=None, workspace=None):
     if isinstance(tensors, TensorList):
         if out is not None:
             raise ZmError("a TensorList has its outputs: pass out to it")
+        tensors.check()
     else:
         tensors = TensorList(tensors, out)
     norm, ws = _norm_call(tensors, norm, workspace)
