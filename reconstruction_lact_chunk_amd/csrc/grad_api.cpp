@@ -14,7 +14,9 @@ using namespace zm;
 namespace {
 
 constexpr int kMaxTensors = 8192;
-constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of one tensor: a table's pieces stay under 2^30
+constexpr int64_t kMaxElements = (int64_t)1 << 36;  // of one tensor
+static_assert(kClipTensors * clip_pieces(kMaxElements, true) + kClipBlocks < (int64_t)1 << 32,
+              "pieces of a table and the kernels' steps over them are counted in 32 bits without a sign");
 
 struct Span {
   uintptr_t at, end;
@@ -76,12 +78,12 @@ struct Tables {
       out.x[m] = t[from].x;
       out.y[m] = t[from].y;
       out.n[m] = t[from].n;
-      out.first[m] = (int32_t)pieces;
+      out.first[m] = (uint32_t)pieces;
       if (f32) out.f32[m >> 5] |= 1u << (m & 31);
       pieces += clip_pieces(t[from].n, f32);
       ++m;
     }
-    out.first[m] = (int32_t)pieces;
+    out.first[m] = (uint32_t)pieces;
     out.count = m;
     return from;
   }

@@ -15,11 +15,11 @@ struct ClipTable {
   const void* x[kClipTensors];
   void* y[kClipTensors];
   int64_t n[kClipTensors];
-  int32_t first[kClipTensors + 1];  // pieces before a tensor's; the last: all
+  uint32_t first[kClipTensors + 1];  // pieces before a tensor's; the last: all
   uint32_t f32[kClipTensors / 32];
   int32_t count;
 };
-inline int64_t clip_pieces(int64_t n, bool f32) {
+constexpr int64_t clip_pieces(int64_t n, bool f32) {
   // from the 16-byte word of the first element on
   return n > 0 ? (n * (f32 ? 4 : 2) + 14) / kClipPieceBytes + 1 : 0;
 }

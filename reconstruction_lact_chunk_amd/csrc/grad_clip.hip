@@ -20,14 +20,14 @@ constexpr int kWords = kClipPieceBytes / 16;     // 16-byte words of a piece
 constexpr int kEach = kWords / kThreads;         // of a thread
 
 // Piece p of the table: tensor i and the piece's number in it.
-__device__ __forceinline__ int find_piece(const ClipTable& t, int p, int& in) {
+__device__ __forceinline__ int find_piece(const ClipTable& t, unsigned p, int& in) {
   int lo = 0, hi = t.count;  // the last tensor whose first piece is at most p (empty ones share theirs)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (t.first[mid] <= p) lo = mid;
     else hi = mid;
   }
-  in = p - t.first[lo];
+  in = (int)(p - t.first[lo]);
   return lo;
 }
 
@@ -121,8 +121,8 @@ __device__ __forceinline__ double piece_squares(const void* p, int64_t n, int pi
 __global__ __launch_bounds__(kThreads) void k_grad_squares(ClipTable t, double* part) {
   __shared__ double red[4];
   double s = 0.0;
-  const int pieces = t.first[t.count];
-  for (int p = blockIdx.x; p < pieces; p += gridDim.x) {
+  const unsigned pieces = t.first[t.count];
+  for (unsigned p = blockIdx.x; p < pieces; p += gridDim.x) {
     int in;
     const int i = find_piece(t, p, in);
     if (t.f32[i >> 5] >> (i & 31) & 1) s += piece_squares<float>(t.x[i], t.n[i], in);
@@ -186,11 +186,11 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(ClipTable t, const doub
   const double s = sqrt(all_squares(part, count, red));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)s;
   const double ratio = (double)max_norm / (s + 1e-6), c = ratio < 1.0 || ratio != ratio ? ratio : 1.0;
-  const int pieces = t.first[t.count];
+  const unsigned pieces = t.first[t.count];
   // the last pieces first: they are what the caches still hold of the norm's pass
-  for (int p = pieces - 1 - (int)blockIdx.x; p >= 0; p -= gridDim.x) {
+  for (unsigned behind = blockIdx.x; behind < pieces; behind += gridDim.x) {
     int in;
-    const int i = find_piece(t, p, in);
+    const int i = find_piece(t, pieces - 1 - behind, in);
     if (c == 1.0 && t.x[i] == t.y[i]) continue;  // the same values
     if (t.f32[i >> 5] >> (i & 31) & 1) piece_scale<float>(t.x[i], t.y[i], t.n[i], in, c);
     else piece_scale<uint16_t>(t.x[i], t.y[i], t.n[i], in, c);
