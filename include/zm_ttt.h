@@ -498,10 +498,12 @@ ZM_API int zm_linear_attention(const zm_linear_desc* desc, int64_t n, const int3
 ZM_API int zm_linear_attention_step(const zm_linear_desc* desc, const void* q, const void* k, const void* v,
                        const float* g, float* state, void* o, void* stream);
 
-/* Bytes of workspace of zm_linear_attention_backward (never less for more tokens): to each 64
- * tokens (fp32: 32; or begun ones of a sequence) of a value head a state, the forward's twice, and
- * with shared key heads two fp32 copies of the value heads' tokens. */
+/* Bytes of workspace of zm_linear_attention_backward (never less for more tokens): the forward's
+ * twice, with shared key heads two fp32 copies of the value heads' tokens, and for dg to each 64
+ * tokens (fp32: 32; or begun ones of a sequence) of a value head a state.  The second: of calls
+ * whose dg is NULL. */
 ZM_API int zm_linear_attention_backward_workspace_size(const zm_linear_desc* desc, int64_t n, size_t* bytes);
+ZM_API int zm_linear_attention_backward_workspace_size_no_dg(const zm_linear_desc* desc, int64_t n, size_t* bytes);
 
 /* The gradient of zm_linear_attention from its inputs alone: d_o [n, heads, d_head] (stride
  * desc->ld_o) and dstate_out (gradient of the last states, NULL: zeros) give dq, dk [n, heads_k,

@@ -35,7 +35,8 @@ EXPORTED = (
     "zm_rotary", "zm_delta_rule_workspace_size", "zm_delta_rule", "zm_delta_rule_step",
     "zm_delta_rule_backward_workspace_size", "zm_delta_rule_backward",
     "zm_linear_attention_workspace_size", "zm_linear_attention", "zm_linear_attention_step",
-    "zm_linear_attention_backward_workspace_size", "zm_linear_attention_backward",
+    "zm_linear_attention_backward_workspace_size",
+    "zm_linear_attention_backward_workspace_size_no_dg", "zm_linear_attention_backward",
     "zm_norm_rotary", "zm_norm_rotary_backward_workspace_size", "zm_norm_rotary_backward",
     "zm_grad_norm_workspace_size", "zm_grad_norm", "zm_clip_grads",
 )
@@ -205,6 +206,8 @@ def load_library(path: str | None = None):
     lib.zm_linear_attention.argtypes = [_AD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
     lib.zm_linear_attention_step.argtypes = [_AD, _P, _P, _P, _P, _P, _P, _P]
     lib.zm_linear_attention_backward_workspace_size.argtypes = [_AD, _I64, ctypes.POINTER(_SZ)]
+    lib.zm_linear_attention_backward_workspace_size_no_dg.argtypes = [_AD, _I64,
+                                                                      ctypes.POINTER(_SZ)]
     lib.zm_linear_attention_backward.argtypes = [_AD, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                                  _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]
     _RN = ctypes.POINTER(NormRotaryDesc)
@@ -221,7 +224,8 @@ def load_library(path: str | None = None):
                  "zm_delta_rule", "zm_delta_rule_step", "zm_delta_rule_backward_workspace_size",
                  "zm_delta_rule_backward", "zm_linear_attention_workspace_size",
                  "zm_linear_attention", "zm_linear_attention_step",
-                 "zm_linear_attention_backward_workspace_size", "zm_linear_attention_backward",
+                 "zm_linear_attention_backward_workspace_size",
+                 "zm_linear_attention_backward_workspace_size_no_dg", "zm_linear_attention_backward",
                  "zm_norm_rotary", "zm_norm_rotary_backward_workspace_size",
                  "zm_norm_rotary_backward", "zm_grad_norm_workspace_size", "zm_grad_norm",
                  "zm_clip_grads"):
@@ -994,11 +998,11 @@ def linear_attention_step(q, k, v, g, state, scale=None, out=None):
     return o
 
 
-def linear_attention_backward_workspace_size(desc: LinearDesc, n: int) -> int:
+def linear_attention_backward_workspace_size(desc: LinearDesc, n: int, dg: bool = True) -> int:
+    """dg: whether the call wants it."""
+    name = "zm_linear_attention_backward_workspace_size" + ("" if dg else "_no_dg")
     out = ctypes.c_size_t(0)
-    _check(load_library().zm_linear_attention_backward_workspace_size(
-        ctypes.byref(desc), int(n), ctypes.byref(out)),
-        "zm_linear_attention_backward_workspace_size")
+    _check(getattr(load_library(), name)(ctypes.byref(desc), int(n), ctypes.byref(out)), name)
     return int(out.value)
 
 
@@ -1033,9 +1037,10 @@ def linear_attention_backward(do, q, k, v, g=None, state=None, dstate=None, offs
         raise ZmError(f"dg must be contiguous fp32 {list(g.shape)}")
     _delta_state("the first states' gradient", dstart, desc)
     _same_gpu(q, do, k, v, g, state, dstate, offsets, *out, workspace)
-    need = linear_attention_backward_workspace_size(desc, n)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None \
-        else workspace
+    ws = workspace
+    if ws is None:
+        need = linear_attention_backward_workspace_size(desc, n, dg is not None)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _run("zm_linear_attention_backward", q.device, ctypes.byref(desc), n, _ptr(offsets),
          _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(dstate), _ptr(dq),
          lds[0], _ptr(dk), lds[1], _ptr(dv), lds[2], _ptr(dg), _ptr(dstart), _ptr(ws),

@@ -133,19 +133,22 @@ size_t forward_ws(LinArgs& a, const zm_linear_desc* d, const LinPlan& p, int64_t
   return c.at;
 }
 
+// What dg alone needs comes last.
 size_t backward_ws(LinArgs& a, const zm_linear_desc* d, const LinPlan& p, int64_t n, const int* offsets, void* ws,
-                   float** sums) {
+                   bool dg, float** sums) {
   Carve c{(char*)ws};
   common_ws(a, c, d, p, n, offsets, 2);
   const size_t dd = (size_t)d->d_head * d->d_head, rows = (size_t)n * d->heads * d->d_head;
-  a.flow = c.take<float>((size_t)n * d->heads);
-  a.d_dump = c.take<float>((size_t)p.n_chunks * d->heads * dd);
-  a.d_exp = c.take<double>((size_t)p.n_chunks * d->heads);
-  *sums = d->ld_g == 0 ? c.take<float>((size_t)p.n_chunks * d->heads) : nullptr;
   if (d->heads != d->heads_k) {
     a.o_part = c.take<float>(rows);
     a.dk_part = c.take<float>(rows);
   }
+  *sums = nullptr;
+  if (!dg) return c.at;
+  a.flow = c.take<float>((size_t)n * d->heads);
+  a.d_dump = c.take<float>((size_t)p.n_chunks * d->heads * dd);
+  a.d_exp = c.take<double>((size_t)p.n_chunks * d->heads);
+  if (d->ld_g == 0) *sums = c.take<float>((size_t)p.n_chunks * d->heads);
   return c.at;
 }
 
@@ -174,6 +177,16 @@ int check_apart(const void* out, std::initializer_list<const void*> others) {
   if (out)
     for (const void* p : others)
       if (p == out) return ZM_ERR_INVALID_ARG;
+  return ZM_OK;
+}
+
+int backward_size(const zm_linear_desc* d, int64_t n, bool dg, size_t* bytes) {
+  if (!bytes) return ZM_ERR_INVALID_ARG;
+  ZM_TRY(check_desc(d));
+  ZM_TRY(check_counts(d, n));
+  LinArgs a{};
+  float* sums;
+  *bytes = backward_ws(a, d, lin_plan(d, n), n, nullptr, nullptr, dg, &sums);
   return ZM_OK;
 }
 
@@ -260,13 +273,11 @@ int zm_linear_attention_step(const zm_linear_desc* desc, const void* q, const vo
 }
 
 int zm_linear_attention_backward_workspace_size(const zm_linear_desc* desc, int64_t n, size_t* bytes) {
-  if (!bytes) return ZM_ERR_INVALID_ARG;
-  ZM_TRY(check_desc(desc));
-  ZM_TRY(check_counts(desc, n));
-  LinArgs a{};
-  float* sums;
-  *bytes = backward_ws(a, desc, lin_plan(desc, n), n, nullptr, nullptr, &sums);
-  return ZM_OK;
+  return backward_size(desc, n, true, bytes);
+}
+
+int zm_linear_attention_backward_workspace_size_no_dg(const zm_linear_desc* desc, int64_t n, size_t* bytes) {
+  return backward_size(desc, n, false, bytes);
 }
 
 int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const int32_t* offsets, const void* d_o,
@@ -298,7 +309,8 @@ int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const in
   const LinPlan p = lin_plan(desc, n);
   LinArgs a{};
   float* sums;
-  ZM_TRY(check_workspace(workspace, workspace_bytes, backward_ws(a, desc, p, n, offsets, workspace, &sums)));
+  const size_t need = backward_ws(a, desc, p, n, offsets, workspace, dg != nullptr, &sums);
+  ZM_TRY(check_workspace(workspace, workspace_bytes, need));
   const hipStream_t st = (hipStream_t)stream;
   const bool f32 = desc->io_dtype == ZM_F32;
   const int d = desc->d_head;
@@ -318,7 +330,6 @@ int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, const in
     a.dv = dv;
     a.ld_dv = ld_dv;
     a.dg = one ? sums : dg;
-    if (!dg) a.flow = nullptr;
     if (a.sq.segs) ZM_HIP(launch_linear_table(a.sq, st));
     if (p.split || a.flow) ZM_HIP(launch_linear_grad_states(a, d, f32, st));
     if (p.split) ZM_HIP(launch_linear_join(a, d, true, st));

@@ -20,7 +20,7 @@
 // (scale with one of the two powers): the same numbers up to the powers, which come from 64-bit exponents
 // (exp2_wide), while |e| stays under kLinSpan.  A chunk that would leave that range
 // takes 2^s into M^ first; one whose own decays do (a reset) is formed with them in place.
-// So the gradients need no state of any chunk in memory.  Few long sequences are cut into
+// So only dg needs states of the chunks in memory (D^T, d_dump below).  Few long sequences are cut into
 // segments: a first pass leaves what each adds to the state, a join makes the states at
 // their starts (or ends) of these.
 //
@@ -137,7 +137,7 @@ struct LinArgs {
   int64_t ld_dv;
   float* o_part;       // dq and dk to each value head [n][heads][d], where these share key heads
   float* dk_part;
-  float* flow;         // [n][heads]: the parts of dg that the first two passes form, or null without g
+  float* flow;         // [n][heads]: the parts of dg that the first two passes form, or null without dg
   float* d_dump;       // D^T at every chunk's end, less a power of two
   double* d_exp;       // [chunks][heads] that power
   float* dg;           // [n][heads], or, with ld_g = 0, the chunks' sums [chunks][heads]
