@@ -60,7 +60,10 @@ LinPlan lin_plan(const zm_linear_desc* d, int64_t n) {
   // segments of two 36; 10000 of 2 heads 55 and 43; 1374 of 8 heads 31 and 34.
   const int64_t each = d->n_seq > 0 ? p.n_chunks / d->n_seq : 0;
   if (seg < 2 && each > 32) seg = 2;
-  if (seg < each / 128) seg = each / 128;
+  // The same of two in longer ones of one head: 33,000 tokens (516 chunks) 68 us, of three 58, their
+  // gradient 137 and 114; 20,000 (313) 50 either way, 90 and 95.  No more than that where 512 workgroups take
+  // fewer: 137,400 of one head in segments of 5 chunks 123 us, of 16 143.
+  if (seg < 3 && each > 400) seg = 3;
   // Two chunks one after the other take less than two launches more: 128 tokens 18 us against
   // 24, 256 tokens 27 against 24.
   if (n <= 2 * p.chunk) seg = p.n_chunks;
