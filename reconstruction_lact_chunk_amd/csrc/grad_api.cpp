@@ -5,6 +5,8 @@
 #include <math.h>
 
 #include <algorithm>
+#include <memory>
+#include <new>
 
 #include "api_util.h"
 #include "grad_clip.h"
@@ -49,8 +51,20 @@ int check_tensors(const zm_tensor* t, int32_t count, bool write) {
 }
 
 // What is written must not overlap another tensor, read or written, but its own input exactly.
+// Up to kFewSpans lie on the stack (16 KB), more on the heap: the caller's stack may be small.
+constexpr int kFewSpans = 1024;
 int check_written(const zm_tensor* t, int32_t count, const float* norm, const void* ws, size_t bytes) {
-  Span s[2 * kMaxTensors + 2];  // 256 KB of the stack
+  Span few[kFewSpans];
+  std::unique_ptr<Span[]> many;
+  Span* s = few;
+  if (2 * (int64_t)count + 2 > kFewSpans) {
+    many.reset(new (std::nothrow) Span[2 * (size_t)count + 2]);
+    if (!many) {
+      set_last_error("no host memory for the spans of %d tensors", (int)count);
+      return ZM_ERR_HIP;
+    }
+    s = many.get();
+  }
   int m = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].n == 0) continue;
