@@ -522,9 +522,9 @@ ZM_API int zm_linear_attention_backward(const zm_linear_desc* desc, int64_t n, c
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients' global norm and clipping: N = sqrt(sum of x^2 over all elements of all
- * tensors), y = x min(1, max_norm / (N + 1e-6)).  Sums are in 64 bits, so N is finite
- * for finite fp32 elements up to its own range.  An N that is infinite makes y 0 (NaN where x is
- * infinite), one that is NaN makes every y NaN. */
+ * tensors), y = x min(1, max_norm / (N + 1e-6)).  Sums are in 64 bits, where N is finite for finite
+ * elements: past fp32's range norm receives infinity, and y is formed with N all the same.  Infinite
+ * elements make y 0 (NaN where x is infinite), NaN ones make every y NaN. */
 typedef struct zm_tensor {
   const void* x;      /* n elements one after the other, aligned to one */
   void* y;            /* where the clipped ones go: x itself, or an array of its own */
@@ -537,7 +537,8 @@ typedef struct zm_tensor {
 ZM_API int zm_grad_norm_workspace_size(int32_t count, size_t* bytes);
 
 /* norm (device, fp32): N.  tensors is host memory that is read during the call alone; the ys
- * are not looked at.  Bitwise reproducible, as the next. */
+ * are not looked at.  The workspace must not overlap a tensor; tensors may overlap each
+ * other.  Bitwise reproducible, as the next. */
 ZM_API int zm_grad_norm(const zm_tensor* tensors, int32_t count, float* norm,
               void* workspace, size_t workspace_bytes, void* stream);
 

@@ -77,6 +77,17 @@ int check_written(const zm_tensor* t, int32_t count, const float* norm, const vo
   return overlapping(s, m) ? ZM_ERR_INVALID_ARG : ZM_OK;
 }
 
+// The partial sums must not be written into a tensor that is still read.
+int check_read(const zm_tensor* t, int32_t count, const void* ws, size_t bytes) {
+  const uintptr_t at = (uintptr_t)ws;
+  for (int32_t i = 0; i < count; ++i) {
+    const uintptr_t x = (uintptr_t)t[i].x;
+    const size_t size = (size_t)t[i].n * (t[i].dtype == ZM_F32 ? 4 : 2);
+    if (t[i].n > 0 && x < at + bytes && at < x + size) return ZM_ERR_INVALID_ARG;
+  }
+  return ZM_OK;
+}
+
 // Tables of up to kClipTensors tensors (empty ones left out), one after the other.
 struct Tables {
   const zm_tensor* t;
@@ -143,6 +154,7 @@ int zm_grad_norm(const zm_tensor* tensors, int32_t count, float* norm, void* wor
   ZM_TRY(check_tensors(tensors, count, false));
   if (!norm || !aligned(norm, 4)) return ZM_ERR_INVALID_ARG;
   ZM_TRY(check_workspace(workspace, workspace_bytes, clip_bytes(count)));
+  ZM_TRY(check_read(tensors, count, workspace, clip_bytes(count)));
   const hipStream_t st = (hipStream_t)stream;
   int slots;
   ZM_HIP(squares(Tables{tensors, count}, (double*)workspace, slots, st));

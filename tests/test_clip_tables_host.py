@@ -47,7 +47,7 @@ int main() {
       std::vector<zm_tensor> t;
       for (int i = 0; i < count; ++i) t.push_back(zm_tensor{(void*)0x1000, nullptr, n, n >> 36 || i % 9 ? ZM_F32 : ZM_BF16, 0});
       zm::tensors = zm::blocks = zm::want = 0;
-      const int s = zm_grad_norm(t.data(), count, (float*)0x2000, (void*)0x10000, (size_t)1 << 40, nullptr);
+      const int s = zm_grad_norm(t.data(), count, (float*)0x2000, (void*)((size_t)1 << 50), (size_t)1 << 40, nullptr);
       size_t need;
       zm_grad_norm_workspace_size(count, &need);
       if (s != ZM_OK || zm::bad || zm::tensors != count || (size_t)zm::blocks * 8 > need) {
