@@ -463,7 +463,8 @@ ZM_API int zm_delta_rule_backward(const zm_delta_desc* desc, int64_t n, const in
  * Products are held beside powers of two of up to 2^60.  So all of these stay below 2^60: values of tokens
  * and states (those on the way too), |q|.|k|, |S| |q|, and |k| |v| and (|q|.|k|) |v| added up over 64 tokens; in the gradient the same
  * with d_o and states' gradients in the places of others, and where dg is wanted also (|q|.|k|) (|d_o|.|v|),
- * (|S| |q|).|d_o| and <|S|, |dS|>.  Tokens up to 2^10 and states up to 2^20 in size do. */
+ * (|S| |q|).|d_o| and <|S|, |dS|>, each times |scale| where that is over 1.  Tokens up to 2^10 and states up
+ * to 2^20 in size do with a scale of at most 1. */
 typedef struct zm_linear_desc {
   int32_t heads;      /* value heads, 1..64, a multiple of heads_k */
   int32_t heads_k;    /* query/key heads */

@@ -53,19 +53,19 @@ LinPlan lin_plan(const zm_linear_desc* d, int64_t n) {
   const int64_t ragged = (int64_t)(p.chunk - 1) * d->n_seq;
   p.n_chunks = (n + ragged) / p.chunk;
   // About this many workgroups in all, two to a compute unit.  8 heads of 128, bf16, us at
-  // 256 / 512 / 1024: 10992 tokens 71 / 69 / 83, 40000 tokens 194 / 162 / 190.
+  // 256 / 512 / 1024: 10992 tokens 69 / 67 / 80, 40000 tokens 187 / 156 / 183.
   const int64_t target = 2 * kTargetWgs;
   int64_t seg = ceil_div(p.n_chunks * d->heads, target);
   // Segments of one chunk make the join long: 3000 tokens (47 chunks) of 8 heads 42 us, in
-  // segments of two 36; 10000 of 2 heads 55 and 43; 1374 of 8 heads 31 and 34.
+  // segments of two 35; 10000 of 2 heads 54 and 42; of fewer chunks one is better: 1374 tokens of 8 heads 31 and 34.
   const int64_t each = d->n_seq > 0 ? p.n_chunks / d->n_seq : 0;
   if (seg < 2 && each > 32) seg = 2;
   // The same of two in longer ones of one head: 33,000 tokens (516 chunks) 68 us, of three 58, their
   // gradient 137 and 114; 20,000 (313) 50 either way, 90 and 95.  No more than that where 512 workgroups take
   // fewer: 137,400 of one head in segments of 5 chunks 123 us, of 16 143.
   if (seg < 3 && each > 400) seg = 3;
-  // Two chunks one after the other take less than two launches more: 128 tokens 18 us against
-  // 24, 256 tokens 27 against 24.
+  // Two chunks one after the other take less than two launches more: 128 tokens 17 us against
+  // 21, 256 tokens (four chunks) 27 against 22.
   if (n <= 2 * p.chunk) seg = p.n_chunks;
   if (seg < 1) seg = 1;
   p.seg_chunks = (int)seg;
@@ -110,7 +110,7 @@ void common_ws(LinArgs& a, Carve& c, const zm_linear_desc* d, const LinPlan& p, 
   s.n_segs = p.n_segs;
   s.n_slots = p.n_slots;
   s.n_split = p.n_split;
-  // 61 sequences of 4 to 24 chunks, 16 heads: 353 -> 291 us
+  // 70 sequences of 4 to 24 chunks, 16 heads: 303 us, in the order of the tokens 318
   s.longest_first = (int64_t)p.n_segs * d->heads > 2 * kTargetWgs && p.n_segs <= kLinSorted;
   s.seg_tokens = p.seg_chunks * p.chunk;
   s.chunk = p.chunk;

@@ -9,8 +9,8 @@
 // head's row lies in the registers of a power of two of lanes and its sums take
 // few exchanges; the angles of a lane's pairs are formed once for all heads of a token.
 // 54,960 fp32 tokens of 20 heads of 64: 139 us, 4.1 TB/s; gradient of 137,400 bf16 tokens of 16 heads
-// of 128: 338 us, 5.0 TB/s; one frame of 1374 tokens 7.7 us, loads, angles and exchanges one after the
-// other.  Stores past the caches gave 3 to 5% for 8 + 8 heads and whole rotations (that gradient 328 us) and
+// of 128: 338 us, 5.0 TB/s; one frame of 1374 tokens 8 us from the caches and 9 from memory, loads, angles and
+// exchanges one after the other.  Stores past the caches gave 3 to 5% for 8 + 8 heads and whole rotations (that gradient 328 us) and
 // cost 3 to 30% for other heads and sections (those fp32 tokens 151 us): not taken.
 #include "rotary_dev.h"
 
@@ -333,8 +333,8 @@ hipError_t forward_launch(const NormRotaryArgs& a, hipStream_t st) {
   Plan pl = plan_of<V>(a.r);
   const int all = a.r.q.heads + a.r.k.heads;
   // Threads for four waves on each SIMD, as far as the heads can be split: a thread with
-  // many heads forms its angles once, one with few starts sooner (one frame: 6.3 us, for eight
-  // waves 8.0, for one 7.0).
+  // many heads forms its angles once, one with few starts sooner (one frame from memory: 8.9 us, for eight
+  // waves 10.1, for two 8.7, for one 10.0).
   const int64_t want = (int64_t)kTargetWgs * 4 * 4 * 64;
   int64_t splits = ceil_div(want, a.r.n * pl.lanes);
   if (splits > all) splits = all;
@@ -367,7 +367,8 @@ hipError_t backward_launch(const NormRotaryArgs& a, hipStream_t st) {
 
 // Runs of 4 pairs where they fit, else of one: a lane then has one group, or two where a
 // head has more than 64 pairs.  Runs of 8 (bf16, 8 + 8 heads of 128, us against runs of 4): one
-// frame 7.5 and 6.3, 100 frames 214 and 211, their gradients 29 and 17, 330 and 326.
+// frame 10.2 and 8.9, 100 frames 213 and 211, gradients of one frame 30 and 17, of 8 frames 63 and 51, of 100
+// frames 323 and 316.
 #define ZM_NORM_ROTARY(F, T)                                                                           \
   do {                                                                                                 \
     const bool adj = a.r.layout == 1;                                                                  \
