@@ -228,11 +228,12 @@ __global__ __launch_bounds__(64) void k_linear_join(LinArgs a, int dd, int ways)
 // cycles over 4 SIMDs (1.6 us), 5600 vector instructions (most of them the cutting of state and
 // w o C into bf16 parts, 2.3 us) and 0.51 MB of LDS reads (1.7 us); 5.2 us a chunk and compute unit
 // in all, since the phases between barriers bring the three one after the other.  137,400 tokens
-// of 8 heads 346 us, 54,321 of 16 heads 302 us (2.2 TB/s) in a kernel trace, which clocks lower than calls alone
-// (480 and 292 us with the passes before); of 342 without loads 262, without products 215.  Two parts of the state and of T save 0.3 us of matrix work and 0.3 of vector work (a tenth of
-// the kernel) and lose what terms that cancel leave.  Four waves of 32 columns (half of the LDS reads, 256
-// registers) and tiles read ahead into registers gave nothing; stores past the caches, which help
-// elsewhere, cost 11%, as q, k and v are all that the caches could keep.
+// of 8 heads 346 us, 54,321 of 16 heads 302 us (2.2 TB/s) in a kernel trace, which clocks lower
+// than calls alone (480 and 292 us with the passes before); of 342 without loads 262, without
+// products 215.  Two parts of the state and of T save 0.3 us of matrix work and 0.3 of vector work (a
+// tenth of the kernel) and lose what terms that cancel leave.  Four waves of 32 columns (half of the
+// LDS reads, 256 registers) and tiles read ahead into registers gave nothing; stores past the
+// caches, which help elsewhere, cost 11%, as q, k and v are all that the caches could keep.
 template <int D, bool F32>
 __global__ __launch_bounds__(4 * D, F32 ? 2 : D == 64 ? 3 : 4) void k_linear_out(LinArgs a) {
   using C = LinCfg<D, F32>;

@@ -9,9 +9,10 @@
 // head's row lies in the registers of a power of two of lanes and its sums take
 // few exchanges; the angles of a lane's pairs are formed once for all heads of a token.
 // 54,960 fp32 tokens of 20 heads of 64: 139 us, 4.1 TB/s; gradient of 137,400 bf16 tokens of 16 heads
-// of 128: 338 us, 5.0 TB/s; one frame of 1374 tokens 8 us from the caches and 9 from memory, loads, angles and
-// exchanges one after the other.  Stores past the caches gave 3 to 5% for 8 + 8 heads and whole rotations (that gradient 328 us) and
-// cost 3 to 30% for other heads and sections (those fp32 tokens 151 us): not taken.
+// of 128: 338 us, 5.0 TB/s; one frame of 1374 tokens 8 us from the caches and 9 from memory, loads,
+// angles and exchanges one after the other.  Stores past the caches gave 3 to 5% for 8 + 8 heads and
+// whole rotations (that gradient 328 us) and cost 3 to 30% for other heads and sections (those fp32
+// tokens 151 us): not taken.
 #include "rotary_dev.h"
 
 namespace zm {
